@@ -114,7 +114,9 @@ enum {
     SEER_CALL_DECODE_GATE_SCORES = 3,
     SEER_CALL_BLOCK_SPARSE_DECODE = 4,
     SEER_CALL_GATE_KEY_CACHE = 5,
-    SEER_CALL_DECODE_GATE_CACHED = 6
+    SEER_CALL_DECODE_GATE_CACHED = 6,
+    SEER_CALL_GATE_KEY_CACHE_QUANT = 8,
+    SEER_CALL_BLOCK_SPARSE_DECODE_QUANT = 9
 };
 
 /*
@@ -329,6 +331,110 @@ SEER_API seer_status seer_decode_block_mask(const seer_shape *shape, const float
 SEER_API seer_status seer_block_sparse_decode(const seer_shape *shape, const void *q_tok, const void *k,
                                               const void *v, const uint8_t *mask, float softmax_scale, void *o,
                                               float *lse, void *workspace, size_t ws_bytes, void *stream);
+
+/*
+ * The quantised KV cache: K and V of the decode step in 4 or 8 bits, in pages
+ * of one key block (64 tokens) so that sequences of different lengths share a
+ * pool.  (The pages about SeerAttention keep a bf16 cache; this is a
+ * deployment form of the same decode step.)
+ *
+ * A token's row of one head is cut into groups of G elements, G = 32 at 4 bits
+ * and 64 at 8.  A group x is stored as
+ *   z = min(x),  s = bf16((max(x) - min(x)) / (2^bits - 1)),
+ *   n = nearest integer to (x - z) / s, ties to even, at most 2^bits - 1
+ * and stands for z + s n.  s below 2^-100 is stored as 0 (with n = 0); a group
+ * that holds a NaN or a magnitude of 2^126 or more is stored as s = 0, z = NaN
+ * and so reads back as NaN.
+ *
+ * pages: DEVICE [n_pages, Hkv, seer_kv_record_bytes(bits, d)], 16-B aligned; a
+ * record holds a head's K and V of the page's 64 tokens.  block_table: DEVICE
+ * int32 [B, max_blocks], the page of block j of sequence b; NULL means page
+ * b * max_blocks + j (n_pages >= B * max_blocks then).  Sequences may share
+ * pages that only reads reach; two rows of one call written to the same place
+ * leave it undefined.
+ *
+ * The record: two halves of 32 tokens, each [K codes 32 x R | K params
+ * 32 x 4 d/G | V codes | V params], R = d bits / 8.  A param is the pair
+ * (bf16 s, bf16 z) of a group, in group order.  Codes are little-endian, the
+ * lower element in the lower nibble.  With t the token of the half and NG = d/G,
+ * 4 bits: the K word of elements 8c .. 8c+7 is word (c % 4) NG + c / 4 of the
+ * row; the V pair of bytes of elements 32g + 4r .. 32g + 4r + 3 is pair g of
+ * chunk r (of 2 NG bytes each), chunk r at place r ^ (4 if d = 128 and t & 4).
+ * 8 bits: the K word of elements 4c .. 4c+3 is word 16 p + 4 (c % 4) + (c/4) % 4
+ * with p = c / 16, at d = 128 p ^ (t & 1); the V bytes of elements
+ * 64g + 8r .. 64g + 8r + 7 are run g of chunk r (of 8 NG bytes), chunk r at
+ * place r ^ (2 ((t >> 1) & 3) at d = 128, 4 ((t >> 2) & 1) at d = 64).
+ *
+ * The calls below leave out every block whose position lies beyond max_blocks
+ * or whose block_table entry is not in [0, n_pages) — rows are then not
+ * written or read, a key block counts as inactive — and record a device error
+ * that seer_check_status reports as SEER_ERR_DEVICE.
+ */
+typedef struct seer_kv_cache {
+    int bits;                   /* 4 or 8                                           */
+    int n_pages;
+    int max_blocks;             /* blocks a sequence may have, 1 .. 16384           */
+    void *pages;
+    const int32_t *block_table; /* DEVICE or NULL                                   */
+} seer_kv_cache;
+
+/* Rows to quantise: bf16, element (b, h, t, c) at b * stride_b + h * stride_h +
+ * t * stride_t + c.  Pointers 16-B aligned, strides >= 0 and multiples of 8. */
+typedef struct seer_kv_rows {
+    const void *k, *v;
+    long long k_stride_b, k_stride_h, k_stride_t;
+    long long v_stride_b, v_stride_h, v_stride_t;
+} seer_kv_rows;
+
+/* Bytes of a record (one head's 64 tokens), or 0 and the last error for a
+ * width or head dim that is not supported.  Host function. */
+SEER_API size_t seer_kv_record_bytes(int bits, int d);
+
+/*
+ * seer_kv_write — quantise rows into the cache as they are produced: a prompt,
+ * a chunk of one, or a decode step's token.  shape->S = n rows per sequence;
+ * row t of sequence b goes to position start[b] + start_pos + t for
+ * t < min(count[b], n).  start, count: DEVICE int32 [B] or NULL (0, and n).
+ * A decode step that keeps its lengths on the device passes them as start with
+ * start_pos = -1.  Other tokens of the pages are left as they are.
+ */
+SEER_API seer_status seer_kv_write(const seer_shape *shape, const seer_kv_cache *cache, const seer_kv_rows *rows,
+                                   const int32_t *start, const int32_t *count, int start_pos, void *stream);
+
+/*
+ * seer_kv_read — the values the cache holds: row t of sequence b of k and v
+ * (bf16 [B,Hkv,n,d], n = shape->S, 16-B aligned; either may be NULL) is the
+ * cache's position start[b] + start_pos + t for t < min(count[b], n), rounded
+ * once to bf16; rows from count[b] on are left as they are.
+ */
+SEER_API seer_status seer_kv_read(const seer_shape *shape, const seer_kv_cache *cache, const int32_t *start,
+                                  const int32_t *count, int start_pos, void *k, void *v, void *stream);
+
+/*
+ * seer_gate_key_cache_quant — seer_gate_key_cache on the quantised cache: the
+ * gate's key rows of blocks first_block .. nb-1, nb = ceil(shape->S / 64) <=
+ * max_blocks.  lens: DEVICE int32 [B], the tokens of each sequence (clamped to
+ * 0 .. S), or NULL for S; a block pools its tokens below that length, and the
+ * key row of a block without one is 0.  kt, wk, params: as there.  Workspace:
+ * seer_workspace_bytes(SEER_CALL_GATE_KEY_CACHE_QUANT), 256-B aligned.
+ */
+SEER_API seer_status seer_gate_key_cache_quant(const seer_shape *shape, const seer_kv_cache *cache,
+                                               const int32_t *lens, const void *wk, const seer_gate_params *gp,
+                                               int first_block, float *kt, void *workspace, size_t ws_bytes,
+                                               void *stream);
+
+/*
+ * seer_block_sparse_decode_quant — seer_block_sparse_decode on the quantised
+ * cache: tokens below the sequence's length (lens as above) in its active
+ * blocks.  q_tok, mask, softmax_scale, o and lse: as there (o = 0 and
+ * lse = -inf where nothing is active).  The cache's values enter the products
+ * unrounded.  Workspace: seer_workspace_bytes(SEER_CALL_BLOCK_SPARSE_DECODE_QUANT),
+ * 16-B aligned.
+ */
+SEER_API seer_status seer_block_sparse_decode_quant(const seer_shape *shape, const void *q_tok,
+                                                    const seer_kv_cache *cache, const int32_t *lens,
+                                                    const uint8_t *mask, float softmax_scale, void *o, float *lse,
+                                                    void *workspace, size_t ws_bytes, void *stream);
 
 /* Workspace bytes a call needs for `shape` (0 for SEER_CALL_BLOCK_SPARSE_PREFILL).
  * Returns 0 and sets the last error for an invalid shape or call id. */

@@ -20,6 +20,13 @@ from ._binding import (  # noqa: F401
     seer_topk_from_density, seer_version, seer_workspace_bytes, shape_of,
 )
 
+from ._binding import (  # noqa: F401,E402
+    SEER_CALL_BLOCK_SPARSE_DECODE_QUANT, SEER_CALL_GATE_KEY_CACHE_QUANT, seer_kv_cache, seer_kv_rows,
+)
+from .kvcache import (  # noqa: F401,E402
+    SeerKVCache, seer_block_sparse_decode_quant, seer_gate_key_cache_quant, seer_kv_read, seer_kv_record_bytes,
+    seer_kv_write,
+)
 from .pipeline import HostPrefill  # noqa: F401,E402
 
 __version__ = "0.1.0"

@@ -33,6 +33,8 @@ SEER_CALL_DECODE_GATE_SCORES = 3
 SEER_CALL_BLOCK_SPARSE_DECODE = 4
 SEER_CALL_GATE_KEY_CACHE = 5
 SEER_CALL_DECODE_GATE_CACHED = 6
+SEER_CALL_GATE_KEY_CACHE_QUANT = 8
+SEER_CALL_BLOCK_SPARSE_DECODE_QUANT = 9
 
 BLOCK = 64
 
@@ -43,6 +45,8 @@ EXPORTS = (
     "seer_last_error", "seer_version", "seer_gate_scores_noalloc", "seer_distill_loss",
     "seer_decode_gate_scores", "seer_decode_block_mask", "seer_block_sparse_decode",
     "seer_gate_key_cache", "seer_decode_gate_scores_cached", "seer_topk_from_density",
+    "seer_kv_record_bytes", "seer_kv_write", "seer_kv_read", "seer_gate_key_cache_quant",
+    "seer_block_sparse_decode_quant",
 )
 
 
@@ -70,6 +74,16 @@ class seer_mask_params(ctypes.Structure):
     _fields_ = [("mode", ctypes.c_int), ("threshold", ctypes.c_float), ("density", ctypes.c_double),
                 ("k_fixed", ctypes.c_int), ("k_per_row", ctypes.c_void_p), ("force_first", ctypes.c_int),
                 ("force_diag", ctypes.c_int)]
+
+
+class seer_kv_cache(ctypes.Structure):
+    _fields_ = [("bits", ctypes.c_int), ("n_pages", ctypes.c_int), ("max_blocks", ctypes.c_int),
+                ("pages", ctypes.c_void_p), ("block_table", ctypes.c_void_p)]
+
+
+class seer_kv_rows(ctypes.Structure):
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p)] + [
+        (f"{n}_stride_{a}", ctypes.c_longlong) for n in "kv" for a in "bht"]
 
 
 _lock = threading.Lock()
@@ -101,11 +115,19 @@ def lib() -> ctypes.CDLL:
             L.seer_gate_key_cache.argtypes = [SP, P, P, ctypes.POINTER(seer_gate_params), I, P, P, Z, P]
             L.seer_decode_gate_scores_cached.argtypes = [SP, P, P, P, ctypes.POINTER(seer_gate_params), P, P, Z, P]
             L.seer_topk_from_density.argtypes = [ctypes.c_double, I, I, I, ctypes.POINTER(ctypes.c_int32)]
+            CP = ctypes.POINTER(seer_kv_cache)
+            L.seer_kv_write.argtypes = [SP, CP, ctypes.POINTER(seer_kv_rows), P, P, I, P]
+            L.seer_kv_read.argtypes = [SP, CP, P, P, I, P, P, P]
+            L.seer_gate_key_cache_quant.argtypes = [SP, CP, P, P, ctypes.POINTER(seer_gate_params), I, P, P, Z, P]
+            L.seer_block_sparse_decode_quant.argtypes = [SP, P, CP, P, P, F, P, P, P, Z, P]
+            L.seer_kv_record_bytes.argtypes = [I, I]
+            L.seer_kv_record_bytes.restype = Z
             for fn in ("seer_gate_scores", "seer_gate_scores_noalloc", "seer_block_mask", "seer_compact_mask",
                        "seer_block_sparse_prefill", "seer_attn_pooled_map", "seer_check_status",
                        "seer_distill_loss", "seer_decode_gate_scores", "seer_decode_block_mask",
                        "seer_block_sparse_decode", "seer_gate_key_cache", "seer_decode_gate_scores_cached",
-                       "seer_topk_from_density"):
+                       "seer_topk_from_density", "seer_kv_write", "seer_kv_read", "seer_gate_key_cache_quant",
+                       "seer_block_sparse_decode_quant"):
                 getattr(L, fn).restype = I
             L.seer_workspace_bytes.argtypes = [I, SP]
             L.seer_workspace_bytes.restype = Z

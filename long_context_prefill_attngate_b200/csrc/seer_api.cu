@@ -13,6 +13,7 @@
 
 #include "../../include/seer.h"
 #include "seer_internal.h"
+#include "seer_kv.cuh"
 #include "seer_ptx.cuh"
 
 namespace seer {
@@ -224,7 +225,10 @@ size_t seer_workspace_bytes(int which_call, const seer_shape *shape)
     case SEER_CALL_DECODE_GATE_CACHED:
         return ((sizeof(float) * (size_t)shape->B * shape->Hq * shape->d + 255) & ~size_t(255)) +
                ((sizeof(float) * (size_t)shape->B * shape->Hq * 256 + 255) & ~size_t(255));
+    case SEER_CALL_GATE_KEY_CACHE_QUANT:
+        return gate_key_ws_bytes(shape->B, shape->Hkv, shape->S, shape->d, true);
     case SEER_CALL_BLOCK_SPARSE_DECODE:
+    case SEER_CALL_BLOCK_SPARSE_DECODE_QUANT:
         return sizeof(float) * (size_t)shape->B * shape->Hq * kMaxDecodeSplits * (shape->d + 2);
     default:
         fail(SEER_ERR_INVALID_ARG, "unknown call id %d", which_call);
@@ -471,6 +475,9 @@ seer_status seer_check_status(void *stream)
         if (v == kStatusSmem)
             return fail(SEER_ERR_DEVICE, "the attention kernel's shared-memory layout did not fit its window once "
                                          "aligned (no output was written)");
+        if (v == kStatusPage)
+            return fail(SEER_ERR_DEVICE, "a quantised-cache call met a position beyond the cache or a block table entry "
+                                         "outside its pages (those blocks were left out)");
         return fail(SEER_ERR_DEVICE, "device-side check failed (code %d)", v);
     }
     return ok();
@@ -602,6 +609,159 @@ seer_status seer_block_sparse_decode(const seer_shape *shape, const void *q_tok,
                       mask, o, lse, static_cast<float *>(workspace), static_cast<cudaStream_t>(stream));
     if (e != cudaSuccess)
         return cuda_fail(e, "seer_block_sparse_decode launch");
+    return ok();
+}
+
+// ------------------------------------------------------------ quantised KV cache
+size_t seer_kv_record_bytes(int bits, int d)
+{
+    const int n = kv_record_bytes(bits, d);
+    if (n == 0)
+        fail(SEER_ERR_UNSUPPORTED, "no cache record for %d bits and head dim %d (4 or 8, 64 or 128)", bits, d);
+    return (size_t)n;
+}
+
+// Checks shared by the calls on a quantised cache.
+static seer_status check_cache(const char *name, const seer_shape *shape, const seer_kv_cache *cache)
+{
+    const seer_status st = check_shape(shape);
+    if (st != SEER_OK)
+        return st;
+    if (cache == nullptr || cache->pages == nullptr)
+        return fail(SEER_ERR_INVALID_ARG, "%s: NULL cache or pages", name);
+    if (cache->bits != 4 && cache->bits != 8)
+        return fail(SEER_ERR_UNSUPPORTED, "%s: a cache of %d bits is not supported (4 or 8)", name, cache->bits);
+    if (!aligned16(cache->pages))
+        return fail(SEER_ERR_INVALID_ARG, "%s: pages must be 16-byte aligned", name);
+    if (cache->n_pages < 1 || cache->max_blocks < 1)
+        return fail(SEER_ERR_INVALID_ARG, "%s: n_pages and max_blocks must be positive", name);
+    if (cache->max_blocks > kMaxNb)
+        return fail(SEER_ERR_UNSUPPORTED, "%s: max_blocks %d exceeds %d", name, cache->max_blocks, kMaxNb);
+    if (cache->block_table == nullptr && cache->n_pages < (long long)shape->B * cache->max_blocks)
+        return fail(SEER_ERR_INVALID_ARG, "%s: %d pages are fewer than B * max_blocks = %lld and there is no block table",
+                    name, cache->n_pages, (long long)shape->B * cache->max_blocks);
+    return SEER_OK;
+}
+
+static seer_status check_cached_length(const char *name, const seer_shape *shape, const seer_kv_cache *cache)
+{
+    if (num_blocks(shape->S) > cache->max_blocks)
+        return fail(SEER_ERR_INVALID_ARG, "%s: %d tokens need %d blocks, the cache has %d per sequence", name, shape->S,
+                    num_blocks(shape->S), cache->max_blocks);
+    return SEER_OK;
+}
+
+static KvView view_of(const seer_kv_cache *cache)
+{
+    return KvView{static_cast<uint8_t *>(cache->pages), cache->block_table, cache->n_pages, cache->max_blocks};
+}
+
+seer_status seer_kv_write(const seer_shape *shape, const seer_kv_cache *cache, const seer_kv_rows *rows,
+                          const int32_t *start, const int32_t *count, int start_pos, void *stream)
+{
+    const seer_status st = check_cache("seer_kv_write", shape, cache);
+    if (st != SEER_OK)
+        return st;
+    if (rows == nullptr || rows->k == nullptr || rows->v == nullptr)
+        return fail(SEER_ERR_INVALID_ARG, "seer_kv_write: NULL rows");
+    if (!aligned16(rows->k) || !aligned16(rows->v))
+        return fail(SEER_ERR_INVALID_ARG, "seer_kv_write: k and v must be 16-byte aligned");
+    for (const long long stride : {rows->k_stride_b, rows->k_stride_h, rows->k_stride_t, rows->v_stride_b,
+                                   rows->v_stride_h, rows->v_stride_t})
+        if (stride < 0 || stride % 8 != 0)
+            return fail(SEER_ERR_INVALID_ARG, "seer_kv_write: row strides must be >= 0 and multiples of 8 elements");
+    int *status = status_ptr();
+    if (status == nullptr)
+        return fail(SEER_ERR_CUDA, "cannot resolve the device status word");
+    const cudaError_t e = launch_kv_write(cache->bits, shape->B, shape->Hkv, shape->S, shape->d, view_of(cache), *rows,
+                                          start, count, start_pos, status, static_cast<cudaStream_t>(stream));
+    if (e != cudaSuccess)
+        return cuda_fail(e, "seer_kv_write launch");
+    return ok();
+}
+
+seer_status seer_kv_read(const seer_shape *shape, const seer_kv_cache *cache, const int32_t *start,
+                         const int32_t *count, int start_pos, void *k, void *v, void *stream)
+{
+    const seer_status st = check_cache("seer_kv_read", shape, cache);
+    if (st != SEER_OK)
+        return st;
+    if (k == nullptr && v == nullptr)
+        return fail(SEER_ERR_INVALID_ARG, "seer_kv_read: k and v are both NULL");
+    if (!aligned16(k) || !aligned16(v))
+        return fail(SEER_ERR_INVALID_ARG, "seer_kv_read: k and v must be 16-byte aligned");
+    int *status = status_ptr();
+    if (status == nullptr)
+        return fail(SEER_ERR_CUDA, "cannot resolve the device status word");
+    const cudaError_t e = launch_kv_read(cache->bits, shape->B, shape->Hkv, shape->S, shape->d, view_of(cache), start,
+                                         count, start_pos, k, v, status, static_cast<cudaStream_t>(stream));
+    if (e != cudaSuccess)
+        return cuda_fail(e, "seer_kv_read launch");
+    return ok();
+}
+
+seer_status seer_gate_key_cache_quant(const seer_shape *shape, const seer_kv_cache *cache, const int32_t *lens,
+                                      const void *wk, const seer_gate_params *gp, int first_block, float *kt,
+                                      void *workspace, size_t ws_bytes, void *stream)
+{
+    seer_status st = check_cache("seer_gate_key_cache_quant", shape, cache);
+    if (st != SEER_OK)
+        return st;
+    // the q, k and wq checks of the shared helper are satisfied with the pages and wk
+    st = check_gate_args("seer_gate_key_cache_quant", shape, cache->pages, cache->pages, wk, wk, gp, kt, workspace,
+                         ws_bytes, 2);
+    if (st != SEER_OK)
+        return st;
+    st = check_cached_length("seer_gate_key_cache_quant", shape, cache);
+    if (st != SEER_OK)
+        return st;
+    if (first_block < 0 || first_block > num_blocks(shape->S))
+        return fail(SEER_ERR_INVALID_ARG, "first_block %d outside [0, %d]", first_block, num_blocks(shape->S));
+    int *status = status_ptr();
+    if (status == nullptr)
+        return fail(SEER_ERR_CUDA, "cannot resolve the device status word");
+    const cudaError_t e = launch_gate_keys_quant(
+        cache->bits, shape->B, shape->Hkv, shape->S, shape->d, gp->d_gate, gp->rope_theta,
+        gp->k_pooling == SEER_KPOOL_MAXMIN, view_of(cache), lens, wk, gp->wk_head_stride, first_block, kt, workspace,
+        status, static_cast<cudaStream_t>(stream));
+    if (e != cudaSuccess)
+        return cuda_fail(e, "seer_gate_key_cache_quant launch");
+    return ok();
+}
+
+seer_status seer_block_sparse_decode_quant(const seer_shape *shape, const void *q_tok, const seer_kv_cache *cache,
+                                           const int32_t *lens, const uint8_t *mask, float softmax_scale, void *o,
+                                           float *lse, void *workspace, size_t ws_bytes, void *stream)
+{
+    seer_status st = check_cache("seer_block_sparse_decode_quant", shape, cache);
+    if (st != SEER_OK)
+        return st;
+    st = attention_common("seer_block_sparse_decode_quant", shape, q_tok, cache->pages, cache->pages, o);
+    if (st != SEER_OK)
+        return st;
+    st = check_cached_length("seer_block_sparse_decode_quant", shape, cache);
+    if (st != SEER_OK)
+        return st;
+    if (mask == nullptr)
+        return fail(SEER_ERR_INVALID_ARG, "seer_block_sparse_decode_quant: NULL mask");
+    if (std::isnan(softmax_scale) || std::isinf(softmax_scale))
+        return fail(SEER_ERR_INVALID_ARG, "softmax_scale must be finite");
+    const size_t need = seer_workspace_bytes(SEER_CALL_BLOCK_SPARSE_DECODE_QUANT, shape);
+    if (workspace == nullptr || ws_bytes < need)
+        return fail(SEER_ERR_WORKSPACE, "seer_block_sparse_decode_quant needs %zu workspace bytes, got %zu", need,
+                    ws_bytes);
+    if (!aligned16(workspace))
+        return fail(SEER_ERR_WORKSPACE, "workspace must be 16-byte aligned");
+    int *status = status_ptr();
+    if (status == nullptr)
+        return fail(SEER_ERR_CUDA, "cannot resolve the device status word");
+    const float scale = softmax_scale > 0.f ? softmax_scale : 1.0f / sqrtf((float)shape->d);
+    const cudaError_t e = launch_decode_quant(
+        cache->bits, shape->B, shape->Hq, shape->Hkv, shape->S, shape->d, scale * 1.4426950408889634f, q_tok,
+        view_of(cache), lens, mask, o, lse, static_cast<float *>(workspace), status, g_timeout_ns,
+        static_cast<cudaStream_t>(stream));
+    if (e != cudaSuccess)
+        return cuda_fail(e, "seer_block_sparse_decode_quant launch");
     return ok();
 }
 

@@ -53,6 +53,8 @@ cudaError_t launch_decode_gate(int B, int Hq, int Hkv, int L, int d, int dg, flo
 cudaError_t launch_gate_keys(int B, int Hkv, int L, int d, int dg, float theta, bool k_maxmin, const void *k,
                              const void *wk, long long wk_stride, int first_block, float *kt, void *ws,
                              cudaStream_t stream);
+cudaError_t launch_project_keys(int B, int Hkv, int nb, int dk, int dg, float theta, const float *kp, const void *wk,
+                                long long wk_stride, int first_block, float *kt, cudaStream_t stream);
 cudaError_t launch_decode_gate_cached(int B, int Hq, int Hkv, int L, int d, int dg, float theta, const void *q_tok,
                                       const void *wq, long long wq_stride, const float *kt, float *scores, void *ws,
                                       cudaStream_t stream);
@@ -65,6 +67,22 @@ int decode_splits(int B, int Hq, int nb);
 int decode_splits_for(int B, int units_per_b, int nb, int per_sm);
 cudaError_t launch_decode(int B, int Hq, int Hkv, int L, int d, float scale_log2, const void *q_tok, const void *k,
                           const void *v, const uint8_t *mask, void *o, float *lse, float *part, cudaStream_t stream);
+
+// Quantised KV cache (seer_kvcache.cu, seer_kvgate.cu, seer_kvdecode.cu).
+struct KvView;
+typedef seer_kv_rows KvRows;
+int kv_record_bytes(int bits, int d);
+cudaError_t launch_kv_write(int bits, int B, int Hkv, int n, int d, const KvView &kv, const KvRows &x,
+                            const int32_t *start, const int32_t *count, int start_pos, int *status,
+                            cudaStream_t stream);
+cudaError_t launch_kv_read(int bits, int B, int Hkv, int n, int d, const KvView &kv, const int32_t *start,
+                           const int32_t *count, int start_pos, void *k, void *v, int *status, cudaStream_t stream);
+cudaError_t launch_gate_keys_quant(int bits, int B, int Hkv, int L, int d, int dg, float theta, bool k_maxmin,
+                                   const KvView &kv, const int32_t *lens, const void *wk, long long wk_stride,
+                                   int first_block, float *kt, void *ws, int *status, cudaStream_t stream);
+cudaError_t launch_decode_quant(int bits, int B, int Hq, int Hkv, int L, int d, float scale_log2, const void *q_tok,
+                                const KvView &kv, const int32_t *lens, const uint8_t *mask, void *o, float *lse,
+                                float *part, int *status, uint64_t timeout_ns, cudaStream_t stream);
 
 // Mask / compaction kernels (seer_mask.cu).
 cudaError_t launch_mask(int B, int Hq, int nb, const float *scores, int mode, float threshold,

@@ -11,7 +11,9 @@ namespace seer {
 // Device status codes written through the status pointer every kernel gets
 // (first error wins).  kStatusSmem: a kernel found its shared-memory layout,
 // after aligning the window's base, larger than the dynamic window it was given.
-enum : int { kStatusOk = 0, kStatusTimeout = 5, kStatusDevice = 6, kStatusRing = 7, kStatusSmem = 8 };
+// kStatusPage: a quantised-cache call met a position beyond the cache or a
+// block table entry that names none of its pages, and left that block out.
+enum : int { kStatusOk = 0, kStatusTimeout = 5, kStatusDevice = 6, kStatusRing = 7, kStatusSmem = 8, kStatusPage = 9 };
 
 __device__ __forceinline__ void set_status(int *status, int s)
 {

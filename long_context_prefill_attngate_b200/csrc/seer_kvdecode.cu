@@ -1,9 +1,34 @@
 // seer_kvdecode.cu — block-sparse attention of one new token per sequence over
 // the quantised cache.
 //
-// o[b,h] = sum over t < len in active blocks of softmax(q . k_t * scale) v_t
-// with k_t, v_t = z + s n of the cache.
+//   o[b,h] = sum over t < len in active blocks of softmax(q . k_t * scale) v_t,
+//   k_t = z + s n (per group of the row), v_t likewise.
+//
+// Each active block crosses HBM once per GQA group: a CTA serves up to eight
+// query heads of one KV head over the union of their active blocks (a head
+// without a block gets p = 0 there).  At 4 bits a token's K and V are 160 bytes
+// for 4 D flops per head, so with CUDA-core products the arithmetic, not HBM,
+// would set the time (at D = 128 and four heads 2048 flops per 160 bytes); the
+// products are mma.sync m16n8k16 with the keys on M (K Q^T) or the output
+// elements on M (V^T P) and the heads on N.  Decode has at most eight columns
+// of N, which leaves a tcgen05 tile nothing to gain.
+//
+//  * The codes enter the MMA as they are: n <= 255 in the low bits of an fp16 is
+//    the subnormal n 2^-24, so one mask (4 bits) or byte permute (8 bits) makes
+//    a pair of operands, and scale and zero are applied outside:
+//      q . k   = sum_g s_g (q_g . n_g) + z_g sum(q_g)        fp32, per key
+//      sum p v = sum_t (p_t s_t,g) n_t + sum_t p_t z_t,g      p s rounded to fp16
+//    q is exact in fp16 after a power of two per head; p s <= 2^15 after a power
+//    of two that follows the largest scale seen (as a running maximum, so it
+//    holds for any range of V).  p z, the row sums and all accumulators are fp32.
+//  * Work of a warp: half records of 32 tokens, each one contiguous bulk copy
+//    into the warp's own ring, so no warp waits for another until the end.
+//  * P leaves K Q^T with keys across lanes and enters V^T P with keys across a
+//    lane's register pair: movmatrix turns each 8 x 8 piece.
+//  * Split over the union's blocks by rank, so splits differ by one block at
+//    most; a second kernel joins them.
 #include <cuda_bf16.h>
+#include <cuda_fp16.h>
 
 #include "seer_internal.h"
 #include "seer_kv.cuh"
@@ -12,7 +37,8 @@ namespace seer {
 
 namespace {
 
-constexpr int kQDT = 128;
+constexpr int kHeads = 8;                 // query heads of a CTA: the N of the MMA
+constexpr int kListMax = 2049;            // blocks of a split (decode_quant_splits)
 
 __device__ __forceinline__ float exp2_approx(float x)
 {
@@ -21,77 +47,538 @@ __device__ __forceinline__ float exp2_approx(float x)
     return y;
 }
 
-// Element e of token t's K or V row in a half record.
-template <class F, int BITS, bool V>
-__device__ __forceinline__ float kv_element(const uint8_t *half, int t, int e)
+__device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                         uint32_t b1)
 {
-    const int m = e * BITS / 8;
-    const uint32_t byte = half[V ? F::kCodeV + F::v_off(t, m) : F::k_off(t, m)];
-    const uint32_t par =
-        *reinterpret_cast<const uint32_t *>(half + (V ? F::kParV : F::kParK) + t * F::PAR + e / F::G * 4);
-    return fmaf(kv_scale(par), (float)(BITS == 8 ? byte : (byte >> (4 * (e & 1))) & 15u), kv_zero(par));
+    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+                 : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+                 : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
-// One CTA per (query head, split); the splits share the head's blocks by
-// index.  A thread has a key in the scores and an output element in P V.
+__device__ __forceinline__ uint32_t movmatrix(uint32_t x)
+{
+    uint32_t y;
+    asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+    return y;
+}
+
+__device__ __forceinline__ uint32_t pack_half2(float lo, float hi)
+{
+    uint32_t r;
+    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+
+__device__ __forceinline__ float pow2_field(int field) { return __uint_as_float((uint32_t)field << 23); }
+
+__device__ __forceinline__ void bulk_copy(uint32_t dst, const void *src, uint32_t bytes, uint32_t bar)
+{
+    asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
+                 "l"(src), "r"(bytes), "r"(bar)
+                 : "memory");
+}
+
+template <int N>
+__device__ __forceinline__ void load_words(uint32_t (&w)[N], const uint8_t *p)
+{
+    if constexpr (N % 4 == 0) {
+#pragma unroll
+        for (int i = 0; i < N / 4; ++i) {
+            const uint4 u = reinterpret_cast<const uint4 *>(p)[i];
+            w[4 * i] = u.x;
+            w[4 * i + 1] = u.y;
+            w[4 * i + 2] = u.z;
+            w[4 * i + 3] = u.w;
+        }
+    } else if constexpr (N == 2) {
+        const uint2 u = *reinterpret_cast<const uint2 *>(p);
+        w[0] = u.x;
+        w[1] = u.y;
+    } else {
+        static_assert(N == 1);
+        w[0] = *reinterpret_cast<const uint32_t *>(p);
+    }
+}
+
+// Row of an MMA tile -> token: within eight rows (0,1,3,2,4,5,7,6), so that the
+// rows of a K fragment's quarter warp have both parities and the four rows that
+// a V fragment reads at once differ in the bits its swizzle uses.
+__device__ __forceinline__ int tile_token(int r) { return r ^ ((r >> 1) & 1); }
+
+struct DecodeArgs {
+    const __nv_bfloat16 *q_tok;
+    KvView kv;
+    const int32_t *lens;
+    const uint8_t *mask;
+    int Hq, Hkv, L, nb, tiles, per_tile, nsplit;
+    float scale_log2;
+    float *part;
+    __nv_bfloat16 *o;
+    float *lse;
+    int *status;
+    uint64_t timeout_ns;
+};
+
+// Warps of a CTA and half records in flight per warp: one CTA per SM whose ring
+// holds two to four tokens' worth of latency (the SM's share of HBM is 24 bytes
+// a cycle, some 36 KB in flight).
 template <int BITS, int D>
-__global__ void __launch_bounds__(kQDT)
-    decode_quant_kernel(const __nv_bfloat16 *q_tok, KvView kv, const int32_t *lens, const uint8_t *mask, int Hq, int Hkv,
-                        int L, int nb, float scale_log2, int nsplit, float *part, int *status)
+struct DecodeCfg {
+    static constexpr int W = BITS == 8 && D == 128 ? 12 : 16;
+    static constexpr int ST = BITS == 4 && D == 64 ? 4 : 2;
+    static constexpr int ring = W * ST * KvFmt<BITS, D>::HALF;
+};
+
+template <int BITS, int D>
+__global__ void __launch_bounds__(DecodeCfg<BITS, D>::W * 32, 1) decode_quant_kernel(const DecodeArgs a)
 {
     using F = KvFmt<BITS, D>;
-    __shared__ float s_q[D], s_p[64], s_red[2];
-    const int split = blockIdx.x, t = threadIdx.x;
-    const long long bh = blockIdx.y;
-    const int b = (int)(bh / Hq), h = (int)(bh % Hq), kvh = h / (Hq / Hkv);
-    const int len = lens != nullptr ? max(0, min(lens[b], L)) : L;
-    if (t < D)
-        s_q[t] = __bfloat162float(q_tok[bh * D + t]);
-    float m = -INFINITY, l = 0.f, o = 0.f;
-    for (int j = split; 64 * j < len; j += nsplit) {
-        if (mask[bh * nb + j] == 0)
-            continue;
-        const int page = kv_page(kv, b, j, status);
-        if (page < 0)
-            continue;
-        __syncthreads();
-        float s = -INFINITY;
-        if (t < 64 && 64 * j + t < len) {
-            const uint8_t *half = kv_half<F>(kv, Hkv, page, kvh, t / 32);
-            float acc = 0.f;
-            for (int e = 0; e < D; ++e)
-                acc = fmaf(s_q[e], kv_element<F, BITS, false>(half, t % 32, e), acc);
-            s = acc * scale_log2;
+    using C = DecodeCfg<BITS, D>;
+    constexpr int W = C::W, ST = C::ST, NG = F::NG, R = F::R;
+    constexpr int KS = D / 16;                      // MMA steps of a score; also MMA rows of an output / 16
+    constexpr int KW = R / 16, VW = R / 32;         // 32-bit words of a lane's K row, V row
+    constexpr int UPG = KS / NG;                    // MMAs of a group
+    extern __shared__ __align__(128) uint8_t ring[];
+    __shared__ __align__(8) uint64_t s_bar[W * ST];
+    __shared__ float2 s_ml[W][kHeads];
+    __shared__ uint32_t s_words[kMaxNb / 32];
+    __shared__ int s_page[kListMax];
+    __shared__ uint16_t s_block[kListMax];
+
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int gid = lane >> 2, tig = lane & 3;
+    const int split = blockIdx.x;
+    const int tile = blockIdx.y % a.tiles, bk = blockIdx.y / a.tiles;
+    const int b = bk / a.Hkv, kvh = bk % a.Hkv;
+    const int g = a.Hq / a.Hkv;
+    const int h0 = kvh * g + tile * a.per_tile;     // first query head, and how many
+    const int gt = min(a.per_tile, g - tile * a.per_tile);
+    const int len = a.lens != nullptr ? max(0, min(a.lens[b], a.L)) : a.L;
+    const uint8_t *mrow = a.mask + ((long long)b * a.Hq + h0) * a.nb;
+
+    asm volatile("griddepcontrol.launch_dependents;");
+    if (lane == 0) {
+        for (int s = 0; s < ST; ++s)
+            mbar_init(smem_u32(&s_bar[warp * ST + s]), 1);
+        fence_mbar_init();
+    }
+
+    // ---- union of the heads' active blocks, one bit each
+    const int nblk = (len + 63) / 64, nwords = (nblk + 31) / 32;
+    for (int c = warp; c < nwords; c += W) {
+        const int j = c * 32 + lane;
+        int any = 0;
+        if (j < nblk) {
+#pragma unroll
+            for (int h = 0; h < kHeads; ++h)
+                if (h < gt)
+                    any |= __ldg(mrow + (long long)h * a.nb + j);
+            if (any != 0 && kv_page(a.kv, b, j, a.status) < 0)
+                any = 0;
         }
-        float wm = s;
-        for (int off = 16; off >= 1; off >>= 1)
-            wm = fmaxf(wm, __shfl_xor_sync(0xffffffffu, wm, off));
-        if (t < 64 && (t & 31) == 0)
-            s_red[t / 32] = wm;
-        __syncthreads();
-        const float m_new = fmaxf(m, fmaxf(s_red[0], s_red[1]));
-        const float m_use = m_new == -INFINITY ? 0.f : m_new;
-        if (t < 64)
-            s_p[t] = exp2_approx(s - m_use);
-        __syncthreads();
-        const float alpha = exp2_approx(m - m_use);
-        m = m_new;
-        l *= alpha;
-        o *= alpha;
-        const int keys = min(64, len - 64 * j);
-        for (int c = 0; c < keys; ++c) {
-            const uint8_t *half = kv_half<F>(kv, Hkv, page, kvh, c / 32);
-            l += s_p[c];
-            if (t < D)
-                o = fmaf(s_p[c], kv_element<F, BITS, true>(half, c % 32, t), o);
+        const unsigned bits = __ballot_sync(0xffffffffu, any != 0);
+        if (lane == 0)
+            s_words[c] = bits;
+    }
+
+    // ---- q fragments: column gid = head h0 + gid, in fp16 times 2^qe
+    uint32_t qf[KS][2];
+    float qs[NG][2], qinv[2];                       // of heads 2 tig, 2 tig + 1: group sums, 2^-qe
+    {
+        float f[KS * 4];                            // this lane's elements, in its K words' order
+        const __nv_bfloat16 *qp = a.q_tok + ((long long)b * a.Hq + h0 + gid) * D;
+#pragma unroll
+        for (int i = 0; i < KS; ++i) {              // four elements at a time
+            const int e = BITS == 4 ? 32 * (i / 2) + 8 * tig + 4 * (i % 2) : 16 * i + 4 * tig;
+            uint2 u = make_uint2(0u, 0u);
+            if (gid < gt)
+                u = __ldg(reinterpret_cast<const uint2 *>(qp + e));
+            f[4 * i] = __uint_as_float(u.x << 16);
+            f[4 * i + 1] = __uint_as_float(u.x & 0xFFFF0000u);
+            f[4 * i + 2] = __uint_as_float(u.y << 16);
+            f[4 * i + 3] = __uint_as_float(u.y & 0xFFFF0000u);
+        }
+        float mx = 0.f;
+#pragma unroll
+        for (int i = 0; i < KS * 4; ++i)
+            mx = fmaxf(mx, fabsf(f[i]));
+        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+        // max |q| 2^qe in [2^14, 2^15); no scaling for 0 and infinity
+        const int eb = (int)(__float_as_uint(mx) >> 23);
+        const int qe = mx == 0.f || eb == 255 ? 0 : min(141 - eb, 126);
+        const float up = pow2_field(127 + qe), down = pow2_field(127 - qe);
+#pragma unroll
+        for (int i = 0; i < KS * 4; ++i)
+            f[i] *= up;
+        float gs[NG];
+#pragma unroll
+        for (int gr = 0; gr < NG; ++gr) {
+            float s = 0.f;
+#pragma unroll
+            for (int i = 0; i < KS * 4 / NG; ++i)
+                s += f[gr * (KS * 4 / NG) + i];
+            s += __shfl_xor_sync(0xffffffffu, s, 1);
+            s += __shfl_xor_sync(0xffffffffu, s, 2);
+            gs[gr] = s * 5.9604644775390625e-8f;    // 2^-24: the unit of the codes' products
+        }
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+            const int src = (2 * tig + u) * 4;
+#pragma unroll
+            for (int gr = 0; gr < NG; ++gr)
+                qs[gr][u] = __shfl_sync(0xffffffffu, gs[gr], src);
+            qinv[u] = __shfl_sync(0xffffffffu, down, src);
+        }
+        // operand pairs as the codes' masks give them: at 4 bits elements (0,4),
+        // (1,5) 2^4, (2,6), (3,7) 2^4 of a word, so the second is taken 2^-4
+#pragma unroll
+        for (int i = 0; i < KS; ++i) {
+            if (BITS == 4) {
+                const float *w = f + 8 * (i / 2) + 2 * (i % 2);
+                qf[i][0] = pack_half2(w[0], w[4]);
+                qf[i][1] = pack_half2(w[1] * 0.0625f, w[5] * 0.0625f);
+            } else {
+                qf[i][0] = pack_half2(f[4 * i], f[4 * i + 1]);
+                qf[i][1] = pack_half2(f[4 * i + 2], f[4 * i + 3]);
+            }
         }
     }
-    float *out = part + (bh * nsplit + split) * (D + 2);
-    if (t < D)
-        out[t] = o;
-    if (t == 0) {
-        out[D] = m;
-        out[D + 1] = l;
+    __syncthreads();
+
+    // ---- this split's blocks: ranks [r0, r1) of the union
+    int r0, r1;
+    {
+        const int per = (nwords + 31) / 32;         // words of a lane
+        int cnt = 0;
+        for (int k = 0; k < per; ++k)
+            if (lane * per + k < nwords)
+                cnt += __popc(s_words[lane * per + k]);
+        int inc = cnt;
+#pragma unroll
+        for (int off = 1; off < 32; off <<= 1) {
+            const int v = __shfl_up_sync(0xffffffffu, inc, off);
+            inc += lane >= off ? v : 0;
+        }
+        const int total = __shfl_sync(0xffffffffu, inc, 31);
+        r0 = total * split / a.nsplit;
+        r1 = total * (split + 1) / a.nsplit;
+        for (int c = warp; c < nwords; c += W) {
+            int base = __shfl_sync(0xffffffffu, inc - cnt, c / per);
+            for (int k = c / per * per; k < c; ++k)
+                base += __popc(s_words[k]);
+            const unsigned w = s_words[c];
+            const int r = base + __popc(w & ((1u << lane) - 1u));
+            if ((w >> lane & 1u) && r >= r0 && r < r1) {
+                const int j = c * 32 + lane;
+                s_block[r - r0] = (uint16_t)j;
+                s_page[r - r0] =
+                    a.kv.table != nullptr ? __ldg(a.kv.table + (long long)b * a.kv.max_blocks + j) : b * a.kv.max_blocks + j;
+            }
+        }
+    }
+    __syncthreads();
+
+    const int n_units = 2 * (r1 - r0);              // half records
+    uint8_t *my = ring + warp * ST * F::HALF;
+    auto issue = [&](int u, int st) {               // lane 0
+        if (u >= n_units || 64 * s_block[u >> 1] + 32 * (u & 1) >= len)
+            return;
+        const uint32_t bar = smem_u32(&s_bar[warp * ST + st]);
+        mbar_arrive_expect_tx(bar, F::HALF);
+        bulk_copy(smem_u32(my + st * F::HALF), kv_half<F>(a.kv, a.Hkv, s_page[u >> 1], kvh, u & 1), F::HALF, bar);
+    };
+    auto head_byte = [&](int u) {
+        return u < n_units && lane < gt ? (int)__ldg(mrow + (long long)lane * a.nb + s_block[u >> 1]) : 0;
+    };
+    if (lane == 0)
+        for (int s = 0; s < ST; ++s)
+            issue(warp + s * W, s);
+
+    float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f}, zacc[NG][2], acc[KS][4];
+    int ve = 27;                                    // exponent field of V's largest scale so far
+#pragma unroll
+    for (int i = 0; i < KS; ++i)
+        acc[i][0] = acc[i][1] = acc[i][2] = acc[i][3] = 0.f;
+#pragma unroll
+    for (int gr = 0; gr < NG; ++gr)
+        zacc[gr][0] = zacc[gr][1] = 0.f;
+    const float to_log2 = a.scale_log2 * 16777216.f;    // 2^24
+
+    int mb = head_byte(warp);
+    int it = 0;
+    for (int u = warp; u < n_units; u += W, ++it) {
+        const unsigned hbits = __ballot_sync(0xffffffffu, mb != 0 || lane >= gt);
+        mb = head_byte(u + W);
+        const int keys = len - (64 * s_block[u >> 1] + 32 * (u & 1));
+        if (keys <= 0)
+            break;                                  // the empty half of the last block: nothing follows
+        const int st = it % ST;
+        {
+            const uint32_t bar = smem_u32(&s_bar[warp * ST + st]), parity = (it / ST) & 1;
+            bool done = mbar_test_wait(bar, parity);
+            if (!done) {
+                const uint64_t t0 = globaltimer();
+                while (!done && globaltimer() - t0 < a.timeout_ns)
+                    done = mbar_try_wait_sleep(bar, parity, 20000u);
+            }
+            if (!__all_sync(0xffffffffu, done)) {
+                // give up: wait for this warp's copies in flight, contribute nothing
+                set_status(a.status, kStatusTimeout);
+                for (int s = 0; s < ST; ++s) {
+                    const int w = it + s;
+                    const int uu = warp + w * W;
+                    if (uu < n_units && 64 * s_block[uu >> 1] + 32 * (uu & 1) < len)
+                        mbar_drain(smem_u32(&s_bar[warp * ST + w % ST]), (w / ST) & 1, 200000000ull);
+                }
+                m[0] = m[1] = -INFINITY;
+                l[0] = l[1] = 0.f;
+                break;
+            }
+        }
+        const uint8_t *h = my + st * F::HALF;
+
+        // ---- scores of two 16-token tiles, log2 units
+        float s[2][4];
+#pragma unroll
+        for (int mt = 0; mt < 2; ++mt) {
+            const int ra = 16 * mt + tile_token(gid), rb = ra + 8;
+            uint32_t ka[KW], kb[KW], pa[NG], pb[NG];
+            if constexpr (BITS == 8 && D == 128) {
+                uint32_t (&a0)[4] = *reinterpret_cast<uint32_t (*)[4]>(ka);
+                uint32_t (&a1)[4] = *reinterpret_cast<uint32_t (*)[4]>(ka + 4);
+                uint32_t (&b0)[4] = *reinterpret_cast<uint32_t (*)[4]>(kb);
+                uint32_t (&b1)[4] = *reinterpret_cast<uint32_t (*)[4]>(kb + 4);
+                load_words(a0, h + ra * R + (ra & 1) * 64 + tig * 16);
+                load_words(a1, h + ra * R + (~ra & 1) * 64 + tig * 16);
+                load_words(b0, h + rb * R + (rb & 1) * 64 + tig * 16);
+                load_words(b1, h + rb * R + (~rb & 1) * 64 + tig * 16);
+            } else {
+                load_words(ka, h + ra * R + tig * (R / 4));
+                load_words(kb, h + rb * R + tig * (R / 4));
+            }
+            load_words(pa, h + F::kParK + ra * F::PAR);
+            load_words(pb, h + F::kParK + rb * F::PAR);
+            s[mt][0] = s[mt][1] = s[mt][2] = s[mt][3] = 0.f;
+#pragma unroll
+            for (int gr = 0; gr < NG; ++gr) {
+                float c[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                for (int i = 0; i < UPG; ++i) {
+                    const int ks = gr * UPG + i;
+                    if (BITS == 4) {
+                        const uint32_t wa = ka[ks / 2] >> (8 * (ks % 2)), wb = kb[ks / 2] >> (8 * (ks % 2));
+                        mma16816(c, wa & 0x000F000Fu, wb & 0x000F000Fu, wa & 0x00F000F0u, wb & 0x00F000F0u, qf[ks][0],
+                                 qf[ks][1]);
+                    } else {
+                        const uint32_t wa = ka[ks], wb = kb[ks];
+                        mma16816(c, __byte_perm(wa, 0u, 0x4140), __byte_perm(wb, 0u, 0x4140),
+                                 __byte_perm(wa, 0u, 0x4342), __byte_perm(wb, 0u, 0x4342), qf[ks][0], qf[ks][1]);
+                    }
+                }
+                const float sa = kv_scale(pa[gr]), za = kv_zero(pa[gr]), sb = kv_scale(pb[gr]), zb = kv_zero(pb[gr]);
+                s[mt][0] = fmaf(sa, c[0], fmaf(za, qs[gr][0], s[mt][0]));
+                s[mt][1] = fmaf(sa, c[1], fmaf(za, qs[gr][1], s[mt][1]));
+                s[mt][2] = fmaf(sb, c[2], fmaf(zb, qs[gr][0], s[mt][2]));
+                s[mt][3] = fmaf(sb, c[3], fmaf(zb, qs[gr][1], s[mt][3]));
+            }
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                s[mt][e] = s[mt][e] * qinv[e & 1] * to_log2;
+        }
+        const bool all_heads = hbits == 0xffffffffu;
+        const bool act0 = hbits >> (2 * tig) & 1u, act1 = hbits >> (2 * tig + 1) & 1u;
+        if (keys < 32 || !all_heads) {
+#pragma unroll
+            for (int mt = 0; mt < 2; ++mt)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const int t = 16 * mt + tile_token(gid) + (e & 2) * 4;
+                    if (t >= keys || !((e & 1) ? act1 : act0))
+                        s[mt][e] = -INFINITY;
+                }
+        }
+
+        // ---- V's params (zero behind the length) and the power of two for p s
+        uint32_t vp[2][2][NG];                      // [tile][row, row + 8]
+        uint32_t vmax = 0;
+#pragma unroll
+        for (int mt = 0; mt < 2; ++mt)
+#pragma unroll
+            for (int hf = 0; hf < 2; ++hf) {
+                const int t = 16 * mt + tile_token(gid) + 8 * hf;
+                load_words(vp[mt][hf], h + F::kParV + t * F::PAR);
+                if (t >= keys)
+#pragma unroll
+                    for (int gr = 0; gr < NG; ++gr)
+                        vp[mt][hf][gr] = 0u;
+#pragma unroll
+                for (int gr = 0; gr < NG; ++gr)
+                    vmax = __vmaxu2(vmax, vp[mt][hf][gr]);
+            }
+        float mx[2];
+#pragma unroll
+        for (int e = 0; e < 2; ++e)
+            mx[e] = fmaxf(fmaxf(s[0][e], s[0][e + 2]), fmaxf(s[1][e], s[1][e + 2]));
+#pragma unroll
+        for (int off = 4; off < 32; off <<= 1) {
+            mx[0] = fmaxf(mx[0], __shfl_xor_sync(0xffffffffu, mx[0], off));
+            mx[1] = fmaxf(mx[1], __shfl_xor_sync(0xffffffffu, mx[1], off));
+            vmax = __vmaxu2(vmax, __shfl_xor_sync(0xffffffffu, vmax, off));
+        }
+        const int ve_new = max(ve, (int)(vmax >> 7 & 0xFFu));
+        float alpha[2], mu[2];
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+            const float mn = fmaxf(m[e], mx[e]);
+            mu[e] = mn == -INFINITY ? 0.f : mn;
+            alpha[e] = mn == -INFINITY ? 1.f : exp2_approx(m[e] - mu[e]);
+            m[e] = mn;
+        }
+        if (__any_sync(0xffffffffu, alpha[0] != 1.f || alpha[1] != 1.f || ve_new != ve)) {
+            const float down = ve - ve_new > -127 ? pow2_field(127 + ve - ve_new) : 0.f;
+#pragma unroll
+            for (int i = 0; i < KS; ++i)
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    acc[i][e] *= alpha[e & 1] * down;
+#pragma unroll
+            for (int gr = 0; gr < NG; ++gr) {
+                zacc[gr][0] *= alpha[0];
+                zacc[gr][1] *= alpha[1];
+            }
+            l[0] *= alpha[0];
+            l[1] *= alpha[1];
+            ve = ve_new;
+        }
+        const float up = pow2_field(268 - ve);      // 2^14 over the power of two below the largest scale
+
+        // ---- P V
+#pragma unroll
+        for (int mt = 0; mt < 2; ++mt) {
+            float p[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                p[e] = exp2_approx(s[mt][e] - mu[e & 1]);
+            l[0] += p[0] + p[2];
+            l[1] += p[1] + p[3];
+            uint32_t v0[VW], v1[VW], v2[VW], v3[VW];
+            {
+                const int t0 = 16 * mt + tile_token(2 * tig), t1 = 16 * mt + tile_token(2 * tig + 1);
+                const int c0 = (gid ^ F::v_swizzle(t0)) * (R / 8), c1 = (gid ^ F::v_swizzle(t1)) * (R / 8);
+                const int c2 = (gid ^ F::v_swizzle(t0 + 8)) * (R / 8), c3 = (gid ^ F::v_swizzle(t1 + 8)) * (R / 8);
+                load_words(v0, h + F::kCodeV + t0 * R + c0);
+                load_words(v1, h + F::kCodeV + t1 * R + c1);
+                load_words(v2, h + F::kCodeV + (t0 + 8) * R + c2);
+                load_words(v3, h + F::kCodeV + (t1 + 8) * R + c3);
+            }
+            float pu[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                pu[e] = p[e] * up;
+#pragma unroll
+            for (int gr = 0; gr < NG; ++gr) {
+                const float sa = kv_scale(vp[mt][0][gr]), sb = kv_scale(vp[mt][1][gr]);
+                const float za = kv_zero(vp[mt][0][gr]), zb = kv_zero(vp[mt][1][gr]);
+                const uint32_t b0 = movmatrix(pack_half2(pu[0] * sa, pu[1] * sa));
+                const uint32_t b1 = movmatrix(pack_half2(pu[2] * sb, pu[3] * sb));
+                if (all_heads) {
+                    zacc[gr][0] = fmaf(p[0], za, fmaf(p[2], zb, zacc[gr][0]));
+                    zacc[gr][1] = fmaf(p[1], za, fmaf(p[3], zb, zacc[gr][1]));
+                } else {                            // a NaN of V stays out of heads that left the block out
+                    zacc[gr][0] = fmaf(p[0], act0 ? za : 0.f, fmaf(p[2], act0 ? zb : 0.f, zacc[gr][0]));
+                    zacc[gr][1] = fmaf(p[1], act1 ? za : 0.f, fmaf(p[3], act1 ? zb : 0.f, zacc[gr][1]));
+                }
+                if constexpr (BITS == 4) {
+                    const unsigned sel = gr & 1 ? 0x7632u : 0x5410u;
+                    uint32_t x01 = __byte_perm(v0[gr / 2], v1[gr / 2], sel), x23 = __byte_perm(v2[gr / 2], v3[gr / 2], sel);
+#pragma unroll
+                    for (int i = 0; i < UPG; ++i) {
+                        mma16816(acc[gr * UPG + i], x01 & 0x000F000Fu, x01 & 0x00F000F0u, x23 & 0x000F000Fu,
+                                 x23 & 0x00F000F0u, b0, b1);
+                        x01 >>= 8;
+                        x23 >>= 8;
+                    }
+                } else {
+#pragma unroll
+                    for (int i = 0; i < UPG; ++i) {
+                        const int w = 2 * gr + i / 2;
+                        const unsigned sel = i & 1 ? 0x7632u : 0x5410u;
+                        const uint32_t x01 = __byte_perm(v0[w], v1[w], sel), x23 = __byte_perm(v2[w], v3[w], sel);
+                        mma16816(acc[gr * UPG + i], __byte_perm(x01, 0u, 0x4240), __byte_perm(x01, 0u, 0x4341),
+                                 __byte_perm(x23, 0u, 0x4240), __byte_perm(x23, 0u, 0x4341), b0, b1);
+                    }
+                }
+            }
+        }
+        __syncwarp();
+        if (lane == 0)
+            issue(u + ST * W, st);
+    }
+
+    // ---- sums over the lanes that share a head, then over the warps
+#pragma unroll
+    for (int off = 4; off < 32; off <<= 1)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+            l[e] += __shfl_xor_sync(0xffffffffu, l[e], off);
+#pragma unroll
+            for (int gr = 0; gr < NG; ++gr)
+                zacc[gr][e] += __shfl_xor_sync(0xffffffffu, zacc[gr][e], off);
+        }
+    __syncwarp();
+    if (gid == 0) {
+        s_ml[warp][2 * tig] = make_float2(m[0], l[0]);
+        s_ml[warp][2 * tig + 1] = make_float2(m[1], l[1]);
+    }
+    float *so = reinterpret_cast<float *>(my);      // [kHeads][D], over this warp's ring
+    {
+        const float un = pow2_field(ve - 14);       // with 2^24 the inverse of `up` and the codes' unit
+#pragma unroll
+        for (int e = 0; e < 2; ++e)
+#pragma unroll
+            for (int gr = 0; gr < NG; ++gr)
+#pragma unroll
+                for (int i = 0; i < UPG; i += 2) {
+                    float4 r;
+                    r.x = acc[gr * UPG + i][e] * un * 16777216.f + zacc[gr][e];
+                    r.y = acc[gr * UPG + i][e + 2] * un * (BITS == 4 ? 1048576.f : 16777216.f) + zacc[gr][e];
+                    r.z = acc[gr * UPG + i + 1][e] * un * 16777216.f + zacc[gr][e];
+                    r.w = acc[gr * UPG + i + 1][e + 2] * un * (BITS == 4 ? 1048576.f : 16777216.f) + zacc[gr][e];
+                    *reinterpret_cast<float4 *>(so + (2 * tig + e) * D + F::G * gr + gid * (F::G / 8) + 2 * i) = r;
+                }
+    }
+    __syncthreads();
+    for (int i = threadIdx.x; i < gt * D; i += W * 32) {
+        const int hh = i / D, c = i % D;
+        float M = -INFINITY;
+#pragma unroll
+        for (int w = 0; w < W; ++w)
+            M = fmaxf(M, s_ml[w][hh].x);
+        const float Mu = M == -INFINITY ? 0.f : M;
+        float sum = 0.f, lt = 0.f;
+#pragma unroll
+        for (int w = 0; w < W; ++w) {
+            const float2 ml = s_ml[w][hh];
+            // a warp that saw only NaN has no maximum but a sum; one that saw nothing has neither
+            const float wt = ml.x == -INFINITY ? (ml.y == 0.f ? 0.f : ml.y) : exp2_approx(ml.x - Mu);
+            lt = fmaf(wt, ml.y, lt);
+            if (wt != 0.f)
+                sum = fmaf(wt, *reinterpret_cast<const float *>(ring + w * ST * F::HALF + i * 4), sum);
+        }
+        const long long bh = (long long)b * a.Hq + h0 + hh;
+        if (a.nsplit == 1) {
+            a.o[bh * D + c] = __float2bfloat16_rn(lt == 0.f ? 0.f : sum / lt);
+            if (c == 0 && a.lse != nullptr)
+                a.lse[bh] = lt == 0.f ? -INFINITY : (Mu + __log2f(lt)) * 0.69314718055994530942f;
+        } else {
+            float *out = a.part + (bh * a.nsplit + split) * (D + 2);
+            out[c] = sum;
+            if (c == 0) {
+                out[D] = M;
+                out[D + 1] = lt;
+            }
+        }
     }
 }
 
@@ -100,34 +587,96 @@ template <int D>
 __global__ void __launch_bounds__(D)
     decode_quant_merge_kernel(const float *part, int nsplit, __nv_bfloat16 *o, float *lse)
 {
+    __shared__ float s_w[kMaxDecodeSplits];
+    asm volatile("griddepcontrol.wait;" ::: "memory");
     const long long bh = blockIdx.x;
     const float *pp = part + bh * nsplit * (D + 2);
-    float M = -INFINITY;
-    for (int s = 0; s < nsplit; ++s)
-        M = fmaxf(M, pp[s * (D + 2) + D]);
-    const float mu = M == -INFINITY ? 0.f : M;
-    float l = 0.f, acc = 0.f;
-    for (int s = 0; s < nsplit; ++s) {
-        const float w = exp2_approx(pp[s * (D + 2) + D] - mu);
-        l = fmaf(w, pp[s * (D + 2) + D + 1], l);
-        acc = fmaf(w, pp[s * (D + 2) + threadIdx.x], acc);
+    const int lane = threadIdx.x & 31;
+    float ms[2], ls[2], M = -INFINITY;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        const int s = lane + 32 * i;
+        ms[i] = s < nsplit ? pp[s * (D + 2) + D] : -INFINITY;
+        ls[i] = s < nsplit ? pp[s * (D + 2) + D + 1] : 0.f;
+        M = fmaxf(M, ms[i]);
     }
+#pragma unroll
+    for (int off = 16; off >= 1; off >>= 1)
+        M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, off));
+    const float mu = M == -INFINITY ? 0.f : M;
+    float l = 0.f;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        const float w = ms[i] == -INFINITY ? (ls[i] == 0.f ? 0.f : ls[i]) : exp2_approx(ms[i] - mu);
+        l = fmaf(w, ls[i], l);
+        if (threadIdx.x < 32 && lane + 32 * i < nsplit)
+            s_w[lane + 32 * i] = w;
+    }
+#pragma unroll
+    for (int off = 16; off >= 1; off >>= 1)
+        l += __shfl_xor_sync(0xffffffffu, l, off);
+    __syncthreads();
+    float acc = 0.f;
+#pragma unroll 8
+    for (int s = 0; s < nsplit; ++s)
+        acc = fmaf(s_w[s], pp[s * (D + 2) + threadIdx.x], acc);
     o[bh * D + threadIdx.x] = __float2bfloat16_rn(l == 0.f ? 0.f : acc / l);
     if (lse != nullptr && threadIdx.x == 0)
         lse[bh] = l == 0.f ? -INFINITY : (mu + __log2f(l)) * 0.69314718055994530942f;
 }
 
-template <int BITS, int D>
-cudaError_t launch(int B, int Hq, int Hkv, int L, float scale_log2, const void *q_tok, const KvView &kv,
-                   const int32_t *lens, const uint8_t *mask, void *o, float *lse, float *part, int *status,
-                   cudaStream_t stream)
+// Splits of a unit (a KV head's head tile): the fewest whose grid fills 97 % of
+// its waves of one CTA per SM, else the best filling count; at least so many
+// that a split's block list fits.
+int decode_quant_splits(long long units, int nb, int sms)
 {
-    const int nb = num_blocks(L);
-    const int ns = decode_splits(B, Hq, nb);
-    decode_quant_kernel<BITS, D><<<dim3(ns, B * Hq), kQDT, 0, stream>>>(
-        static_cast<const __nv_bfloat16 *>(q_tok), kv, lens, mask, Hq, Hkv, L, nb, scale_log2, ns, part, status);
-    decode_quant_merge_kernel<D><<<B * Hq, D, 0, stream>>>(part, ns, static_cast<__nv_bfloat16 *>(o), lse);
-    return cudaGetLastError();
+    const int lo = (nb + kListMax - 2) / (kListMax - 1), cap = nb < kMaxDecodeSplits ? nb : kMaxDecodeSplits;
+    int best = lo;
+    double best_eff = -1.0;
+    for (int ns = lo; ns <= cap; ++ns) {
+        const long long ctas = units * ns, waves = (ctas + sms - 1) / sms;
+        const double eff = (double)ctas / (double)(waves * sms);
+        if (eff > best_eff) {
+            best_eff = eff;
+            best = ns;
+        }
+        if (eff >= 0.97)
+            break;
+    }
+    return best;
+}
+
+template <int BITS, int D>
+cudaError_t launch(DecodeArgs a, int B, cudaStream_t stream)
+{
+    using C = DecodeCfg<BITS, D>;
+    const int g = a.Hq / a.Hkv;
+    a.tiles = (g + kHeads - 1) / kHeads;
+    a.per_tile = (g + a.tiles - 1) / a.tiles;
+    int dev = 0, sms = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e == cudaSuccess)
+        e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+    if (e == cudaSuccess)
+        e = cudaFuncSetAttribute(decode_quant_kernel<BITS, D>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::ring);
+    if (e != cudaSuccess)
+        return e;
+    const int units = B * a.Hkv * a.tiles;
+    a.nsplit = decode_quant_splits(units, a.nb, sms);
+    decode_quant_kernel<BITS, D><<<dim3(a.nsplit, units), C::W * 32, C::ring, stream>>>(a);
+    e = cudaGetLastError();
+    if (e != cudaSuccess || a.nsplit == 1)
+        return e;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(B * a.Hq);
+    cfg.blockDim = dim3(D);
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];                    // the launch overlaps the first kernel; it waits for its end
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, decode_quant_merge_kernel<D>, (const float *)a.part, a.nsplit, a.o, a.lse);
 }
 
 } // namespace
@@ -136,14 +685,24 @@ cudaError_t launch_decode_quant(int bits, int B, int Hq, int Hkv, int L, int d, 
                                 const KvView &kv, const int32_t *lens, const uint8_t *mask, void *o, float *lse,
                                 float *part, int *status, uint64_t timeout_ns, cudaStream_t stream)
 {
-    (void)timeout_ns;
-    if (bits == 4 && d == 128)
-        return launch<4, 128>(B, Hq, Hkv, L, scale_log2, q_tok, kv, lens, mask, o, lse, part, status, stream);
+    DecodeArgs a{};
+    a.q_tok = static_cast<const __nv_bfloat16 *>(q_tok);
+    a.kv = kv;
+    a.lens = lens;
+    a.mask = mask;
+    a.Hq = Hq;
+    a.Hkv = Hkv;
+    a.L = L;
+    a.nb = num_blocks(L);
+    a.scale_log2 = scale_log2;
+    a.part = part;
+    a.o = static_cast<__nv_bfloat16 *>(o);
+    a.lse = lse;
+    a.status = status;
+    a.timeout_ns = timeout_ns;
     if (bits == 4)
-        return launch<4, 64>(B, Hq, Hkv, L, scale_log2, q_tok, kv, lens, mask, o, lse, part, status, stream);
-    if (d == 128)
-        return launch<8, 128>(B, Hq, Hkv, L, scale_log2, q_tok, kv, lens, mask, o, lse, part, status, stream);
-    return launch<8, 64>(B, Hq, Hkv, L, scale_log2, q_tok, kv, lens, mask, o, lse, part, status, stream);
+        return d == 128 ? launch<4, 128>(a, B, stream) : launch<4, 64>(a, B, stream);
+    return d == 128 ? launch<8, 128>(a, B, stream) : launch<8, 64>(a, B, stream);
 }
 
 } // namespace seer

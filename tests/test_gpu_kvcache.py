@@ -514,3 +514,20 @@ def test_two_streams_at_once():
         assert torch.equal(a, o) and torch.equal(b, lse)
     again = seer.seer_kv_read(cache, 64)
     assert torch.equal(raw[0], again[0]) and torch.equal(raw[1], again[1])
+
+
+def test_decode_wait_timeout_is_reported_and_recoverable():
+    """With the wait limit at 0 the first unfinished copy gives up: a status, no fault; the next call is exact.
+    The cache is long enough that every warp waits for some of its copies."""
+    cache, q, mask, o, lse = attend(4, 128, 2, 8, 2, 60000, 1.0, seed=41)
+    try:
+        seer.seer_set_wait_timeout_ns(0)
+        seer.seer_block_sparse_decode_quant(q.cuda(), cache, mask.cuda(), 60000)
+        with pytest.raises(seer.SeerError) as e:
+            seer.seer_check_status()
+        assert e.value.status == seer.SEER_ERR_TIMEOUT
+    finally:
+        seer.seer_set_wait_timeout_ns(2_000_000_000)
+    o2, l2 = seer.seer_block_sparse_decode_quant(q.cuda(), cache, mask.cuda(), 60000, return_lse=True)
+    seer.seer_check_status()
+    assert torch.equal(o, o2) and torch.equal(lse, l2)

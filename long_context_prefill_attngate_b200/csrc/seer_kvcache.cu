@@ -32,25 +32,72 @@ struct RowMap {
     static constexpr int NW = BITS / 4;                  // code words of a lane
 };
 
-// Row t of sequence b: the half record that holds it, and its token there; null
-// when the row is not to be touched (behind the count, or outside the cache).
+// A CTA has one page of one head, 64 positions of which the call's rows cover
+// [lo, hi): the page is looked up once and every row's address is an offset.
+// Rows at positions below 0 or past the cache are recorded and left out.
+struct PageRows {
+    uint8_t *record;             // null: nothing to do here
+    int lo, hi;                  // tokens of the page
+    int row0;                    // row of token 0 (may be negative)
+};
+
 template <class F>
-__device__ __forceinline__ uint8_t *locate(const KvView &kv, int Hkv, int b, int kvh, int t, int rows,
-                                           const int32_t *start, int start_pos, int *tok, int *status)
+__device__ __forceinline__ PageRows page_rows(const KvView &kv, int Hkv, int b, int kvh, int n, const int32_t *start,
+                                              const int32_t *count, int start_pos, int *status)
 {
-    if (t >= rows)
-        return nullptr;
-    const long long pos = (long long)(start != nullptr ? __ldg(start + b) : 0) + start_pos + t;
-    if (pos < 0 || pos >= 64LL * kv.max_blocks) {
+    PageRows r{nullptr, 0, 0, 0};
+    const int rows = count != nullptr ? min(__ldg(count + b), n) : n;
+    const long long first = (long long)(start != nullptr ? __ldg(start + b) : 0) + start_pos;
+    if (rows <= 0)
+        return r;
+    // beyond +- 2^22 no row of at most 2^20 meets a cache of at most 2^20 tokens
+    const int base = (int)max(-(1LL << 22), min(1LL << 22, first));
+    const int j = max(base, 0) / 64 + (int)blockIdx.x;
+    if (base < 0 && blockIdx.x == 0)
         set_status(status, kStatusPage);
-        return nullptr;
+    r.row0 = 64 * j - base;
+    r.lo = max(0, -r.row0);
+    r.hi = min(64, rows - r.row0);
+    if (r.lo >= r.hi)
+        return r;
+    if (j >= kv.max_blocks) {
+        set_status(status, kStatusPage);
+        return r;
     }
-    const int page = kv_page(kv, b, (int)(pos / 64), status);
-    if (page < 0)
-        return nullptr;
-    *tok = (int)(pos % 32);
-    return kv_half<F>(kv, Hkv, page, kvh, (int)(pos % 64) / 32);
+    const int page = kv_page(kv, b, j, status);
+    if (page >= 0)
+        r.record = kv_half<F>(kv, Hkv, page, kvh, 0);
+    return r;
 }
+
+__device__ __forceinline__ float2 add2(float2 a, float2 b)
+{
+    float2 d;
+    asm("{\n\t.reg .b64 ra, rb, rd;\n\tmov.b64 ra, {%2, %3};\n\tmov.b64 rb, {%4, %5};\n\t"
+        "add.rn.f32x2 rd, ra, rb;\n\tmov.b64 {%0, %1}, rd;\n\t}"
+        : "=f"(d.x), "=f"(d.y)
+        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+    return d;
+}
+__device__ __forceinline__ float2 mul2(float2 a, float2 b)
+{
+    float2 d;
+    asm("{\n\t.reg .b64 ra, rb, rd;\n\tmov.b64 ra, {%2, %3};\n\tmov.b64 rb, {%4, %5};\n\t"
+        "mul.rn.f32x2 rd, ra, rb;\n\tmov.b64 {%0, %1}, rd;\n\t}"
+        : "=f"(d.x), "=f"(d.y)
+        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+    return d;
+}
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c)
+{
+    float2 d;
+    asm("{\n\t.reg .b64 ra, rb, rc, rd;\n\tmov.b64 ra, {%2, %3};\n\tmov.b64 rb, {%4, %5};\n\tmov.b64 rc, {%6, %7};\n\t"
+        "fma.rn.f32x2 rd, ra, rb, rc;\n\tmov.b64 {%0, %1}, rd;\n\t}"
+        : "=f"(d.x), "=f"(d.y)
+        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+    return d;
+}
+__device__ __forceinline__ float2 both(float x) { return make_float2(x, x); }
 
 // The code words of a V row change lanes between element order (lane c: the
 // words of elements 8c .. 8c+7) and the order they lie in (lane c: four bytes
@@ -118,188 +165,185 @@ __device__ __forceinline__ uint2 k8_from_store(uint2 w, int lane)
     return j & 1 ? make_uint2(y0, y1) : make_uint2(x0, x1);
 }
 
-// U rows per lane, their loads in flight together.
-template <int BITS, int D, int U>
+// The code words and the param of eight elements.  t / s is divided as IEEE
+// division would (quotient by the reciprocal, then one step with the exact
+// remainder), which puts a half where it is one: bf16 differences and an 8-bit s
+// keep every other quotient further from a half than 2^-24 of it.
+template <int BITS, int D>
+__device__ __forceinline__ uint32_t quantise8(const uint4 in, uint32_t (&code)[BITS / 4])
+{
+    using F = KvFmt<BITS, D>;
+    constexpr int GL = RowMap<BITS, D>::GL;
+    const uint32_t w[4] = {in.x, in.y, in.z, in.w};
+    __nv_bfloat162 p[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        p[i] = *reinterpret_cast<const __nv_bfloat162 *>(&w[i]);
+    __nv_bfloat162 mn = __hmin2_nan(__hmin2_nan(p[0], p[1]), __hmin2_nan(p[2], p[3]));
+    __nv_bfloat162 mx = __hmax2_nan(__hmax2_nan(p[0], p[1]), __hmax2_nan(p[2], p[3]));
+#pragma unroll
+    for (int off = 1; off < GL; off <<= 1) {
+        mn = __hmin2_nan(mn, __shfl_xor_sync(0xffffffffu, mn, off));
+        mx = __hmax2_nan(mx, __shfl_xor_sync(0xffffffffu, mx, off));
+    }
+    const __nv_bfloat16 lob = __hmin_nan(mn.x, mn.y), hib = __hmax_nan(mx.x, mx.y);
+    const float lo = __bfloat162float(lob), hi = __bfloat162float(hib);
+    const bool ok = lo > -8.507059173023462e37f && hi < 8.507059173023462e37f;   // 2^126; false for a NaN
+    __nv_bfloat16 sb = __float2bfloat16_rn(__fdiv_rn(hi - lo, (float)F::TOP));
+    if (!ok || __bfloat162float(sb) < 7.888609052210118e-31f)                   // 2^-100
+        sb = __float2bfloat16_rn(0.f);
+    const float s = __bfloat162float(sb);
+    const float inv = s > 0.f ? __fdividef(1.f, s) : 0.f;
+    const float zr = ok ? lo : 0.f;
+    constexpr uint32_t kMagic = 0x4B400000u;             // 1.5 2^23: adding it leaves the integer in the low bits
+    uint32_t acc[BITS / 4] = {};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const float2 v = make_float2(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xFFFF0000u));
+        const float2 t = add2(v, both(-zr));
+        float2 q = mul2(t, both(inv));
+        q = fma2(fma2(q, both(-s), t), both(inv), q);
+        if (BITS == 8)                                   // s may be up to 2^-8 below the range / 255, not so at 15
+            q = make_float2(fminf(q.x, (float)F::TOP), fminf(q.y, (float)F::TOP));
+        const float2 m = add2(q, both(__uint_as_float(kMagic)));
+        constexpr int per = 32 / BITS;
+        acc[2 * i / per] += __float_as_uint(m.x) * (1u << (2 * i % per * BITS));
+        acc[(2 * i + 1) / per] += __float_as_uint(m.y) * (1u << ((2 * i + 1) % per * BITS));
+    }
+    // the sums carry kMagic times 1 + 2^BITS + ...
+    constexpr uint32_t bias = kMagic * (BITS == 4 ? 0x11111111u : 0x01010101u);
+#pragma unroll
+    for (int i = 0; i < BITS / 4; ++i)
+        code[i] = s > 0.f ? acc[i] - bias : 0u;
+    return (uint32_t)__bfloat16_as_ushort(sb) | (ok ? (uint32_t)__bfloat16_as_ushort(lob) : 0x7FC0u) << 16;
+}
+
+template <int BITS, int D>
 __global__ void __launch_bounds__(kRowThreads) kv_write_kernel(KvView kv, KvRows x, int Hkv, int n, const int32_t *start,
                                                                const int32_t *count, int start_pos, int *status)
 {
     using F = KvFmt<BITS, D>;
     using M = RowMap<BITS, D>;
+    constexpr int NI = 64 / (kRowThreads / 32 * M::RPW);  // accesses of a lane for each of K and V
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, c = lane % M::CH;
     const int b = blockIdx.y / Hkv, kvh = blockIdx.y % Hkv;
-    const bool is_v = blockIdx.z != 0;
-    const int rows = count != nullptr ? min(__ldg(count + b), n) : n;
-    const int t0 = (int)blockIdx.x * (kRowThreads / 32 * M::RPW * U) + warp * (M::RPW * U) + lane / M::CH;
-    const __nv_bfloat16 *src = static_cast<const __nv_bfloat16 *>(is_v ? x.v : x.k) +
-                               (is_v ? b * x.v_stride_b + kvh * x.v_stride_h : b * x.k_stride_b + kvh * x.k_stride_h) + 8 * c;
-    const long long st = is_v ? x.v_stride_t : x.k_stride_t;
-    if (t0 - lane / M::CH >= rows)
-        return;                                          // the whole warp
-    uint4 in[U];
+    const PageRows r = page_rows<F>(kv, Hkv, b, kvh, n, start, count, start_pos, status);
+    if (r.record == nullptr)
+        return;
+    const __nv_bfloat16 *src[2] = {
+        static_cast<const __nv_bfloat16 *>(x.k) + b * x.k_stride_b + kvh * x.k_stride_h + r.row0 * x.k_stride_t + 8 * c,
+        static_cast<const __nv_bfloat16 *>(x.v) + b * x.v_stride_b + kvh * x.v_stride_h + r.row0 * x.v_stride_t + 8 * c};
+    uint4 in[2][NI];
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-        const int t = t0 + u * M::RPW;
-        in[u] = t < rows ? __ldg(reinterpret_cast<const uint4 *>(src + t * st)) : make_uint4(0u, 0u, 0u, 0u);
-    }
+    for (int is_v = 0; is_v < 2; ++is_v)
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-        const uint32_t w[4] = {in[u].x, in[u].y, in[u].z, in[u].w};
-        __nv_bfloat162 p[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-            p[i] = *reinterpret_cast<const __nv_bfloat162 *>(&w[i]);
-        __nv_bfloat162 mn = __hmin2_nan(__hmin2_nan(p[0], p[1]), __hmin2_nan(p[2], p[3]));
-        __nv_bfloat162 mx = __hmax2_nan(__hmax2_nan(p[0], p[1]), __hmax2_nan(p[2], p[3]));
-#pragma unroll
-        for (int off = 1; off < M::GL; off <<= 1) {
-            mn = __hmin2_nan(mn, __shfl_xor_sync(0xffffffffu, mn, off));
-            mx = __hmax2_nan(mx, __shfl_xor_sync(0xffffffffu, mx, off));
+        for (int i = 0; i < NI; ++i) {
+            const int t = (i * (kRowThreads / 32) + warp) * M::RPW + lane / M::CH;
+            in[is_v][i] = make_uint4(0u, 0u, 0u, 0u);
+            if (t >= r.lo && t < r.hi)
+                in[is_v][i] = __ldg(reinterpret_cast<const uint4 *>(src[is_v] + t * (is_v ? x.v_stride_t : x.k_stride_t)));
         }
-        const __nv_bfloat16 lob = __hmin_nan(mn.x, mn.y), hib = __hmax_nan(mx.x, mx.y);
-        const float lo = __bfloat162float(lob), hi = __bfloat162float(hib);
-        const bool ok = lo > -8.507059173023462e37f && hi < 8.507059173023462e37f;   // 2^126; false for a NaN
-        __nv_bfloat16 sb = __float2bfloat16_rn(__fdiv_rn(hi - lo, (float)F::TOP));
-        if (!ok || __bfloat162float(sb) < 7.888609052210118e-31f)                   // 2^-100
-            sb = __float2bfloat16_rn(0.f);
-        const float s = __bfloat162float(sb), inv = s > 0.f ? __fdividef(1.f, s) : 0.f;
-        const float zr = ok ? lo : 0.f;
-        // n: t / s rounded by an addition, then checked against the exact remainder
-        // t - n s (a few bits of bf16 products): where the reciprocal's error put
-        // it on the wrong side of a half, or at a half on the odd side, it moves by one
-        constexpr float kMagic = 12582912.f;             // 1.5 2^23
-        float q[8], worst = 0.f;
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            const float v = __uint_as_float(e & 1 ? w[e / 2] & 0xFFFF0000u : w[e / 2] << 16);
-            const float d = v - zr;
-            q[e] = fmaf(d, inv, kMagic) - kMagic;
-            worst = fmaxf(worst, fabsf(fmaf(-q[e], s, d)));
-        }
-        if (2.f * worst >= s) {
+    for (int is_v = 0; is_v < 2; ++is_v)
 #pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                const float v = __uint_as_float(e & 1 ? w[e / 2] & 0xFFFF0000u : w[e / 2] << 16);
-                const float r = 2.f * fmaf(-q[e], s, v - zr);
-                const bool odd = ((int)q[e] & 1) != 0;
-                q[e] += r > s || (r == s && odd) ? 1.f : -r > s || (-r == s && odd) ? -1.f : 0.f;
+        for (int i = 0; i < NI; ++i) {
+            const int tw = (i * (kRowThreads / 32) + warp) * M::RPW, t = tw + lane / M::CH;
+            if (tw + M::RPW <= r.lo || tw >= r.hi)
+                continue;                                // the whole warp
+            uint32_t code[M::NW];
+            const uint32_t par = quantise8<BITS, D>(in[is_v][i], code);
+            const int tok = t % 32;
+            uint8_t *half = r.record + t / 32 * F::HALF, *base = half + (is_v ? F::kCodeV : 0);
+            const bool mine = t >= r.lo && t < r.hi;
+            if constexpr (BITS == 4) {
+                const uint32_t out = is_v ? v4_exchange<D>(code[0], lane, true) : code[0];
+                if (mine)
+                    *reinterpret_cast<uint32_t *>(base + (is_v ? v_place<4, D>(tok, c) : F::k_off(tok, 4 * c))) = out;
+            } else {
+                uint2 out = make_uint2(code[0], code[1]);
+                if (!is_v)
+                    out = k8_to_store<D>(out, lane);
+                if (mine)
+                    *reinterpret_cast<uint2 *>(base + (is_v ? v_place<8, D>(tok, c) : k8_place<D>(tok, c))) = out;
             }
+            if (mine && c % M::GL == 0)
+                *reinterpret_cast<uint32_t *>(half + (is_v ? F::kParV : F::kParK) + tok * F::PAR + c / M::GL * 4) = par;
         }
-        uint32_t code[M::NW] = {};
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            const uint32_t n_e = s > 0.f ? __float_as_uint(fminf(q[e], (float)F::TOP) + kMagic) & (uint32_t)F::TOP : 0u;
-            code[e * BITS / 32] |= n_e << (e * BITS % 32);
-        }
-        const int t = t0 + u * M::RPW;
-        int tok = 0;
-        uint8_t *half = locate<F>(kv, Hkv, b, kvh, t, rows, start, start_pos, &tok, status);
-        uint8_t *base = half + (is_v ? F::kCodeV : 0);
-        if constexpr (BITS == 4) {
-            const uint32_t out = is_v ? v4_exchange<D>(code[0], lane, true) : code[0];
-            if (half != nullptr)
-                *reinterpret_cast<uint32_t *>(base + (is_v ? v_place<4, D>(tok, c) : F::k_off(tok, 4 * c))) = out;
-        } else {
-            uint2 out = make_uint2(code[0], code[1]);
-            if (!is_v)
-                out = k8_to_store<D>(out, lane);
-            if (half != nullptr)
-                *reinterpret_cast<uint2 *>(base + (is_v ? v_place<8, D>(tok, c) : k8_place<D>(tok, c))) = out;
-        }
-        if (half != nullptr && c % M::GL == 0)
-            *reinterpret_cast<uint32_t *>(half + (is_v ? F::kParV : F::kParK) + tok * F::PAR + c / M::GL * 4) =
-                (uint32_t)__bfloat16_as_ushort(sb) | (ok ? (uint32_t)__bfloat16_as_ushort(lob) : 0x7FC0u) << 16;
-    }
 }
 
-template <int BITS, int D, int U>
+template <int BITS, int D>
 __global__ void __launch_bounds__(kRowThreads) kv_read_kernel(KvView kv, int Hkv, int n, const int32_t *start,
                                                               const int32_t *count, int start_pos,
                                                               __nv_bfloat16 *k, __nv_bfloat16 *v, int *status)
 {
     using F = KvFmt<BITS, D>;
     using M = RowMap<BITS, D>;
+    constexpr int NI = 64 / (kRowThreads / 32 * M::RPW);
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, c = lane % M::CH;
     const int b = blockIdx.y / Hkv, kvh = blockIdx.y % Hkv;
-    const bool is_v = k == nullptr || blockIdx.z != 0;
-    const int rows = count != nullptr ? min(__ldg(count + b), n) : n;
-    const int t0 = (int)blockIdx.x * (kRowThreads / 32 * M::RPW * U) + warp * (M::RPW * U) + lane / M::CH;
-    if (t0 - lane / M::CH >= rows)
-        return;                                          // the whole warp
-    uint32_t code[U][M::NW], par[U];
-    bool have[U];
+    const PageRows r = page_rows<F>(kv, Hkv, b, kvh, n, start, count, start_pos, status);
+    if (r.record == nullptr)
+        return;
+    uint32_t code[2][NI][M::NW], par[2][NI];
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-        int tok = 0;
-        const uint8_t *half = locate<F>(kv, Hkv, b, kvh, t0 + u * M::RPW, rows, start, start_pos, &tok, status);
-        have[u] = half != nullptr;
-        code[u][0] = code[u][M::NW - 1] = par[u] = 0u;
-        if (have[u]) {
-            const uint8_t *base = half + (is_v ? F::kCodeV : 0);
+    for (int is_v = 0; is_v < 2; ++is_v)
+#pragma unroll
+        for (int i = 0; i < NI; ++i) {
+            const int t = (i * (kRowThreads / 32) + warp) * M::RPW + lane / M::CH, tok = t % 32;
+            code[is_v][i][0] = code[is_v][i][M::NW - 1] = par[is_v][i] = 0u;
+            if (t < r.lo || t >= r.hi || (is_v ? v : k) == nullptr)
+                continue;
+            const uint8_t *half = r.record + t / 32 * F::HALF, *base = half + (is_v ? F::kCodeV : 0);
             if constexpr (BITS == 4) {
-                code[u][0] = *reinterpret_cast<const uint32_t *>(base + (is_v ? v_place<4, D>(tok, c) : F::k_off(tok, 4 * c)));
+                code[is_v][i][0] =
+                    *reinterpret_cast<const uint32_t *>(base + (is_v ? v_place<4, D>(tok, c) : F::k_off(tok, 4 * c)));
             } else {
-                const uint2 w = *reinterpret_cast<const uint2 *>(base + (is_v ? v_place<8, D>(tok, c) : k8_place<D>(tok, c)));
-                code[u][0] = w.x;
-                code[u][M::NW - 1] = w.y;
+                const uint2 w =
+                    *reinterpret_cast<const uint2 *>(base + (is_v ? v_place<8, D>(tok, c) : k8_place<D>(tok, c)));
+                code[is_v][i][0] = w.x;
+                code[is_v][i][M::NW - 1] = w.y;
             }
-            par[u] = *reinterpret_cast<const uint32_t *>(half + (is_v ? F::kParV : F::kParK) + tok * F::PAR + c / M::GL * 4);
+            par[is_v][i] =
+                *reinterpret_cast<const uint32_t *>(half + (is_v ? F::kParV : F::kParK) + tok * F::PAR + c / M::GL * 4);
+        }
+#pragma unroll
+    for (int is_v = 0; is_v < 2; ++is_v) {
+        __nv_bfloat16 *out = (is_v ? v : k) + ((long long)blockIdx.y * n + r.row0) * D + 8 * c;
+#pragma unroll
+        for (int i = 0; i < NI; ++i) {
+            const int tw = (i * (kRowThreads / 32) + warp) * M::RPW, t = tw + lane / M::CH;
+            if (tw + M::RPW <= r.lo || tw >= r.hi || (is_v ? v : k) == nullptr)
+                continue;                                // the whole warp
+            uint32_t(&w)[M::NW] = code[is_v][i];
+            if constexpr (BITS == 4) {
+                if (is_v)
+                    w[0] = v4_exchange<D>(w[0], lane, false);
+            } else if (!is_v) {
+                const uint2 x = k8_from_store<D>(make_uint2(w[0], w[1]), lane);
+                w[0] = x.x;
+                w[M::NW - 1] = x.y;
+            }
+            const float s = kv_scale(par[is_v][i]), z = kv_zero(par[is_v][i]);
+            uint32_t o[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                constexpr int per = 32 / BITS;
+                const uint32_t q0 = w[2 * e / per] >> (2 * e % per * BITS), q1 = w[(2 * e + 1) / per] >> ((2 * e + 1) % per * BITS);
+                // the code as a float: 2^23 + n, less 2^23
+                float2 f = make_float2(__uint_as_float((q0 & (uint32_t)F::TOP) | 0x4B000000u),
+                                       __uint_as_float((q1 & (uint32_t)F::TOP) | 0x4B000000u));
+                f = fma2(add2(f, both(-8388608.f)), both(s), both(z));
+                const __nv_bfloat162 h = __floats2bfloat162_rn(f.x, f.y);
+                o[e] = *reinterpret_cast<const uint32_t *>(&h);
+            }
+            if (t >= r.lo && t < r.hi)
+                *reinterpret_cast<uint4 *>(out + (long long)t * D) = make_uint4(o[0], o[1], o[2], o[3]);
         }
     }
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-        if constexpr (BITS == 4) {
-            if (is_v)
-                code[u][0] = v4_exchange<D>(code[u][0], lane, false);
-        } else if (!is_v) {
-            const uint2 w = k8_from_store<D>(make_uint2(code[u][0], code[u][1]), lane);
-            code[u][0] = w.x;
-            code[u][M::NW - 1] = w.y;
-        }
-        const float s = kv_scale(par[u]), z = kv_zero(par[u]);
-        uint4 r;
-        uint32_t *rw = &r.x;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            float f[2];
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-                const uint32_t q = code[u][(2 * i + e) * BITS / 32] >> ((2 * i + e) * BITS % 32) & (uint32_t)F::TOP;
-                f[e] = fmaf(s, __uint_as_float(q | 0x4B000000u) - 8388608.f, z);    // q as a float: 2^23 + q, less 2^23
-            }
-            const __nv_bfloat162 h = __floats2bfloat162_rn(f[0], f[1]);
-            rw[i] = *reinterpret_cast<const uint32_t *>(&h);
-        }
-        if (have[u])
-            *reinterpret_cast<uint4 *>((is_v ? v : k) + ((long long)blockIdx.y * n + t0 + u * M::RPW) * D + 8 * c) = r;
-    }
 }
 
-// Rows per lane: four where that still leaves two CTAs an SM, else one.
-bool four_rows(int B, int Hkv, int n, int d)
-{
-    return (long long)B * Hkv * n * 2 >= 4LL * 296 * (kRowThreads / (d / 8));
-}
-
-template <int BITS, int D, int U>
-cudaError_t write_rows(int B, int Hkv, int n, const KvView &kv, const KvRows &x, const int32_t *start,
-                       const int32_t *count, int start_pos, int *status, cudaStream_t stream)
-{
-    const int per = kRowThreads / (D / 8) * U;
-    kv_write_kernel<BITS, D, U><<<dim3((n + per - 1) / per, B * Hkv, 2), kRowThreads, 0, stream>>>(
-        kv, x, Hkv, n, start, count, start_pos, status);
-    return cudaGetLastError();
-}
-
-template <int BITS, int D, int U>
-cudaError_t read_rows(int B, int Hkv, int n, const KvView &kv, const int32_t *start, const int32_t *count, int start_pos,
-                      void *k, void *v, int *status, cudaStream_t stream)
-{
-    const int per = kRowThreads / (D / 8) * U;
-    kv_read_kernel<BITS, D, U>
-        <<<dim3((n + per - 1) / per, B * Hkv, k != nullptr && v != nullptr ? 2 : 1), kRowThreads, 0, stream>>>(
-            kv, Hkv, n, start, count, start_pos, static_cast<__nv_bfloat16 *>(k), static_cast<__nv_bfloat16 *>(v), status);
-    return cudaGetLastError();
-}
+// Pages that n rows can touch: one more than they fill, since they may start anywhere.
+unsigned pages_of(int n) { return (unsigned)(n - 1) / 64 + 2; }
 
 } // namespace
 
@@ -315,23 +359,21 @@ int kv_record_bytes(int bits, int d)
 cudaError_t launch_kv_write(int bits, int B, int Hkv, int n, int d, const KvView &kv, const KvRows &x,
                             const int32_t *start, const int32_t *count, int start_pos, int *status, cudaStream_t stream)
 {
-    const bool four = four_rows(B, Hkv, n, d);
-    auto f = bits == 4 ? (d == 128 ? (four ? write_rows<4, 128, 4> : write_rows<4, 128, 1>)
-                                   : (four ? write_rows<4, 64, 4> : write_rows<4, 64, 1>))
-                       : (d == 128 ? (four ? write_rows<8, 128, 4> : write_rows<8, 128, 1>)
-                                   : (four ? write_rows<8, 64, 4> : write_rows<8, 64, 1>));
-    return f(B, Hkv, n, kv, x, start, count, start_pos, status, stream);
+    const auto f = bits == 4 ? (d == 128 ? kv_write_kernel<4, 128> : kv_write_kernel<4, 64>)
+                             : (d == 128 ? kv_write_kernel<8, 128> : kv_write_kernel<8, 64>);
+    f<<<dim3(pages_of(n), B * Hkv), kRowThreads, 0, stream>>>(kv, x, Hkv, n, start, count, start_pos, status);
+    return cudaGetLastError();
 }
 
 cudaError_t launch_kv_read(int bits, int B, int Hkv, int n, int d, const KvView &kv, const int32_t *start,
                            const int32_t *count, int start_pos, void *k, void *v, int *status, cudaStream_t stream)
 {
-    const bool four = four_rows(B, Hkv, n, d);
-    auto f = bits == 4 ? (d == 128 ? (four ? read_rows<4, 128, 4> : read_rows<4, 128, 1>)
-                                   : (four ? read_rows<4, 64, 4> : read_rows<4, 64, 1>))
-                       : (d == 128 ? (four ? read_rows<8, 128, 4> : read_rows<8, 128, 1>)
-                                   : (four ? read_rows<8, 64, 4> : read_rows<8, 64, 1>));
-    return f(B, Hkv, n, kv, start, count, start_pos, k, v, status, stream);
+    const auto f = bits == 4 ? (d == 128 ? kv_read_kernel<4, 128> : kv_read_kernel<4, 64>)
+                             : (d == 128 ? kv_read_kernel<8, 128> : kv_read_kernel<8, 64>);
+    f<<<dim3(pages_of(n), B * Hkv), kRowThreads, 0, stream>>>(kv, Hkv, n, start, count, start_pos,
+                                                              static_cast<__nv_bfloat16 *>(k),
+                                                              static_cast<__nv_bfloat16 *>(v), status);
+    return cudaGetLastError();
 }
 
 } // namespace seer

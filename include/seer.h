@@ -115,8 +115,7 @@ enum {
     SEER_CALL_BLOCK_SPARSE_DECODE = 4,
     SEER_CALL_GATE_KEY_CACHE = 5,
     SEER_CALL_DECODE_GATE_CACHED = 6,
-    SEER_CALL_GATE_KEY_CACHE_QUANT = 8,
-    SEER_CALL_BLOCK_SPARSE_DECODE_QUANT = 9
+    SEER_CALL_BLOCK_SPARSE_DECODE_QUANT = 8
 };
 
 /*
@@ -415,13 +414,11 @@ SEER_API seer_status seer_kv_read(const seer_shape *shape, const seer_kv_cache *
  * gate's key rows of blocks first_block .. nb-1, nb = ceil(shape->S / 64) <=
  * max_blocks.  lens: DEVICE int32 [B], the tokens of each sequence (clamped to
  * 0 .. S), or NULL for S; a block pools its tokens below that length, and the
- * key row of a block without one is 0.  kt, wk, params: as there.  Workspace:
- * seer_workspace_bytes(SEER_CALL_GATE_KEY_CACHE_QUANT), 256-B aligned.
+ * key row of a block without one is 0.  kt, wk, params: as there.  No workspace.
  */
 SEER_API seer_status seer_gate_key_cache_quant(const seer_shape *shape, const seer_kv_cache *cache,
                                                const int32_t *lens, const void *wk, const seer_gate_params *gp,
-                                               int first_block, float *kt, void *workspace, size_t ws_bytes,
-                                               void *stream);
+                                               int first_block, float *kt, void *stream);
 
 /*
  * seer_block_sparse_decode_quant — seer_block_sparse_decode on the quantised

@@ -21,7 +21,7 @@ from ._binding import (  # noqa: F401
 )
 
 from ._binding import (  # noqa: F401,E402
-    SEER_CALL_BLOCK_SPARSE_DECODE_QUANT, SEER_CALL_GATE_KEY_CACHE_QUANT, seer_kv_cache, seer_kv_rows,
+    SEER_CALL_BLOCK_SPARSE_DECODE_QUANT, seer_kv_cache, seer_kv_rows,
 )
 from .kvcache import (  # noqa: F401,E402
     SeerKVCache, seer_block_sparse_decode_quant, seer_gate_key_cache_quant, seer_kv_read, seer_kv_record_bytes,

@@ -33,8 +33,7 @@ SEER_CALL_DECODE_GATE_SCORES = 3
 SEER_CALL_BLOCK_SPARSE_DECODE = 4
 SEER_CALL_GATE_KEY_CACHE = 5
 SEER_CALL_DECODE_GATE_CACHED = 6
-SEER_CALL_GATE_KEY_CACHE_QUANT = 8
-SEER_CALL_BLOCK_SPARSE_DECODE_QUANT = 9
+SEER_CALL_BLOCK_SPARSE_DECODE_QUANT = 8
 
 BLOCK = 64
 
@@ -118,7 +117,7 @@ def lib() -> ctypes.CDLL:
             CP = ctypes.POINTER(seer_kv_cache)
             L.seer_kv_write.argtypes = [SP, CP, ctypes.POINTER(seer_kv_rows), P, P, I, P]
             L.seer_kv_read.argtypes = [SP, CP, P, P, I, P, P, P]
-            L.seer_gate_key_cache_quant.argtypes = [SP, CP, P, P, ctypes.POINTER(seer_gate_params), I, P, P, Z, P]
+            L.seer_gate_key_cache_quant.argtypes = [SP, CP, P, P, ctypes.POINTER(seer_gate_params), I, P, P]
             L.seer_block_sparse_decode_quant.argtypes = [SP, P, CP, P, P, F, P, P, P, Z, P]
             L.seer_kv_record_bytes.argtypes = [I, I]
             L.seer_kv_record_bytes.restype = Z

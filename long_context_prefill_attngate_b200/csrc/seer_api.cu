@@ -225,8 +225,6 @@ size_t seer_workspace_bytes(int which_call, const seer_shape *shape)
     case SEER_CALL_DECODE_GATE_CACHED:
         return ((sizeof(float) * (size_t)shape->B * shape->Hq * shape->d + 255) & ~size_t(255)) +
                ((sizeof(float) * (size_t)shape->B * shape->Hq * 256 + 255) & ~size_t(255));
-    case SEER_CALL_GATE_KEY_CACHE_QUANT:
-        return gate_key_ws_bytes(shape->B, shape->Hkv, shape->S, shape->d, true);
     case SEER_CALL_BLOCK_SPARSE_DECODE:
     case SEER_CALL_BLOCK_SPARSE_DECODE_QUANT:
         return sizeof(float) * (size_t)shape->B * shape->Hq * kMaxDecodeSplits * (shape->d + 2);
@@ -238,7 +236,7 @@ size_t seer_workspace_bytes(int which_call, const seer_shape *shape)
 
 // Argument checks shared by the prefill and decode gates.
 // need_kind: 0 = the prefill gate's workspace, 1 = the decode gate's, 2 = the
-// key-cache call's, 3 = the cached decode row's.
+// key-cache call's, 3 = the cached decode row's, 4 = none.
 static seer_status check_gate_args(const char *name, const seer_shape *shape, const void *q, const void *k,
                                    const void *wq, const void *wk, const seer_gate_params *gp, const float *scores,
                                    void *workspace, size_t ws_bytes, int need_kind = 0)
@@ -264,6 +262,8 @@ static seer_status check_gate_args(const char *name, const seer_shape *shape, co
     if (gate_projection_smem(maxmin ? 2 * shape->d : shape->d, gp->d_gate) > 227 * 1024)
         return fail(SEER_ERR_UNSUPPORTED, "d_gate %d too large for %s K pooling at d = %d", gp->d_gate,
                     maxmin ? "max+min" : "average", shape->d);
+    if (need_kind == 4)
+        return SEER_OK;
     size_t need = gate_workspace_bytes(shape->B, shape->Hq, shape->Hkv, shape->S, shape->d, gp->d_gate, maxmin);
     if (need_kind == 1)
         need = decode_gate_ws_bytes(shape->B, shape->Hq, shape->Hkv, shape->S, shape->d, gp->d_gate, maxmin);
@@ -702,14 +702,14 @@ seer_status seer_kv_read(const seer_shape *shape, const seer_kv_cache *cache, co
 
 seer_status seer_gate_key_cache_quant(const seer_shape *shape, const seer_kv_cache *cache, const int32_t *lens,
                                       const void *wk, const seer_gate_params *gp, int first_block, float *kt,
-                                      void *workspace, size_t ws_bytes, void *stream)
+                                      void *stream)
 {
     seer_status st = check_cache("seer_gate_key_cache_quant", shape, cache);
     if (st != SEER_OK)
         return st;
     // the q, k and wq checks of the shared helper are satisfied with the pages and wk
-    st = check_gate_args("seer_gate_key_cache_quant", shape, cache->pages, cache->pages, wk, wk, gp, kt, workspace,
-                         ws_bytes, 2);
+    st = check_gate_args("seer_gate_key_cache_quant", shape, cache->pages, cache->pages, wk, wk, gp, kt, nullptr, 0,
+                         4);
     if (st != SEER_OK)
         return st;
     st = check_cached_length("seer_gate_key_cache_quant", shape, cache);
@@ -722,8 +722,8 @@ seer_status seer_gate_key_cache_quant(const seer_shape *shape, const seer_kv_cac
         return fail(SEER_ERR_CUDA, "cannot resolve the device status word");
     const cudaError_t e = launch_gate_keys_quant(
         cache->bits, shape->B, shape->Hkv, shape->S, shape->d, gp->d_gate, gp->rope_theta,
-        gp->k_pooling == SEER_KPOOL_MAXMIN, view_of(cache), lens, wk, gp->wk_head_stride, first_block, kt, workspace,
-        status, static_cast<cudaStream_t>(stream));
+        gp->k_pooling == SEER_KPOOL_MAXMIN, view_of(cache), lens, wk, gp->wk_head_stride, first_block, kt, status,
+        static_cast<cudaStream_t>(stream));
     if (e != cudaSuccess)
         return cuda_fail(e, "seer_gate_key_cache_quant launch");
     return ok();

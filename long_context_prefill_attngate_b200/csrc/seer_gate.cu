@@ -842,24 +842,6 @@ cudaError_t launch_gate(int B, int Hq, int Hkv, int S, int d, int dg, float thet
 
 namespace seer {
 
-// The key rows of blocks first_block .. nb-1 from their pooled rows kp
-// [B*Hkv, nb, dk]: projected and rotated into kt [B*Hkv, nb, dg].
-cudaError_t launch_project_keys(int B, int Hkv, int nb, int dk, int dg, float theta, const float *kp, const void *wk,
-                                long long wk_stride, int first_block, float *kt, cudaStream_t stream)
-{
-    const int nsel = nb - first_block;
-    const size_t psmem = gate_projection_smem(dk, dg);
-    const cudaError_t e =
-        cudaFuncSetAttribute(project_rope_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)psmem);
-    if (e != cudaSuccess)
-        return e;
-    const ProjJob jk{kp + (size_t)first_block * dk, Hkv, dk, static_cast<const __nv_bfloat16 *>(wk), wk_stride,
-                     kt + (size_t)first_block * dg};
-    project_rope_kernel<<<dim3(B * Hkv, (nsel + kProjRows - 1) / kProjRows), kProjThreads, psmem, stream>>>(
-        jk, jk, B * Hkv, nsel, nb, dg, (double)theta, first_block);
-    return cudaGetLastError();
-}
-
 // Decode gate ("SeerAttention-R": the gate without query pooling).  Its K
 // side is the prefill gate's: pooled K of the L-token cache, projected, block
 // RoPE, one row per block.  Those rows only change when a block changes, so
@@ -892,7 +874,15 @@ cudaError_t launch_gate_keys(int B, int Hkv, int L, int d, int dg, float theta, 
     cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess)
         return e;
-    return launch_project_keys(B, Hkv, nb, dk, dg, theta, kp, wk, wk_stride, first_block, kt, stream);
+    const size_t psmem = gate_projection_smem(dk, dg);
+    e = cudaFuncSetAttribute(project_rope_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)psmem);
+    if (e != cudaSuccess)
+        return e;
+    const ProjJob jk{kp + (size_t)first_block * dk, Hkv, dk, static_cast<const __nv_bfloat16 *>(wk), wk_stride,
+                     kt + (size_t)first_block * dg};
+    project_rope_kernel<<<dim3(B * Hkv, (nsel + kProjRows - 1) / kProjRows), kProjThreads, psmem, stream>>>(
+        jk, jk, B * Hkv, nsel, nb, dg, (double)theta, first_block);
+    return cudaGetLastError();
 }
 
 cudaError_t launch_decode_gate_cached(int B, int Hq, int Hkv, int L, int d, int dg, float theta, const void *q_tok,

@@ -53,8 +53,6 @@ cudaError_t launch_decode_gate(int B, int Hq, int Hkv, int L, int d, int dg, flo
 cudaError_t launch_gate_keys(int B, int Hkv, int L, int d, int dg, float theta, bool k_maxmin, const void *k,
                              const void *wk, long long wk_stride, int first_block, float *kt, void *ws,
                              cudaStream_t stream);
-cudaError_t launch_project_keys(int B, int Hkv, int nb, int dk, int dg, float theta, const float *kp, const void *wk,
-                                long long wk_stride, int first_block, float *kt, cudaStream_t stream);
 cudaError_t launch_decode_gate_cached(int B, int Hq, int Hkv, int L, int d, int dg, float theta, const void *q_tok,
                                       const void *wq, long long wq_stride, const float *kt, float *scores, void *ws,
                                       cudaStream_t stream);
@@ -79,7 +77,7 @@ cudaError_t launch_kv_read(int bits, int B, int Hkv, int n, int d, const KvView 
                            const int32_t *count, int start_pos, void *k, void *v, int *status, cudaStream_t stream);
 cudaError_t launch_gate_keys_quant(int bits, int B, int Hkv, int L, int d, int dg, float theta, bool k_maxmin,
                                    const KvView &kv, const int32_t *lens, const void *wk, long long wk_stride,
-                                   int first_block, float *kt, void *ws, int *status, cudaStream_t stream);
+                                   int first_block, float *kt, int *status, cudaStream_t stream);
 cudaError_t launch_decode_quant(int bits, int B, int Hq, int Hkv, int L, int d, float scale_log2, const void *q_tok,
                                 const KvView &kv, const int32_t *lens, const uint8_t *mask, void *o, float *lse,
                                 float *part, int *status, uint64_t timeout_ns, cudaStream_t stream);

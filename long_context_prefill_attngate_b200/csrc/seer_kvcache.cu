@@ -189,14 +189,18 @@ __device__ __forceinline__ uint32_t quantise8(const uint4 in, uint32_t (&code)[B
     const __nv_bfloat16 lob = __hmin_nan(mn.x, mn.y), hib = __hmax_nan(mx.x, mx.y);
     const float lo = __bfloat162float(lob), hi = __bfloat162float(hib);
     const bool ok = lo > -8.507059173023462e37f && hi < 8.507059173023462e37f;   // 2^126; false for a NaN
-    __nv_bfloat16 sb = __float2bfloat16_rn(__fdiv_rn(hi - lo, (float)F::TOP));
+    constexpr float kInvTop = 1.f / F::TOP;
+    const float range = hi - lo, s0 = range * kInvTop;   // range / TOP as IEEE division rounds it
+    __nv_bfloat16 sb = __float2bfloat16_rn(fmaf(fmaf(s0, -(float)F::TOP, range), kInvTop, s0));
     if (!ok || __bfloat162float(sb) < 7.888609052210118e-31f)                   // 2^-100
         sb = __float2bfloat16_rn(0.f);
     const float s = __bfloat162float(sb);
-    const float inv = s > 0.f ? __fdividef(1.f, s) : 0.f;
+    float inv;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(inv) : "f"(s));
+    inv = s > 0.f ? inv : 0.f;
     const float zr = ok ? lo : 0.f;
     constexpr uint32_t kMagic = 0x4B400000u;             // 1.5 2^23: adding it leaves the integer in the low bits
-    uint32_t acc[BITS / 4] = {};
+    uint32_t pair[4];                                    // n of two elements in the low bits
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
         const float2 v = make_float2(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xFFFF0000u));
@@ -206,15 +210,18 @@ __device__ __forceinline__ uint32_t quantise8(const uint4 in, uint32_t (&code)[B
         if (BITS == 8)                                   // s may be up to 2^-8 below the range / 255, not so at 15
             q = make_float2(fminf(q.x, (float)F::TOP), fminf(q.y, (float)F::TOP));
         const float2 m = add2(q, both(__uint_as_float(kMagic)));
-        constexpr int per = 32 / BITS;
-        acc[2 * i / per] += __float_as_uint(m.x) * (1u << (2 * i % per * BITS));
-        acc[(2 * i + 1) / per] += __float_as_uint(m.y) * (1u << ((2 * i + 1) % per * BITS));
+        pair[i] = __float_as_uint(m.y) * (1u << BITS) + __float_as_uint(m.x);
     }
-    // the sums carry kMagic times 1 + 2^BITS + ...
-    constexpr uint32_t bias = kMagic * (BITS == 4 ? 0x11111111u : 0x01010101u);
+    if constexpr (BITS == 4)
+        code[0] = __byte_perm(__byte_perm(pair[0], pair[1], 0x0040), __byte_perm(pair[2], pair[3], 0x0040), 0x5410);
+    else {
+        code[0] = __byte_perm(pair[0], pair[1], 0x5410);
+        code[1] = __byte_perm(pair[2], pair[3], 0x5410);
+    }
+    if (!ok)
 #pragma unroll
-    for (int i = 0; i < BITS / 4; ++i)
-        code[i] = s > 0.f ? acc[i] - bias : 0u;
+        for (int i = 0; i < BITS / 4; ++i)
+            code[i] = 0u;
     return (uint32_t)__bfloat16_as_ushort(sb) | (ok ? (uint32_t)__bfloat16_as_ushort(lob) : 0x7FC0u) << 16;
 }
 

@@ -130,7 +130,7 @@ def seer_kv_read(cache, n: int, start=None, count=None, start_pos: int = 0, k=No
 
 
 def seer_gate_key_cache_quant(cache, wk, L: int, kt=None, first_block: int = 0, lens=None, rope_theta: float = 5e5,
-                              workspace=None, stream=None, wk_head_stride: int | None = None, k_maxmin: bool = False):
+                              stream=None, wk_head_stride: int | None = None, k_maxmin: bool = False):
     """seer_gate_key_cache on the quantised cache: key rows fp32 [B,Hkv,nb,d_gate] of blocks first_block.. of a cache
     of L tokens, or of lens[b] (device int32 [B]) tokens each."""
     torch = _torch()
@@ -150,9 +150,8 @@ def seer_gate_key_cache_quant(cache, wk, L: int, kt=None, first_block: int = 0, 
 
     def call(st):
         out = torch.empty(shape, dtype=torch.float32, device=dev) if kt is None else kt
-        ws, wsb = B._workspace(B.SEER_CALL_GATE_KEY_CACHE_QUANT, sh, dev, workspace)
         _check(B.lib().seer_gate_key_cache_quant(ctypes.byref(sh), ctypes.byref(cache._c), _ptr(lens), _ptr(wk),
-                                                 ctypes.byref(gp), int(first_block), _ptr(out), _ptr(ws), wsb, st))
+                                                 ctypes.byref(gp), int(first_block), _ptr(out), st))
         return out
 
     return _on(dev, stream, call)

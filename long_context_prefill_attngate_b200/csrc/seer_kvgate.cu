@@ -4,9 +4,13 @@
 //
 // One kernel: a CTA pools sixteen blocks of a head and projects them.
 //  * Pooling reads the K half of each record once (HBM-bound for a whole
-//    cache): a warp has a block at a time, a lane every fourth of eight rows'
-//    words; sums of s n and of z in fp32, the 64 tokens joined by a
-//    reduce-scatter over the eight lanes of a row's word.
+//    cache).  The mean is an MMA too: the codes, transposed by pairing two
+//    tokens' words, are the fp16 subnormals n 2^-24 on M (as in the decode
+//    kernel), a group's scales are a column of N, normalised by the block's
+//    largest scale (exact in fp16 down to 2^-29 of it), and z is summed in fp32.
+//    0.75 integer operations an element instead of two and two fp32 ones.
+//    Max and min (the other pooling) take z + s n element by element; their
+//    warps share a block's rows when the CTA has few blocks.
 //  * Projection: sixteen pooled rows are the M of an mma.sync m16n8k16 (the
 //    refresh of a decode step has one row; a tcgen05 tile would be 1/128
 //    full).  Wk is bf16 as it is; a pooled value enters as three bf16 parts,
@@ -14,7 +18,10 @@
 //    fp32 as with plain fp32 FMAs.
 //  * Rotation as in the bf16 cache's key rows: frequency and angle in double,
 //    reduced modulo 2 pi, then fp32.
+#include <cmath>
+
 #include <cuda_bf16.h>
+#include <cuda_fp16.h>
 
 #include "seer_internal.h"
 #include "seer_kv.cuh"
@@ -27,15 +34,6 @@ constexpr int kGateThreads = 256;
 constexpr int kGateRows = 16;                            // blocks of a CTA: the M of the MMA
 constexpr int kPad = 8;                                  // bf16 padding of shared rows: ldmatrix without bank conflicts
 
-__device__ __forceinline__ float2 add2(float2 a, float2 b)
-{
-    float2 d;
-    asm("{\n\t.reg .b64 ra, rb, rd;\n\tmov.b64 ra, {%2, %3};\n\tmov.b64 rb, {%4, %5};\n\t"
-        "add.rn.f32x2 rd, ra, rb;\n\tmov.b64 {%0, %1}, rd;\n\t}"
-        : "=f"(d.x), "=f"(d.y)
-        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
-    return d;
-}
 __device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c)
 {
     float2 d;
@@ -85,16 +83,9 @@ __device__ __forceinline__ float min_nan(float a, float b)
     return r;
 }
 
-enum { kSum = 0, kMax = 1, kMin = 2 };
-
-__device__ __forceinline__ float join(int op, float a, float b)
-{
-    return op == kSum ? a + b : op == kMax ? max_nan(a, b) : min_nan(a, b);
-}
-
-// v[NV] of each of the eight lanes that differ in bits 2..4, joined: lane bits
-// 2..4 = i end with the values [i NV/8, (i + 1) NV/8) in v[0 ..].
-template <int OP, int NV>
+// v[NV] of each of the eight lanes that differ in bits 2..4, joined: the lane
+// whose bits are i ends with the values [i NV/8, (i + 1) NV/8) in v[0 ..].
+template <bool MAX, int NV>
 __device__ __forceinline__ void reduce_scatter(float (&v)[NV], int lane)
 {
 #pragma unroll
@@ -104,35 +95,243 @@ __device__ __forceinline__ void reduce_scatter(float (&v)[NV], int lane)
 #pragma unroll
         for (int i = 0; i < n; ++i) {
             const float send = upper ? v[i] : v[i + n], keep = upper ? v[i + n] : v[i];
-            v[i] = join(OP, keep, __shfl_xor_sync(0xffffffffu, send, off));
+            const float got = __shfl_xor_sync(0xffffffffu, send, off);
+            v[i] = MAX ? max_nan(keep, got) : min_nan(keep, got);
         }
     }
 }
 
-// x[0 .. N) of one pooled row from element e on, as three bf16 parts.
-template <int N>
-__device__ __forceinline__ void put_parts(__nv_bfloat16 *row, int part_stride, int e, const float *x)
+// Order-preserving keys, a NaN above everything: a maximum by atomicMax.
+__device__ __forceinline__ uint32_t max_key(float x)
 {
+    const uint32_t u = __float_as_uint(x);
+    return x != x ? 0xFFFFFFFFu : u >> 31 ? ~u : u | 0x80000000u;
+}
+__device__ __forceinline__ float from_max_key(uint32_t k)
+{
+    return k == 0xFFFFFFFFu ? __uint_as_float(0x7FC00000u) : __uint_as_float(k >> 31 ? k & 0x7FFFFFFFu : ~k);
+}
+
+__device__ __forceinline__ void mma_f16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                        uint32_t b1)
+{
+    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+                 : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+                 : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+__device__ __forceinline__ uint32_t pack_half2(float lo, float hi)
+{
+    uint32_t r;
+    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+
+template <int N>
+__device__ __forceinline__ void ldg_words(uint32_t (&w)[N], const uint8_t *p)
+{
+    if constexpr (N == 8) {
+        const uint4 x = __ldg(reinterpret_cast<const uint4 *>(p)), y = __ldg(reinterpret_cast<const uint4 *>(p) + 1);
+        w[0] = x.x, w[1] = x.y, w[2] = x.z, w[3] = x.w, w[4] = y.x, w[5] = y.y, w[6] = y.z, w[7] = y.w;
+    } else if constexpr (N == 4) {
+        const uint4 x = __ldg(reinterpret_cast<const uint4 *>(p));
+        w[0] = x.x, w[1] = x.y, w[2] = x.z, w[3] = x.w;
+    } else if constexpr (N == 2) {
+        const uint2 x = __ldg(reinterpret_cast<const uint2 *>(p));
+        w[0] = x.x, w[1] = x.y;
+    } else {
+        static_assert(N == 1);
+        w[0] = __ldg(reinterpret_cast<const uint32_t *>(p));
+    }
+}
+
+// One pooled value as three bf16 parts.
+__device__ __forceinline__ void put_parts(__nv_bfloat16 *at, int part_stride, float x)
+{
+    const __nv_bfloat16 hi = __float2bfloat16_rn(x);
+    const float r = x - __bfloat162float(hi);
+    const __nv_bfloat16 mid = __float2bfloat16_rn(r);
+    at[0] = hi;
+    at[part_stride] = mid;
+    at[2 * part_stride] = __float2bfloat16_rn(r - __bfloat162float(mid));
+}
+
+// The mean of block (page, kvh), `rows` tokens of it, by one warp into row[D]
+// (three parts).  A lane has rows k, k + 1, k + 8, k + 9 (k = 2 tig) of each
+// 16-token tile and the words of its eighth of a row: gid.
+template <int BITS, int D>
+__device__ __forceinline__ void pool_mean(const uint8_t *rec, int rows, __nv_bfloat16 *row, int part_stride, int lane)
+{
+    using F = KvFmt<BITS, D>;
+    constexpr int VW = F::R / 32, EPW = 32 / BITS;       // a lane's words of a row, elements of a word
+    const int gid = lane >> 2, tig = lane & 3;
+    // every load of the block first (rows behind its tokens too: their scales count as 0)
+    uint32_t w[4][4][VW], par[4][4];                     // [tile][row of the lane]
 #pragma unroll
-    for (int i = 0; i < N; ++i) {
-        const __nv_bfloat16 hi = __float2bfloat16_rn(x[i]);
-        const float r = x[i] - __bfloat162float(hi);
-        const __nv_bfloat16 mid = __float2bfloat16_rn(r);
-        row[e + i] = hi;
-        row[part_stride + e + i] = mid;
-        row[2 * part_stride + e + i] = __float2bfloat16_rn(r - __bfloat162float(mid));
+    for (int mt = 0; mt < 4; ++mt)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int t = (16 * mt + 2 * tig + (i & 1) + (i >> 1) * 8) % 32;
+            const int at = BITS == 8 && D == 128 ? ((gid >> 2) ^ (t & 1)) * 64 + (gid & 3) * 16 : gid * (F::R / 8);
+            ldg_words(w[mt][i], rec + mt / 2 * F::HALF + t * F::R + at);
+        }
+    // scales of group gid and the sum of its zeros
+    uint32_t smax = 0;
+    float zs = 0.f;
+#pragma unroll
+    for (int mt = 0; mt < 4; ++mt)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int t = 16 * mt + 2 * tig + (i & 1) + (i >> 1) * 8;
+            par[mt][i] = gid < F::NG && t < rows ? __ldg(reinterpret_cast<const uint32_t *>(
+                                                             rec + t / 32 * F::HALF + F::kParK + t % 32 * F::PAR) + gid)
+                                                 : 0u;
+        }
+#pragma unroll
+    for (int mt = 0; mt < 4; ++mt)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            smax = max(smax, par[mt][i] & 0xFFFFu);
+            zs += kv_zero(par[mt][i]);
+        }
+    zs += __shfl_xor_sync(0xffffffffu, zs, 1);
+    zs += __shfl_xor_sync(0xffffffffu, zs, 2);
+    smax = __reduce_max_sync(0xffffffffu, smax);
+    const int se = max((int)(smax >> 7), 27);            // exponent field of the largest scale, at least 2^-100's
+    const float up = __uint_as_float((uint32_t)(268 - se) << 23);      // scales to at most 2^15
+    float c[VW][EPW / 2][4];
+#pragma unroll
+    for (int k = 0; k < VW; ++k)
+#pragma unroll
+        for (int m = 0; m < EPW / 2; ++m)
+            c[k][m][0] = c[k][m][1] = c[k][m][2] = c[k][m][3] = 0.f;
+#pragma unroll
+    for (int mt = 0; mt < 4; ++mt) {
+        const uint32_t b0 = pack_half2(kv_scale(par[mt][0]) * up, kv_scale(par[mt][1]) * up);
+        const uint32_t b1 = pack_half2(kv_scale(par[mt][2]) * up, kv_scale(par[mt][3]) * up);
+#pragma unroll
+        for (int k = 0; k < VW; ++k)
+#pragma unroll
+            for (int hw = 0; hw < 2; ++hw) {             // halves of a word of two tokens
+                uint32_t x01 = __byte_perm(w[mt][0][k], w[mt][1][k], hw ? 0x7632 : 0x5410);
+                uint32_t x23 = __byte_perm(w[mt][2][k], w[mt][3][k], hw ? 0x7632 : 0x5410);
+                if constexpr (BITS == 4) {
+#pragma unroll
+                    for (int u = 0; u < 2; ++u) {
+                        mma_f16(c[k][2 * hw + u], x01 & 0x000F000Fu, x01 & 0x00F000F0u, x23 & 0x000F000Fu,
+                                x23 & 0x00F000F0u, b0, b1);
+                        x01 >>= 8;
+                        x23 >>= 8;
+                    }
+                } else {
+                    mma_f16(c[k][hw], __byte_perm(x01, 0u, 0x4240), __byte_perm(x01, 0u, 0x4341),
+                            __byte_perm(x23, 0u, 0x4240), __byte_perm(x23, 0u, 0x4341), b0, b1);
+                }
+            }
+    }
+    // a lane's elements: of word k, (hw, u) -> e; the group of its words is a column of c
+    const float down = __uint_as_float((uint32_t)(se - 14) << 23), inv = 1.f / (float)rows;
+#pragma unroll
+    for (int k = 0; k < VW; ++k) {
+        int gr, e0;                                      // group and first element of the word
+        if (BITS == 4) {
+            const int wd = gid * VW + k;
+            gr = wd % F::NG;
+            e0 = 32 * gr + wd / F::NG * 8;
+        } else if (D == 128) {
+            gr = gid >> 2;
+            e0 = 64 * gr + 16 * k + 4 * (gid & 3);
+        } else {
+            gr = 0;
+            e0 = 16 * (gid * 2 % 4 + k) + 4 * (gid / 2);
+        }
+        const float z = __shfl_sync(0xffffffffu, zs, gr * 4);
+        if (tig != gr >> 1)
+            continue;
+#pragma unroll
+        for (int m = 0; m < EPW / 2; ++m)
+#pragma unroll
+            for (int r = 0; r < 2; ++r) {                // element 2m + r in the rows' lower or upper eight
+                const float sum = (gr & 1 ? c[k][m][2 * r + 1] : c[k][m][2 * r]) * down * (BITS == 4 && r ? 1048576.f : 16777216.f);
+                put_parts(row + e0 + 2 * m + r, part_stride, (sum + z) * inv);
+            }
+    }
+}
+
+// The maxima and minima of the tokens [8 p0, 8 p1) of a block, by one warp,
+// joined into keys kx[D] (of the maximum) and kx[D ..] (of minus the minimum).
+template <int BITS, int D>
+__device__ __forceinline__ void pool_extrema(const uint8_t *rec, int rows, int p0, int p1, uint32_t *kx, int lane)
+{
+    using F = KvFmt<BITS, D>;
+    constexpr int KW = F::R / 16, NV = D / 4, EPW = 32 / BITS;   // a lane's words of a row, its elements, elements of a word
+    const int gid = lane >> 2, tig = lane & 3;
+    // value of a code's unit: by the parity of the element at 4 bits (2^-20, 2^-24)
+    auto unit = [](int e) { return BITS == 4 && e % 2 ? 9.5367431640625e-7f : 5.9604644775390625e-8f; };
+    float v[NV], v2[NV];
+#pragma unroll
+    for (int e = 0; e < NV; ++e) {
+        v[e] = -INFINITY;
+        v2[e] = INFINITY;
+    }
+#pragma unroll 1
+    for (int p = p0; p < p1; ++p) {
+        const int t = 8 * p + gid;
+        if (8 * p >= rows)
+            break;
+        const uint8_t *half = rec + t / 32 * F::HALF;
+        uint32_t code[KW], par[F::NG];
+        if constexpr (BITS == 8 && D == 128) {
+            uint32_t (&lo)[4] = *reinterpret_cast<uint32_t (*)[4]>(code);
+            uint32_t (&hi)[4] = *reinterpret_cast<uint32_t (*)[4]>(code + 4);
+            ldg_words(lo, half + t % 32 * F::R + (t & 1) * 64 + tig * 16);
+            ldg_words(hi, half + t % 32 * F::R + (~t & 1) * 64 + tig * 16);
+        } else {
+            ldg_words(code, half + t % 32 * F::R + tig * (F::R / 4));
+        }
+        ldg_words(par, half + F::kParK + t % 32 * F::PAR);
+        const bool in = t < rows;
+#pragma unroll
+        for (int k = 0; k < KW; ++k) {
+            const uint32_t pr = par[k / (KW / F::NG)];
+            const float s = kv_scale(pr), z = kv_zero(pr);
+#pragma unroll
+            for (int e = 0; e < EPW / 2; ++e) {          // two codes as fp16 subnormals, widened
+                const int e0 = BITS == 4 ? e : 2 * e, e1 = BITS == 4 ? e + 4 : 2 * e + 1;
+                const uint32_t h = BITS == 4 ? code[k] >> (e / 2 * 8) & (e % 2 ? 0x00F000F0u : 0x000F000Fu)
+                                             : __byte_perm(code[k], 0u, e ? 0x4342 : 0x4140);
+                const float2 n = __half22float2(*reinterpret_cast<const __half2 *>(&h));
+                const float2 x = fma2(n, both(s), both(z * unit(e0)));
+                if (in) {
+                    v[k * EPW + e0] = max_nan(v[k * EPW + e0], x.x);
+                    v[k * EPW + e1] = max_nan(v[k * EPW + e1], x.y);
+                    v2[k * EPW + e0] = min_nan(v2[k * EPW + e0], x.x);
+                    v2[k * EPW + e1] = min_nan(v2[k * EPW + e1], x.y);
+                }
+            }
+        }
+    }
+    reduce_scatter<true>(v, lane);
+    reduce_scatter<false>(v2, lane);
+    // the lane's values of the joined row: NV/8 neighbouring elements, from an even one on
+    constexpr int N = NV / 8;
+    const int at = gid * N, k = at / EPW;
+    const int e0 = (BITS == 4 ? 32 * k + 8 * tig : 16 * k + 4 * tig) + at % EPW;
+#pragma unroll
+    for (int e = 0; e < N; ++e) {
+        atomicMax(kx + e0 + e, max_key(v[e] * (1.f / unit(e))));
+        atomicMax(kx + D + e0 + e, max_key(-v2[e] * (1.f / unit(e))));
     }
 }
 
 template <int BITS, int D, bool MAXMIN>
-__global__ void __launch_bounds__(kGateThreads)
+__global__ void __launch_bounds__(kGateThreads, 2)
     kv_gate_kernel(KvView kv, int Hkv, int L, const int32_t *lens, int nb, int first, const __nv_bfloat16 *wk,
-                   long long wk_stride, int dg, double theta, float *kt, int *status)
+                   long long wk_stride, int dg, double log_freq, float *kt, int *status)
 {
     using F = KvFmt<BITS, D>;
     constexpr int DK = MAXMIN ? 2 * D : D;
     constexpr int XS = DK + kPad;                        // shared row strides (elements)
-    constexpr int KW = F::R / 16, NV = D / 4, EPW = 32 / BITS;   // a lane's words of a row, its elements, elements of a word
     extern __shared__ __align__(16) uint8_t gsm[];
     const int dgp = (dg + 7) & ~7, ws = dgp + kPad, ys = dg + 1;
     __nv_bfloat16 *sw = reinterpret_cast<__nv_bfloat16 *>(gsm);          // [DK][ws]
@@ -147,9 +346,11 @@ __global__ void __launch_bounds__(kGateThreads)
     // ---- Wk of the head on its way to shared memory
     const __nv_bfloat16 *w = wk + (long long)kvh * wk_stride;
     if (dg % 8 == 0 && (reinterpret_cast<uintptr_t>(w) & 15) == 0) {
-        const int ch = dg / 8;
-        for (int i = threadIdx.x; i < DK * ch; i += kGateThreads)
-            cp_async16(smem_u32(sw + i / ch * ws + i % ch * 8), w + (long long)i * 8);
+        const int ch = dg / 8, lg = 32 - __clz(ch - 1);  // 16-byte pieces of a row; a row's lanes, rounded up to 2^lg
+        const int c = lane & ((1 << lg) - 1);
+        if (c < ch)
+            for (int r = (warp << (5 - lg)) + (lane >> lg); r < DK; r += (kGateThreads / 32) << (5 - lg))
+                cp_async16(smem_u32(sw + r * ws + c * 8), w + r * dg + c * 8);
     } else {
         for (int i = threadIdx.x; i < DK * dgp; i += kGateThreads) {
             const int r = i / dgp, c = i % dgp;
@@ -158,146 +359,88 @@ __global__ void __launch_bounds__(kGateThreads)
     }
     asm volatile("cp.async.commit_group;" ::: "memory");
     if (threadIdx.x < dg / 2)
-        sfreq[threadIdx.x] = pow(theta, -2.0 * (double)threadIdx.x / (double)dg);
+        sfreq[threadIdx.x] = exp(log_freq * (double)threadIdx.x);
 
-    // ---- pooling: warp w has blocks w, w + 8
-    for (int i = warp; i < kGateRows; i += kGateThreads / 32) {
-        const int j = j0 + i;
-        const int rows = j < nb ? min(64, len - 64 * j) : 0;
-        const int page = rows > 0 ? kv_page(kv, b, j, status) : -1;
-        float v[NV], v2[MAXMIN ? NV : 1], zs[F::NG];
-#pragma unroll
-        for (int e = 0; e < NV; ++e) {
-            v[e] = MAXMIN ? -INFINITY : 0.f;
-            if (MAXMIN)
-                v2[e] = INFINITY;
+    // ---- pooling (rows of sx behind the last block stay unwritten: their
+    // products are rows of their own, which nothing reads)
+    constexpr int kWarps = kGateThreads / 32;
+    const int valid = min(kGateRows, nb - j0);
+    auto tokens = [&](int i) { return i < valid ? min(64, len - 64 * (j0 + i)) : 0; };
+    auto record = [&](int i) -> const uint8_t * {        // null where block j0 + i has no token or no page
+        const int page = tokens(i) > 0 ? kv_page(kv, b, j0 + i, status) : -1;
+        return page < 0 ? nullptr : kv_half<F>(kv, Hkv, page, kvh, 0);
+    };
+    if constexpr (MAXMIN) {
+        uint32_t *kx = reinterpret_cast<uint32_t *>(sy + kGateRows * ys);          // [kGateRows][DK]
+        for (int i = threadIdx.x; i < valid * DK; i += kGateThreads)
+            kx[i] = 0u;
+        __syncthreads();
+        const int parts = valid <= 4 ? kWarps : 1;       // warps that share a block: an eighth costs a fifth of the whole
+        for (int u = warp; u < valid * parts; u += kWarps) {
+            const int i = u / parts, p = u % parts;
+            const uint8_t *rec = record(i);
+            if (rec != nullptr)
+                pool_extrema<BITS, D>(rec, tokens(i), p * (8 / parts), (p + 1) * (8 / parts), kx + i * DK, lane);
         }
-#pragma unroll
-        for (int gr = 0; gr < F::NG; ++gr)
-            zs[gr] = 0.f;
-        if (page >= 0) {
-#pragma unroll
-            for (int hf = 0; hf < 2; ++hf) {
-                const uint8_t *half = kv_half<F>(kv, Hkv, page, kvh, hf);
-                uint32_t code[4][KW], par[4][F::NG];
-                if (32 * hf >= rows)
-                    break;
-#pragma unroll
-                for (int r = 0; r < 4; ++r) {
-                    const int t = gid + 8 * r;
-                    if constexpr (BITS == 8 && D == 128) {
-                        const uint4 x0 = __ldg(reinterpret_cast<const uint4 *>(half + t * F::R + (t & 1) * 64 + tig * 16));
-                        const uint4 x1 = __ldg(reinterpret_cast<const uint4 *>(half + t * F::R + (~t & 1) * 64 + tig * 16));
-                        code[r][0] = x0.x, code[r][1] = x0.y, code[r][2] = x0.z, code[r][3] = x0.w;
-                        code[r][4] = x1.x, code[r][5] = x1.y, code[r][6] = x1.z, code[r][7] = x1.w;
-                    } else if constexpr (KW == 4) {
-                        const uint4 x0 = __ldg(reinterpret_cast<const uint4 *>(half + t * F::R + tig * 16));
-                        code[r][0] = x0.x, code[r][1] = x0.y, code[r][2] = x0.z, code[r][3] = x0.w;
-                    } else {
-                        const uint2 x0 = __ldg(reinterpret_cast<const uint2 *>(half + t * F::R + tig * 8));
-                        code[r][0] = x0.x, code[r][1] = x0.y;
-                    }
-#pragma unroll
-                    for (int gr = 0; gr < F::NG; ++gr)
-                        par[r][gr] = __ldg(reinterpret_cast<const uint32_t *>(half + F::kParK + t * F::PAR) + gr);
-                }
-#pragma unroll
-                for (int r = 0; r < 4; ++r) {
-                    const bool in = 32 * hf + gid + 8 * r < rows;
-#pragma unroll
-                    for (int k = 0; k < KW; ++k) {
-                        const int gr = k / (KW / F::NG);
-                        const uint32_t p = in ? par[r][gr] : 0u;
-                        const float s = kv_scale(p), z = kv_zero(p);
-                        if (!MAXMIN && k % (KW / F::NG) == 0)
-                            zs[gr] += z;
-#pragma unroll
-                        for (int e = 0; e < EPW; e += 2) {
-                            const uint32_t q0 = code[r][k] >> (e * BITS), q1 = code[r][k] >> ((e + 1) * BITS);
-                            const float2 n = add2(make_float2(__uint_as_float((q0 & (uint32_t)F::TOP) | 0x4B000000u),
-                                                              __uint_as_float((q1 & (uint32_t)F::TOP) | 0x4B000000u)),
-                                                  both(-8388608.f));
-                            float &a0 = v[k * EPW + e], &a1 = v[k * EPW + e + 1];
-                            if constexpr (MAXMIN) {
-                                const float2 x = fma2(n, both(s), both(z));
-                                a0 = in ? max_nan(a0, x.x) : a0;
-                                a1 = in ? max_nan(a1, x.y) : a1;
-                                v2[k * EPW + e] = in ? min_nan(v2[k * EPW + e], x.x) : v2[k * EPW + e];
-                                v2[k * EPW + e + 1] = in ? min_nan(v2[k * EPW + e + 1], x.y) : v2[k * EPW + e + 1];
-                            } else {
-                                const float2 x = fma2(n, both(s), make_float2(a0, a1));
-                                a0 = x.x;
-                                a1 = x.y;
-                            }
-                        }
-                    }
-                }
-            }
+        __syncthreads();
+        for (int i = threadIdx.x; i < valid * DK; i += kGateThreads) {
+            const float x = kx[i] == 0u ? 0.f : from_max_key(kx[i]);     // no token: 0
+            put_parts(sx + i / DK * XS + i % DK, kGateRows * XS, i % DK < D ? x : -x);
         }
-        // the lane's values of the joined row: NV/8 neighbouring elements
-        constexpr int N = NV / 8;
-        const int at = gid * N, k = at / EPW;            // value index, its word
-        const int e0 = (BITS == 4 ? 32 * k + 8 * tig : 16 * k + 4 * tig) + at % EPW;
-        __nv_bfloat16 *row = sx + i * XS;
-        reduce_scatter<MAXMIN ? kMax : kSum>(v, lane);
-        if constexpr (MAXMIN) {
-            reduce_scatter<kMin>(v2, lane);
-            if (page < 0)
-#pragma unroll
-                for (int e = 0; e < N; ++e)
-                    v[e] = v2[e] = 0.f;
-            put_parts<N>(row, kGateRows * XS, e0, v);
-            put_parts<N>(row, kGateRows * XS, D + e0, v2);
-        } else {
-#pragma unroll
-            for (int off = 4; off < 32; off <<= 1)
-#pragma unroll
-                for (int gr = 0; gr < F::NG; ++gr)
-                    zs[gr] += __shfl_xor_sync(0xffffffffu, zs[gr], off);
-            float z = zs[0];
-#pragma unroll
-            for (int gr = 1; gr < F::NG; ++gr)
-                z = k / (KW / F::NG) == gr ? zs[gr] : z;
-#pragma unroll
-            for (int e = 0; e < N; ++e)
-                v[e] = page < 0 ? 0.f : (v[e] + z) / (float)rows;
-            put_parts<N>(row, kGateRows * XS, e0, v);
+    } else {
+        const uint8_t *next = record(warp);
+        for (int i = warp; i < valid; i += kWarps) {
+            const uint8_t *rec = next;
+            next = record(i + kWarps);                   // a table entry ahead
+            if (rec != nullptr)
+                pool_mean<BITS, D>(rec, tokens(i), sx + i * XS, kGateRows * XS, lane);
+            else
+                for (int e = lane; e < D; e += 32)
+                    put_parts(sx + i * XS + e, kGateRows * XS, 0.f);
         }
     }
     asm volatile("cp.async.wait_group 0;" ::: "memory");
     __syncthreads();
 
-    // ---- projection: eight columns at a time
-    for (int n0 = warp * 8; n0 < dgp; n0 += kGateThreads / 32 * 8) {
-        float c[4] = {0.f, 0.f, 0.f, 0.f}, cl[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll 4
+    // ---- projection: a warp has eight columns, and eight 64 further on
+    constexpr int kColStep = kGateThreads / 32 * 8;
+    for (int n0 = warp * 8; n0 < dgp; n0 += 2 * kColStep) {
+        const int n1 = n0 + kColStep < dgp ? n0 + kColStep : n0;
+        float c[2][4] = {}, cl[2][4] = {};               // by the hi parts, by the other two
+#pragma unroll 8
         for (int k0 = 0; k0 < DK; k0 += 16) {
-            uint32_t b0, b1, x[4];
+            uint32_t b0, b1, d0, d1, x[4], y[4], z[4];
             ldmatrix2_trans(b0, b1, smem_u32(sw + (k0 + (lane & 15)) * ws + n0));
+            ldmatrix2_trans(d0, d1, smem_u32(sw + (k0 + (lane & 15)) * ws + n1));
             const uint32_t xa = smem_u32(sx + (lane & 15) * XS + k0 + (lane >> 4) * 8);
             ldmatrix4(x, xa);
-            mma_bf16(c, x, b0, b1);
-            ldmatrix4(x, xa + kGateRows * XS * 2);
-            mma_bf16(cl, x, b0, b1);
-            ldmatrix4(x, xa + 2 * kGateRows * XS * 2);
-            mma_bf16(cl, x, b0, b1);
+            ldmatrix4(y, xa + kGateRows * XS * 2);
+            ldmatrix4(z, xa + 2 * kGateRows * XS * 2);
+            mma_bf16(c[0], x, b0, b1);
+            mma_bf16(c[1], x, d0, d1);
+            mma_bf16(cl[0], y, b0, b1);
+            mma_bf16(cl[1], y, d0, d1);
+            mma_bf16(cl[0], z, b0, b1);
+            mma_bf16(cl[1], z, d0, d1);
         }
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            const int col = n0 + 2 * tig + (e & 1);
-            if (col < dg)
-                sy[(gid + (e >> 1) * 8) * ys + col] = c[e] + cl[e];
-        }
+        for (int u = 0; u < 2; ++u)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const int col = (u ? n1 : n0) + 2 * tig + (e & 1);
+                if (col < dg)
+                    sy[(gid + (e >> 1) * 8) * ys + col] = c[u][e] + cl[u][e];
+            }
     }
     __syncthreads();
 
     // ---- rotation, pairs (t, t + dg/2) at the position of the block
     constexpr double kTwoPi = 6.283185307179586476925286766559;
-    const int half = dg / 2;
-    for (int i = threadIdx.x; i < kGateRows * half; i += kGateThreads) {
-        const int r = i / half, t = i % half, j = j0 + r;
-        if (j >= nb)
-            break;
+    const int half = dg / 2, lgh = half > 1 ? 32 - __clz(half - 1) : 0;   // a row's threads, rounded up to 2^lgh
+    const int t = threadIdx.x & ((1 << lgh) - 1);
+#pragma unroll 4
+    for (int r = threadIdx.x >> lgh; r < (t < half ? valid : 0); r += kGateThreads >> lgh) {
+        const int j = j0 + r;
         const double ang = (double)j * sfreq[t];
         const double red = ang - rint(ang * (1.0 / kTwoPi)) * kTwoPi;
         float sn, cs;
@@ -316,13 +459,14 @@ cudaError_t launch(int B, int Hkv, int L, const KvView &kv, const int32_t *lens,
     constexpr int DK = MAXMIN ? 2 * D : D;
     const int nb = num_blocks(L), dgp = (dg + 7) & ~7;
     const size_t smem = sizeof(__nv_bfloat16) * ((size_t)DK * (dgp + kPad) + 3 * kGateRows * (DK + kPad)) +
-                        sizeof(double) * (dg / 2) + sizeof(float) * kGateRows * (dg + 1);
+                        sizeof(double) * (dg / 2) + sizeof(float) * kGateRows * (dg + 1 + (MAXMIN ? DK : 0));
     const cudaError_t e = cudaFuncSetAttribute(kv_gate_kernel<BITS, D, MAXMIN>,
                                                cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess)
         return e;
     kv_gate_kernel<BITS, D, MAXMIN><<<dim3((nb - first + kGateRows - 1) / kGateRows, B * Hkv), kGateThreads, smem, stream>>>(
-        kv, Hkv, L, lens, nb, first, static_cast<const __nv_bfloat16 *>(wk), wk_stride, dg, (double)theta, kt, status);
+        kv, Hkv, L, lens, nb, first, static_cast<const __nv_bfloat16 *>(wk), wk_stride, dg,
+        -2.0 * log((double)theta) / dg, kt, status);
     return cudaGetLastError();
 }
 

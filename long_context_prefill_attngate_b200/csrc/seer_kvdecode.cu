@@ -16,7 +16,8 @@
 //  * The codes enter the MMA as they are: n <= 255 in the low bits of an fp16 is
 //    the subnormal n 2^-24, so one mask (4 bits) or byte permute (8 bits) makes
 //    a pair of operands, and scale and zero are applied outside:
-//      q . k   = sum_g s_g (q_g . n_g) + z_g sum(q_g)        fp32, per key
+//      q . k   = sum_g s_g (q_g . n_g) + z_g sum(q_g)        per key; the second by an
+//                MMA of the params as they lie with sum(q_g) in three bf16 parts
 //      sum p v = sum_t (p_t s_t,g) n_t + sum_t p_t z_t,g      p s rounded to fp16
 //    q is exact in fp16 after a power of two per head; p s <= 2^15 after a power
 //    of two that follows the largest scale seen (as a running maximum, so it
@@ -51,6 +52,14 @@ __device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1
                                          uint32_t b1)
 {
     asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+                 : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+                 : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+__device__ __forceinline__ void mma16816_bf16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                              uint32_t b0, uint32_t b1)
+{
+    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
                  : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
                  : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
@@ -105,6 +114,80 @@ __device__ __forceinline__ void load_words(uint32_t (&w)[N], const uint8_t *p)
 // a V fragment reads at once differ in the bits its swizzle uses.
 __device__ __forceinline__ int tile_token(int r) { return r ^ ((r >> 1) & 1); }
 
+// The B operand of the scores for head gid (0 where there is none): K's code
+// order, in fp16 times 2^qe; qz: the group sums as the B operand that takes K's
+// params as they lie, (s, z) of group tig, so 0 for s and the sum for z, in
+// three bf16 parts (rows 2 tig, 2 tig + 1 of the hi, mid and lo operand);
+// qinv: 2^-qe of heads 2 tig, 2 tig + 1.  One warp.
+template <int D>
+constexpr int kQWords = D / 8 + 5;                  // words of a lane: odd multiples keep the banks apart
+
+template <int BITS, int D>
+__device__ __forceinline__ void q_fragments(const __nv_bfloat16 *qp, bool have, int lane, uint32_t (&qf)[D / 16][2],
+                                            uint32_t (&qz)[3], float (&qinv)[2])
+{
+    constexpr int KS = D / 16, NG = KvFmt<BITS, D>::NG;
+    const int tig = lane & 3;
+    float f[KS * 4];                                // this lane's elements, in its K words' order
+#pragma unroll
+    for (int i = 0; i < KS; ++i) {                  // four elements at a time
+        const int e = BITS == 4 ? 32 * (i / 2) + 8 * tig + 4 * (i % 2) : 16 * i + 4 * tig;
+        uint2 u = make_uint2(0u, 0u);
+        if (have)
+            u = __ldg(reinterpret_cast<const uint2 *>(qp + e));
+        f[4 * i] = __uint_as_float(u.x << 16);
+        f[4 * i + 1] = __uint_as_float(u.x & 0xFFFF0000u);
+        f[4 * i + 2] = __uint_as_float(u.y << 16);
+        f[4 * i + 3] = __uint_as_float(u.y & 0xFFFF0000u);
+    }
+    float mx = 0.f;
+#pragma unroll
+    for (int i = 0; i < KS * 4; ++i)
+        mx = fmaxf(mx, fabsf(f[i]));
+    mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+    mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+    // max |q| 2^qe in [2^14, 2^15); no scaling for 0 and infinity
+    const int eb = (int)(__float_as_uint(mx) >> 23);
+    const int qe = mx == 0.f || eb == 255 ? 0 : min(141 - eb, 126);
+    const float up = pow2_field(127 + qe), down = pow2_field(127 - qe);
+#pragma unroll
+    for (int i = 0; i < KS * 4; ++i)
+        f[i] *= up;
+    float sum = 0.f;                                // of group tig
+#pragma unroll
+    for (int gr = 0; gr < NG; ++gr) {
+        float s = 0.f;
+#pragma unroll
+        for (int i = 0; i < KS * 4 / NG; ++i)
+            s += f[gr * (KS * 4 / NG) + i];
+        s += __shfl_xor_sync(0xffffffffu, s, 1);
+        s += __shfl_xor_sync(0xffffffffu, s, 2);
+        sum = gr == tig ? s * 5.9604644775390625e-8f : sum;         // 2^-24: the unit of the codes' products
+    }
+#pragma unroll
+    for (int i = 0; i < 3; ++i) {
+        const __nv_bfloat16 part = __float2bfloat16_rn(sum);
+        qz[i] = (uint32_t)__bfloat16_as_ushort(part) << 16;
+        sum -= __bfloat162float(part);
+    }
+#pragma unroll
+    for (int u = 0; u < 2; ++u)
+        qinv[u] = __shfl_sync(0xffffffffu, down, (2 * tig + u) * 4);
+    // operand pairs as the codes' masks give them: at 4 bits elements (0,4),
+    // (1,5) 2^4, (2,6), (3,7) 2^4 of a word, so the second is taken 2^-4
+#pragma unroll
+    for (int i = 0; i < KS; ++i) {
+        if (BITS == 4) {
+            const float *w = f + 8 * (i / 2) + 2 * (i % 2);
+            qf[i][0] = pack_half2(w[0], w[4]);
+            qf[i][1] = pack_half2(w[1] * 0.0625f, w[5] * 0.0625f);
+        } else {
+            qf[i][0] = pack_half2(f[4 * i], f[4 * i + 1]);
+            qf[i][1] = pack_half2(f[4 * i + 2], f[4 * i + 3]);
+        }
+    }
+}
+
 struct DecodeArgs {
     const __nv_bfloat16 *q_tok;
     KvView kv;
@@ -144,6 +227,7 @@ __global__ void __launch_bounds__(DecodeCfg<BITS, D>::W * 32, 1) decode_quant_ke
     __shared__ uint32_t s_words[kMaxNb / 32];
     __shared__ int s_page[kListMax];
     __shared__ uint16_t s_block[kListMax];
+    __shared__ uint32_t s_q[32 * kQWords<D>];
 
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int gid = lane >> 2, tig = lane & 3;
@@ -163,88 +247,80 @@ __global__ void __launch_bounds__(DecodeCfg<BITS, D>::W * 32, 1) decode_quant_ke
         fence_mbar_init();
     }
 
-    // ---- union of the heads' active blocks, one bit each
-    const int nblk = (len + 63) / 64, nwords = (nblk + 31) / 32;
-    for (int c = warp; c < nwords; c += W) {
-        const int j = c * 32 + lane;
-        int any = 0;
-        if (j < nblk) {
-#pragma unroll
-            for (int h = 0; h < kHeads; ++h)
-                if (h < gt)
-                    any |= __ldg(mrow + (long long)h * a.nb + j);
-            if (any != 0 && kv_page(a.kv, b, j, a.status) < 0)
-                any = 0;
-        }
-        const unsigned bits = __ballot_sync(0xffffffffu, any != 0);
-        if (lane == 0)
-            s_words[c] = bits;
-    }
-
-    // ---- q fragments: column gid = head h0 + gid, in fp16 times 2^qe
-    uint32_t qf[KS][2];
-    float qs[NG][2], qinv[2];                       // of heads 2 tig, 2 tig + 1: group sums, 2^-qe
-    {
-        float f[KS * 4];                            // this lane's elements, in its K words' order
-        const __nv_bfloat16 *qp = a.q_tok + ((long long)b * a.Hq + h0 + gid) * D;
-#pragma unroll
-        for (int i = 0; i < KS; ++i) {              // four elements at a time
-            const int e = BITS == 4 ? 32 * (i / 2) + 8 * tig + 4 * (i % 2) : 16 * i + 4 * tig;
-            uint2 u = make_uint2(0u, 0u);
-            if (gid < gt)
-                u = __ldg(reinterpret_cast<const uint2 *>(qp + e));
-            f[4 * i] = __uint_as_float(u.x << 16);
-            f[4 * i + 1] = __uint_as_float(u.x & 0xFFFF0000u);
-            f[4 * i + 2] = __uint_as_float(u.y << 16);
-            f[4 * i + 3] = __uint_as_float(u.y & 0xFFFF0000u);
-        }
-        float mx = 0.f;
-#pragma unroll
-        for (int i = 0; i < KS * 4; ++i)
-            mx = fmaxf(mx, fabsf(f[i]));
-        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
-        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
-        // max |q| 2^qe in [2^14, 2^15); no scaling for 0 and infinity
-        const int eb = (int)(__float_as_uint(mx) >> 23);
-        const int qe = mx == 0.f || eb == 255 ? 0 : min(141 - eb, 126);
-        const float up = pow2_field(127 + qe), down = pow2_field(127 - qe);
-#pragma unroll
-        for (int i = 0; i < KS * 4; ++i)
-            f[i] *= up;
-        float gs[NG];
-#pragma unroll
-        for (int gr = 0; gr < NG; ++gr) {
-            float s = 0.f;
-#pragma unroll
-            for (int i = 0; i < KS * 4 / NG; ++i)
-                s += f[gr * (KS * 4 / NG) + i];
-            s += __shfl_xor_sync(0xffffffffu, s, 1);
-            s += __shfl_xor_sync(0xffffffffu, s, 2);
-            gs[gr] = s * 5.9604644775390625e-8f;    // 2^-24: the unit of the codes' products
-        }
-#pragma unroll
-        for (int u = 0; u < 2; ++u) {
-            const int src = (2 * tig + u) * 4;
-#pragma unroll
-            for (int gr = 0; gr < NG; ++gr)
-                qs[gr][u] = __shfl_sync(0xffffffffu, gs[gr], src);
-            qinv[u] = __shfl_sync(0xffffffffu, down, src);
-        }
-        // operand pairs as the codes' masks give them: at 4 bits elements (0,4),
-        // (1,5) 2^4, (2,6), (3,7) 2^4 of a word, so the second is taken 2^-4
+    // ---- q, by one warp for all of them
+    uint32_t qf[KS][2], qz[3];
+    float qinv[2];
+    if (warp == W - 1) {
+        q_fragments<BITS, D>(a.q_tok + ((long long)b * a.Hq + h0 + gid) * D, gid < gt, lane, qf, qz, qinv);
+        uint32_t *to = s_q + lane * kQWords<D>;
 #pragma unroll
         for (int i = 0; i < KS; ++i) {
-            if (BITS == 4) {
-                const float *w = f + 8 * (i / 2) + 2 * (i % 2);
-                qf[i][0] = pack_half2(w[0], w[4]);
-                qf[i][1] = pack_half2(w[1] * 0.0625f, w[5] * 0.0625f);
-            } else {
-                qf[i][0] = pack_half2(f[4 * i], f[4 * i + 1]);
-                qf[i][1] = pack_half2(f[4 * i + 2], f[4 * i + 3]);
+            to[2 * i] = qf[i][0];
+            to[2 * i + 1] = qf[i][1];
+        }
+#pragma unroll
+        for (int i = 0; i < 3; ++i)
+            to[2 * KS + i] = qz[i];
+        to[2 * KS + 3] = __float_as_uint(qinv[0]);
+        to[2 * KS + 4] = __float_as_uint(qinv[1]);
+    }
+
+    // ---- union of the heads' active blocks, one bit each: kMaskWords words of 32
+    // blocks a warp at a time, all their loads (the table's too, and the first
+    // ones before the length is known) in flight together
+    constexpr int kMaskWords = 4;
+    const int nblk = (len + 63) / 64, nwords = (nblk + 31) / 32;
+    int page[kMaskWords];
+    for (int c0 = warp; c0 < (c0 == warp ? (a.nb + 31) / 32 : nwords); c0 += kMaskWords * W) {
+        int raw[kMaskWords][kHeads], any[kMaskWords], pg[kMaskWords];
+        // no branch between the loads: blocks past the row and heads past the tile
+        // read the last one again
+#pragma unroll
+        for (int i = 0; i < kMaskWords; ++i) {
+            const int j = min((c0 + i * W) * 32 + lane, a.nb - 1);
+#pragma unroll
+            for (int h = 0; h < kHeads; ++h)
+                raw[i][h] = __ldg(mrow + (long long)min(h, gt - 1) * a.nb + j);
+            pg[i] = b * a.kv.max_blocks + j;
+            if (a.kv.table != nullptr)
+                pg[i] = __ldg(a.kv.table + pg[i]);
+        }
+#pragma unroll
+        for (int i = 0; i < kMaskWords; ++i) {
+            any[i] = 0;
+#pragma unroll
+            for (int h = 0; h < kHeads; ++h)
+                any[i] |= raw[i][h];
+        }
+#pragma unroll
+        for (int i = 0; i < kMaskWords; ++i) {
+            if ((c0 + i * W) * 32 + lane >= nblk)
+                any[i] = 0;
+            if (any[i] != 0 && (pg[i] < 0 || pg[i] >= a.kv.n_pages)) {
+                set_status(a.status, kStatusPage);
+                any[i] = 0;
             }
+            const unsigned bits = __ballot_sync(0xffffffffu, any[i] != 0);
+            if (lane == 0 && c0 + i * W < nwords)
+                s_words[c0 + i * W] = bits;
+            if (c0 == warp)
+                page[i] = pg[i];
         }
     }
     __syncthreads();
+    if (warp != W - 1) {
+        const uint32_t *from = s_q + lane * kQWords<D>;
+#pragma unroll
+        for (int i = 0; i < KS; ++i) {
+            qf[i][0] = from[2 * i];
+            qf[i][1] = from[2 * i + 1];
+        }
+#pragma unroll
+        for (int i = 0; i < 3; ++i)
+            qz[i] = from[2 * KS + i];
+        qinv[0] = __uint_as_float(from[2 * KS + 3]);
+        qinv[1] = __uint_as_float(from[2 * KS + 4]);
+    }
 
     // ---- this split's blocks: ranks [r0, r1) of the union
     int r0, r1;
@@ -263,7 +339,7 @@ __global__ void __launch_bounds__(DecodeCfg<BITS, D>::W * 32, 1) decode_quant_ke
         const int total = __shfl_sync(0xffffffffu, inc, 31);
         r0 = total * split / a.nsplit;
         r1 = total * (split + 1) / a.nsplit;
-        for (int c = warp; c < nwords; c += W) {
+        auto list = [&](int c, int pg) {            // word c's blocks; pg < 0: look the page up
             int base = __shfl_sync(0xffffffffu, inc - cnt, c / per);
             for (int k = c / per * per; k < c; ++k)
                 base += __popc(s_words[k]);
@@ -272,10 +348,17 @@ __global__ void __launch_bounds__(DecodeCfg<BITS, D>::W * 32, 1) decode_quant_ke
             if ((w >> lane & 1u) && r >= r0 && r < r1) {
                 const int j = c * 32 + lane;
                 s_block[r - r0] = (uint16_t)j;
-                s_page[r - r0] =
-                    a.kv.table != nullptr ? __ldg(a.kv.table + (long long)b * a.kv.max_blocks + j) : b * a.kv.max_blocks + j;
+                s_page[r - r0] = pg >= 0 ? pg
+                                 : a.kv.table != nullptr ? __ldg(a.kv.table + (long long)b * a.kv.max_blocks + j)
+                                                         : b * a.kv.max_blocks + j;
             }
-        }
+        };
+#pragma unroll
+        for (int i = 0; i < kMaskWords; ++i)
+            if (warp + i * W < nwords)
+                list(warp + i * W, page[i]);
+        for (int c = warp + kMaskWords * W; c < nwords; c += W)
+            list(c, -1);
     }
     __syncthreads();
 
@@ -360,6 +443,12 @@ __global__ void __launch_bounds__(DecodeCfg<BITS, D>::W * 32, 1) decode_quant_ke
             load_words(pa, h + F::kParK + ra * F::PAR);
             load_words(pb, h + F::kParK + rb * F::PAR);
             s[mt][0] = s[mt][1] = s[mt][2] = s[mt][3] = 0.f;
+            {                                       // z sum(q) of the groups: the params themselves are the operand
+                const uint32_t wa = tig < NG ? *reinterpret_cast<const uint32_t *>(h + F::kParK + ra * F::PAR + tig * 4) : 0u;
+                const uint32_t wb = tig < NG ? *reinterpret_cast<const uint32_t *>(h + F::kParK + rb * F::PAR + tig * 4) : 0u;
+                mma16816_bf16(s[mt], wa, wb, wa, wb, qz[0], qz[1]);
+                mma16816_bf16(s[mt], wa, wb, 0u, 0u, qz[2], 0u);
+            }
 #pragma unroll
             for (int gr = 0; gr < NG; ++gr) {
                 float c[4] = {0.f, 0.f, 0.f, 0.f};
@@ -376,11 +465,11 @@ __global__ void __launch_bounds__(DecodeCfg<BITS, D>::W * 32, 1) decode_quant_ke
                                  __byte_perm(wa, 0u, 0x4342), __byte_perm(wb, 0u, 0x4342), qf[ks][0], qf[ks][1]);
                     }
                 }
-                const float sa = kv_scale(pa[gr]), za = kv_zero(pa[gr]), sb = kv_scale(pb[gr]), zb = kv_zero(pb[gr]);
-                s[mt][0] = fmaf(sa, c[0], fmaf(za, qs[gr][0], s[mt][0]));
-                s[mt][1] = fmaf(sa, c[1], fmaf(za, qs[gr][1], s[mt][1]));
-                s[mt][2] = fmaf(sb, c[2], fmaf(zb, qs[gr][0], s[mt][2]));
-                s[mt][3] = fmaf(sb, c[3], fmaf(zb, qs[gr][1], s[mt][3]));
+                const float sa = kv_scale(pa[gr]), sb = kv_scale(pb[gr]);
+                s[mt][0] = fmaf(sa, c[0], s[mt][0]);
+                s[mt][1] = fmaf(sa, c[1], s[mt][1]);
+                s[mt][2] = fmaf(sb, c[2], s[mt][2]);
+                s[mt][3] = fmaf(sb, c[3], s[mt][3]);
             }
 #pragma unroll
             for (int e = 0; e < 4; ++e)
@@ -388,15 +477,13 @@ __global__ void __launch_bounds__(DecodeCfg<BITS, D>::W * 32, 1) decode_quant_ke
         }
         const bool all_heads = hbits == 0xffffffffu;
         const bool act0 = hbits >> (2 * tig) & 1u, act1 = hbits >> (2 * tig + 1) & 1u;
-        if (keys < 32 || !all_heads) {
+        if (keys < 32) {                            // the sequence's last tokens
 #pragma unroll
             for (int mt = 0; mt < 2; ++mt)
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const int t = 16 * mt + tile_token(gid) + (e & 2) * 4;
-                    if (t >= keys || !((e & 1) ? act1 : act0))
+                for (int e = 0; e < 4; ++e)
+                    if (16 * mt + tile_token(gid) + (e & 2) * 4 >= keys)
                         s[mt][e] = -INFINITY;
-                }
         }
 
         // ---- V's params (zero behind the length) and the power of two for p s
@@ -408,13 +495,15 @@ __global__ void __launch_bounds__(DecodeCfg<BITS, D>::W * 32, 1) decode_quant_ke
             for (int hf = 0; hf < 2; ++hf) {
                 const int t = 16 * mt + tile_token(gid) + 8 * hf;
                 load_words(vp[mt][hf], h + F::kParV + t * F::PAR);
-                if (t >= keys)
+                if (keys < 32 && t >= keys)
 #pragma unroll
                     for (int gr = 0; gr < NG; ++gr)
                         vp[mt][hf][gr] = 0u;
+                if constexpr (NG == 1)
+                    vmax = __vmaxu2(vmax, vp[mt][hf][0]);
 #pragma unroll
-                for (int gr = 0; gr < NG; ++gr)
-                    vmax = __vmaxu2(vmax, vp[mt][hf][gr]);
+                for (int gr = 0; gr + 1 < NG; gr += 2)
+                    vmax = __vimax3_u16x2(vmax, vp[mt][hf][gr], vp[mt][hf][gr + 1]);
             }
         float mx[2];
 #pragma unroll
@@ -430,7 +519,8 @@ __global__ void __launch_bounds__(DecodeCfg<BITS, D>::W * 32, 1) decode_quant_ke
         float alpha[2], mu[2];
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
-            const float mn = fmaxf(m[e], mx[e]);
+            // a head that left the block out: its maximum stays and its p are 0
+            const float mn = (e ? act1 : act0) ? fmaxf(m[e], mx[e]) : m[e];
             mu[e] = mn == -INFINITY ? 0.f : mn;
             alpha[e] = mn == -INFINITY ? 1.f : exp2_approx(m[e] - mu[e]);
             m[e] = mn;
@@ -460,6 +550,12 @@ __global__ void __launch_bounds__(DecodeCfg<BITS, D>::W * 32, 1) decode_quant_ke
 #pragma unroll
             for (int e = 0; e < 4; ++e)
                 p[e] = exp2_approx(s[mt][e] - mu[e & 1]);
+            if (!all_heads) {
+                p[0] = act0 ? p[0] : 0.f;
+                p[1] = act1 ? p[1] : 0.f;
+                p[2] = act0 ? p[2] : 0.f;
+                p[3] = act1 ? p[3] : 0.f;
+            }
             l[0] += p[0] + p[2];
             l[1] += p[1] + p[3];
             uint32_t v0[VW], v1[VW], v2[VW], v3[VW];
@@ -482,13 +578,10 @@ __global__ void __launch_bounds__(DecodeCfg<BITS, D>::W * 32, 1) decode_quant_ke
                 const float za = kv_zero(vp[mt][0][gr]), zb = kv_zero(vp[mt][1][gr]);
                 const uint32_t b0 = movmatrix(pack_half2(pu[0] * sa, pu[1] * sa));
                 const uint32_t b1 = movmatrix(pack_half2(pu[2] * sb, pu[3] * sb));
-                if (all_heads) {
+                if (act0)                           // a NaN of V stays out of heads that left the block out
                     zacc[gr][0] = fmaf(p[0], za, fmaf(p[2], zb, zacc[gr][0]));
+                if (act1)
                     zacc[gr][1] = fmaf(p[1], za, fmaf(p[3], zb, zacc[gr][1]));
-                } else {                            // a NaN of V stays out of heads that left the block out
-                    zacc[gr][0] = fmaf(p[0], act0 ? za : 0.f, fmaf(p[2], act0 ? zb : 0.f, zacc[gr][0]));
-                    zacc[gr][1] = fmaf(p[1], act1 ? za : 0.f, fmaf(p[3], act1 ? zb : 0.f, zacc[gr][1]));
-                }
                 if constexpr (BITS == 4) {
                     const unsigned sel = gr & 1 ? 0x7632u : 0x5410u;
                     uint32_t x01 = __byte_perm(v0[gr / 2], v1[gr / 2], sel), x23 = __byte_perm(v2[gr / 2], v3[gr / 2], sel);

@@ -87,6 +87,19 @@ __device__ __forceinline__ void bulk_copy(uint32_t dst, const void *src, uint32_
                  : "memory");
 }
 
+// Weight of a part (maximum m, sum l) in the whole (maximum M), all in log2 units.
+// A part that saw only NaN has no maximum but a sum; one that saw nothing has neither.
+__device__ __forceinline__ float split_weight(float m, float l, float M)
+{
+    return m == -INFINITY ? (l == 0.f ? 0.f : l) : exp2_approx(m - M);
+}
+
+// Natural log of l 2^M; -inf where nothing was active.
+__device__ __forceinline__ float log_sum(float M, float l)
+{
+    return l == 0.f ? -INFINITY : ((M == -INFINITY ? 0.f : M) + __log2f(l)) * 0.69314718055994530942f;
+}
+
 template <int N>
 __device__ __forceinline__ void load_words(uint32_t (&w)[N], const uint8_t *p)
 {
@@ -114,78 +127,64 @@ __device__ __forceinline__ void load_words(uint32_t (&w)[N], const uint8_t *p)
 // a V fragment reads at once differ in the bits its swizzle uses.
 __device__ __forceinline__ int tile_token(int r) { return r ^ ((r >> 1) & 1); }
 
-// The B operand of the scores for head gid (0 where there is none): K's code
-// order, in fp16 times 2^qe; qz: the group sums as the B operand that takes K's
-// params as they lie, (s, z) of group tig, so 0 for s and the sum for z, in
-// three bf16 parts (rows 2 tig, 2 tig + 1 of the hi, mid and lo operand);
-// qinv: 2^-qe of heads 2 tig, 2 tig + 1.  One warp.
+// q of one head for the MMAs, by one warp: its elements in fp16 times 2^qe, in
+// the order of the codes' operands (at 4 bits a word's elements 0,4,1,5,2,6,3,7
+// with the odd ones times 2^-4, as the codes' masks give them), its group sums in
+// three bf16 parts (for the products with z), and 2^-qe.
 template <int D>
-constexpr int kQWords = D / 8 + 5;                  // words of a lane: odd multiples keep the banks apart
+struct HeadQ {
+    uint16_t f16[D];
+    uint16_t sum[3][4];
+    float inv;
+    uint32_t pad;
+};
 
 template <int BITS, int D>
-__device__ __forceinline__ void q_fragments(const __nv_bfloat16 *qp, bool have, int lane, uint32_t (&qf)[D / 16][2],
-                                            uint32_t (&qz)[3], float (&qinv)[2])
+__device__ __forceinline__ void prepare_q(const __nv_bfloat16 *qp, int lane, HeadQ<D> *out)
 {
-    constexpr int KS = D / 16, NG = KvFmt<BITS, D>::NG;
-    const int tig = lane & 3;
-    float f[KS * 4];                                // this lane's elements, in its K words' order
-#pragma unroll
-    for (int i = 0; i < KS; ++i) {                  // four elements at a time
-        const int e = BITS == 4 ? 32 * (i / 2) + 8 * tig + 4 * (i % 2) : 16 * i + 4 * tig;
-        uint2 u = make_uint2(0u, 0u);
-        if (have)
-            u = __ldg(reinterpret_cast<const uint2 *>(qp + e));
-        f[4 * i] = __uint_as_float(u.x << 16);
-        f[4 * i + 1] = __uint_as_float(u.x & 0xFFFF0000u);
-        f[4 * i + 2] = __uint_as_float(u.y << 16);
-        f[4 * i + 3] = __uint_as_float(u.y & 0xFFFF0000u);
+    constexpr int N = D / 32, GL = KvFmt<BITS, D>::G / N;   // elements of a lane, lanes of a group
+    float f[N];
+    if constexpr (N == 4) {
+        const uint2 u = qp != nullptr ? __ldg(reinterpret_cast<const uint2 *>(qp) + lane) : make_uint2(0u, 0u);
+        f[0] = __uint_as_float(u.x << 16);
+        f[1] = __uint_as_float(u.x & 0xFFFF0000u);
+        f[2] = __uint_as_float(u.y << 16);
+        f[3] = __uint_as_float(u.y & 0xFFFF0000u);
+    } else {
+        const uint32_t u = qp != nullptr ? __ldg(reinterpret_cast<const uint32_t *>(qp) + lane) : 0u;
+        f[0] = __uint_as_float(u << 16);
+        f[1] = __uint_as_float(u & 0xFFFF0000u);
     }
     float mx = 0.f;
 #pragma unroll
-    for (int i = 0; i < KS * 4; ++i)
+    for (int i = 0; i < N; ++i)
         mx = fmaxf(mx, fabsf(f[i]));
-    mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
-    mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
-    // max |q| 2^qe in [2^14, 2^15); no scaling for 0 and infinity
-    const int eb = (int)(__float_as_uint(mx) >> 23);
-    const int qe = mx == 0.f || eb == 255 ? 0 : min(141 - eb, 126);
-    const float up = pow2_field(127 + qe), down = pow2_field(127 - qe);
+    // max |q| 2^qe in [2^14, 2^15) where 2^qe is a float; no scaling for infinity
+    const int eb = (int)(__reduce_max_sync(0xffffffffu, __float_as_uint(mx)) >> 23);
+    const int qe = eb == 255 ? 0 : min(141 - eb, 126);
+    const float up = pow2_field(127 + qe);
+    float s = 0.f;
 #pragma unroll
-    for (int i = 0; i < KS * 4; ++i)
+    for (int i = 0; i < N; ++i) {
         f[i] *= up;
-    float sum = 0.f;                                // of group tig
-#pragma unroll
-    for (int gr = 0; gr < NG; ++gr) {
-        float s = 0.f;
-#pragma unroll
-        for (int i = 0; i < KS * 4 / NG; ++i)
-            s += f[gr * (KS * 4 / NG) + i];
-        s += __shfl_xor_sync(0xffffffffu, s, 1);
-        s += __shfl_xor_sync(0xffffffffu, s, 2);
-        sum = gr == tig ? s * 5.9604644775390625e-8f : sum;         // 2^-24: the unit of the codes' products
+        s += f[i];
+        const int e = N * lane + i;
+        const int at = BITS == 4 ? (e & ~7) + (e & 3) * 2 + (e >> 2 & 1) : e;
+        out->f16[at] = __half_as_ushort(__float2half_rn(BITS == 4 && e & 1 ? f[i] * 0.0625f : f[i]));
     }
 #pragma unroll
-    for (int i = 0; i < 3; ++i) {
-        const __nv_bfloat16 part = __float2bfloat16_rn(sum);
-        qz[i] = (uint32_t)__bfloat16_as_ushort(part) << 16;
-        sum -= __bfloat162float(part);
-    }
+    for (int off = 1; off < GL; off <<= 1)
+        s += __shfl_xor_sync(0xffffffffu, s, off);
+    s *= 5.9604644775390625e-8f;                    // 2^-24: the unit of the codes' products
+    if (lane % GL == 0)
 #pragma unroll
-    for (int u = 0; u < 2; ++u)
-        qinv[u] = __shfl_sync(0xffffffffu, down, (2 * tig + u) * 4);
-    // operand pairs as the codes' masks give them: at 4 bits elements (0,4),
-    // (1,5) 2^4, (2,6), (3,7) 2^4 of a word, so the second is taken 2^-4
-#pragma unroll
-    for (int i = 0; i < KS; ++i) {
-        if (BITS == 4) {
-            const float *w = f + 8 * (i / 2) + 2 * (i % 2);
-            qf[i][0] = pack_half2(w[0], w[4]);
-            qf[i][1] = pack_half2(w[1] * 0.0625f, w[5] * 0.0625f);
-        } else {
-            qf[i][0] = pack_half2(f[4 * i], f[4 * i + 1]);
-            qf[i][1] = pack_half2(f[4 * i + 2], f[4 * i + 3]);
+        for (int i = 0; i < 3; ++i) {
+            const __nv_bfloat16 part = __float2bfloat16_rn(s);
+            out->sum[i][lane / GL] = __bfloat16_as_ushort(part);
+            s -= __bfloat162float(part);
         }
-    }
+    if (lane == 0)
+        out->inv = pow2_field(127 - qe);
 }
 
 struct DecodeArgs {
@@ -223,11 +222,11 @@ __global__ void __launch_bounds__(DecodeCfg<BITS, D>::W * 32, 1) decode_quant_ke
     constexpr int UPG = KS / NG;                    // MMAs of a group
     extern __shared__ __align__(128) uint8_t ring[];
     __shared__ __align__(8) uint64_t s_bar[W * ST];
-    __shared__ float2 s_ml[W][kHeads];
+    __shared__ float2 s_ml[W][kHeads], s_sum[kHeads];
     __shared__ uint32_t s_words[kMaxNb / 32];
     __shared__ int s_page[kListMax];
     __shared__ uint16_t s_block[kListMax];
-    __shared__ uint32_t s_q[32 * kQWords<D>];
+    __shared__ __align__(16) HeadQ<D> s_q[kHeads];
 
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int gid = lane >> 2, tig = lane & 3;
@@ -247,23 +246,9 @@ __global__ void __launch_bounds__(DecodeCfg<BITS, D>::W * 32, 1) decode_quant_ke
         fence_mbar_init();
     }
 
-    // ---- q, by one warp for all of them
-    uint32_t qf[KS][2], qz[3];
-    float qinv[2];
-    if (warp == W - 1) {
-        q_fragments<BITS, D>(a.q_tok + ((long long)b * a.Hq + h0 + gid) * D, gid < gt, lane, qf, qz, qinv);
-        uint32_t *to = s_q + lane * kQWords<D>;
-#pragma unroll
-        for (int i = 0; i < KS; ++i) {
-            to[2 * i] = qf[i][0];
-            to[2 * i + 1] = qf[i][1];
-        }
-#pragma unroll
-        for (int i = 0; i < 3; ++i)
-            to[2 * KS + i] = qz[i];
-        to[2 * KS + 3] = __float_as_uint(qinv[0]);
-        to[2 * KS + 4] = __float_as_uint(qinv[1]);
-    }
+    // ---- q, a warp per head (0 where there is none)
+    if (warp < kHeads)
+        prepare_q<BITS, D>(warp < gt ? a.q_tok + ((long long)b * a.Hq + h0 + warp) * D : nullptr, lane, &s_q[warp]);
 
     // ---- union of the heads' active blocks, one bit each: kMaskWords words of 32
     // blocks a warp at a time, all their loads (the table's too, and the first
@@ -273,25 +258,29 @@ __global__ void __launch_bounds__(DecodeCfg<BITS, D>::W * 32, 1) decode_quant_ke
     int page[kMaskWords];
     for (int c0 = warp; c0 < (c0 == warp ? (a.nb + 31) / 32 : nwords); c0 += kMaskWords * W) {
         int raw[kMaskWords][kHeads], any[kMaskWords], pg[kMaskWords];
-        // no branch between the loads: blocks past the row and heads past the tile
-        // read the last one again
+        // (blocks past the row read its last one: the branches are the warp's)
 #pragma unroll
         for (int i = 0; i < kMaskWords; ++i) {
+            any[i] = pg[i] = 0;
+            if (i > 0 && (c0 + i * W) * 32 >= a.nb)
+                continue;
             const int j = min((c0 + i * W) * 32 + lane, a.nb - 1);
 #pragma unroll
-            for (int h = 0; h < kHeads; ++h)
-                raw[i][h] = __ldg(mrow + (long long)min(h, gt - 1) * a.nb + j);
+            for (int h = 0; h < kHeads; ++h) {
+                raw[i][h] = 0;
+                if (h < gt)
+                    raw[i][h] = __ldg(mrow + (long long)h * a.nb + j);
+            }
             pg[i] = b * a.kv.max_blocks + j;
             if (a.kv.table != nullptr)
                 pg[i] = __ldg(a.kv.table + pg[i]);
         }
 #pragma unroll
-        for (int i = 0; i < kMaskWords; ++i) {
-            any[i] = 0;
+        for (int i = 0; i < kMaskWords; ++i)
+            if (i == 0 || (c0 + i * W) * 32 < a.nb)
 #pragma unroll
-            for (int h = 0; h < kHeads; ++h)
-                any[i] |= raw[i][h];
-        }
+                for (int h = 0; h < kHeads; ++h)
+                    any[i] |= raw[i][h];
 #pragma unroll
         for (int i = 0; i < kMaskWords; ++i) {
             if ((c0 + i * W) * 32 + lane >= nblk)
@@ -308,19 +297,32 @@ __global__ void __launch_bounds__(DecodeCfg<BITS, D>::W * 32, 1) decode_quant_ke
         }
     }
     __syncthreads();
-    if (warp != W - 1) {
-        const uint32_t *from = s_q + lane * kQWords<D>;
+    uint32_t qf[KS][2], qz[3];                      // operands of column gid
+    {
+        const HeadQ<D> &q = s_q[gid];
 #pragma unroll
-        for (int i = 0; i < KS; ++i) {
-            qf[i][0] = from[2 * i];
-            qf[i][1] = from[2 * i + 1];
+        for (int i = 0; i < KS; i += 2) {
+            if (BITS == 4) {                        // a word's eight elements: two MMA steps
+                const uint4 u = *reinterpret_cast<const uint4 *>(q.f16 + 16 * i + 8 * tig);
+                qf[i][0] = u.x;
+                qf[i][1] = u.y;
+                qf[i + 1][0] = u.z;
+                qf[i + 1][1] = u.w;
+            } else {
+#pragma unroll
+                for (int k = 0; k < 2; ++k) {
+                    const uint2 u = *reinterpret_cast<const uint2 *>(q.f16 + 16 * (i + k) + 4 * tig);
+                    qf[i + k][0] = u.x;
+                    qf[i + k][1] = u.y;
+                }
+            }
         }
+        // the params' operand is (s, z) of group tig: 0 for s and the sum for z
 #pragma unroll
         for (int i = 0; i < 3; ++i)
-            qz[i] = from[2 * KS + i];
-        qinv[0] = __uint_as_float(from[2 * KS + 3]);
-        qinv[1] = __uint_as_float(from[2 * KS + 4]);
+            qz[i] = tig < NG ? (uint32_t)q.sum[i][tig] << 16 : 0u;
     }
+    const float qinv[2] = {s_q[2 * tig].inv, s_q[2 * tig + 1].inv};
 
     // ---- this split's blocks: ranks [r0, r1) of the union
     int r0, r1;
@@ -642,20 +644,30 @@ __global__ void __launch_bounds__(DecodeCfg<BITS, D>::W * 32, 1) decode_quant_ke
                 }
     }
     __syncthreads();
+    if (warp < gt) {                                // the warps' weights for head `warp`
+        const float2 ml = lane < W ? s_ml[lane][warp] : make_float2(-INFINITY, 0.f);
+        float M = ml.x;
+#pragma unroll
+        for (int off = 16; off >= 1; off >>= 1)
+            M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, off));
+        const float wt = split_weight(ml.x, ml.y, M);
+        float lt = wt * ml.y;
+#pragma unroll
+        for (int off = 16; off >= 1; off >>= 1)
+            lt += __shfl_xor_sync(0xffffffffu, lt, off);
+        if (lane < W)
+            s_ml[lane][warp].x = wt;
+        if (lane == 0)
+            s_sum[warp] = make_float2(M, lt);
+    }
+    __syncthreads();
     for (int i = threadIdx.x; i < gt * D; i += W * 32) {
         const int hh = i / D, c = i % D;
-        float M = -INFINITY;
-#pragma unroll
-        for (int w = 0; w < W; ++w)
-            M = fmaxf(M, s_ml[w][hh].x);
-        const float Mu = M == -INFINITY ? 0.f : M;
-        float sum = 0.f, lt = 0.f;
+        const float lt = s_sum[hh].y;
+        float sum = 0.f;
 #pragma unroll
         for (int w = 0; w < W; ++w) {
-            const float2 ml = s_ml[w][hh];
-            // a warp that saw only NaN has no maximum but a sum; one that saw nothing has neither
-            const float wt = ml.x == -INFINITY ? (ml.y == 0.f ? 0.f : ml.y) : exp2_approx(ml.x - Mu);
-            lt = fmaf(wt, ml.y, lt);
+            const float wt = s_ml[w][hh].x;
             if (wt != 0.f)
                 sum = fmaf(wt, *reinterpret_cast<const float *>(ring + w * ST * F::HALF + i * 4), sum);
         }
@@ -663,12 +675,12 @@ __global__ void __launch_bounds__(DecodeCfg<BITS, D>::W * 32, 1) decode_quant_ke
         if (a.nsplit == 1) {
             a.o[bh * D + c] = __float2bfloat16_rn(lt == 0.f ? 0.f : sum / lt);
             if (c == 0 && a.lse != nullptr)
-                a.lse[bh] = lt == 0.f ? -INFINITY : (Mu + __log2f(lt)) * 0.69314718055994530942f;
+                a.lse[bh] = log_sum(s_sum[hh].x, lt);
         } else {
             float *out = a.part + (bh * a.nsplit + split) * (D + 2);
             out[c] = sum;
             if (c == 0) {
-                out[D] = M;
+                out[D] = s_sum[hh].x;
                 out[D + 1] = lt;
             }
         }
@@ -696,11 +708,10 @@ __global__ void __launch_bounds__(D)
 #pragma unroll
     for (int off = 16; off >= 1; off >>= 1)
         M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, off));
-    const float mu = M == -INFINITY ? 0.f : M;
     float l = 0.f;
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
-        const float w = ms[i] == -INFINITY ? (ls[i] == 0.f ? 0.f : ls[i]) : exp2_approx(ms[i] - mu);
+        const float w = split_weight(ms[i], ls[i], M);
         l = fmaf(w, ls[i], l);
         if (threadIdx.x < 32 && lane + 32 * i < nsplit)
             s_w[lane + 32 * i] = w;
@@ -715,7 +726,7 @@ __global__ void __launch_bounds__(D)
         acc = fmaf(s_w[s], pp[s * (D + 2) + threadIdx.x], acc);
     o[bh * D + threadIdx.x] = __float2bfloat16_rn(l == 0.f ? 0.f : acc / l);
     if (lse != nullptr && threadIdx.x == 0)
-        lse[bh] = l == 0.f ? -INFINITY : (mu + __log2f(l)) * 0.69314718055994530942f;
+        lse[bh] = log_sum(M, l);
 }
 
 // Splits of a unit (a KV head's head tile): the fewest whose grid fills 97 % of

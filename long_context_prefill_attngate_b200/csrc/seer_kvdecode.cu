@@ -39,7 +39,7 @@ namespace seer {
 namespace {
 
 constexpr int kHeads = 8;                 // query heads of a CTA: the N of the MMA
-constexpr int kListMax = 2049;            // blocks of a split (decode_quant_splits)
+constexpr int kListMax = 513;             // blocks of a split (decode_quant_splits)
 
 __device__ __forceinline__ float exp2_approx(float x)
 {
@@ -51,15 +51,32 @@ __device__ __forceinline__ float exp2_approx(float x)
 __device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                          uint32_t b1)
 {
-    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
                  : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
                  : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+// The first product of a sum: no accumulator to clear.
+__device__ __forceinline__ void mma16816_0(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                           uint32_t b1)
+{
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
+        : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
+}
+
+__device__ __forceinline__ void mma16816_bf16_0(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                                uint32_t b0, uint32_t b1)
+{
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
+        : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
 }
 
 __device__ __forceinline__ void mma16816_bf16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
                                               uint32_t b0, uint32_t b1)
 {
-    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
                  : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
                  : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
@@ -201,18 +218,19 @@ struct DecodeArgs {
     uint64_t timeout_ns;
 };
 
-// Warps of a CTA and half records in flight per warp: one CTA per SM whose ring
-// holds two to four tokens' worth of latency (the SM's share of HBM is 24 bytes
-// a cycle, some 36 KB in flight).
+// Warps of a CTA and half records in flight per warp.  Two CTAs share an SM, so
+// that one's start and end (some 8,000 cycles of latencies) pass under the
+// other's products; their rings hold 70 to 200 KB, where the SM's share of HBM
+// (24 bytes a cycle) needs some 40 KB in flight.
 template <int BITS, int D>
 struct DecodeCfg {
-    static constexpr int W = BITS == 8 && D == 128 ? 12 : 16;
+    static constexpr int W = BITS == 8 && D == 128 ? 6 : 8;
     static constexpr int ST = BITS == 4 && D == 64 ? 4 : 2;
     static constexpr int ring = W * ST * KvFmt<BITS, D>::HALF;
 };
 
 template <int BITS, int D>
-__global__ void __launch_bounds__(DecodeCfg<BITS, D>::W * 32, 1) decode_quant_kernel(const DecodeArgs a)
+__global__ void __launch_bounds__(DecodeCfg<BITS, D>::W * 32, 2) decode_quant_kernel(const DecodeArgs a)
 {
     using F = KvFmt<BITS, D>;
     using C = DecodeCfg<BITS, D>;
@@ -224,7 +242,7 @@ __global__ void __launch_bounds__(DecodeCfg<BITS, D>::W * 32, 1) decode_quant_ke
     __shared__ __align__(8) uint64_t s_bar[W * ST];
     __shared__ float2 s_ml[W][kHeads], s_sum[kHeads];
     __shared__ uint32_t s_words[kMaxNb / 32];
-    __shared__ int s_page[kListMax];
+    __shared__ uint32_t s_rec[kListMax];            // a block's record from the start of the pages, in 512 bytes
     __shared__ uint16_t s_block[kListMax];
     __shared__ __align__(16) HeadQ<D> s_q[kHeads];
 
@@ -247,8 +265,8 @@ __global__ void __launch_bounds__(DecodeCfg<BITS, D>::W * 32, 1) decode_quant_ke
     }
 
     // ---- q, a warp per head (0 where there is none)
-    if (warp < kHeads)
-        prepare_q<BITS, D>(warp < gt ? a.q_tok + ((long long)b * a.Hq + h0 + warp) * D : nullptr, lane, &s_q[warp]);
+    for (int h = warp; h < kHeads; h += W)
+        prepare_q<BITS, D>(h < gt ? a.q_tok + ((long long)b * a.Hq + h0 + h) * D : nullptr, lane, &s_q[h]);
 
     // ---- union of the heads' active blocks, one bit each: kMaskWords words of 32
     // blocks a warp at a time, all their loads (the table's too, and the first
@@ -350,9 +368,9 @@ __global__ void __launch_bounds__(DecodeCfg<BITS, D>::W * 32, 1) decode_quant_ke
             if ((w >> lane & 1u) && r >= r0 && r < r1) {
                 const int j = c * 32 + lane;
                 s_block[r - r0] = (uint16_t)j;
-                s_page[r - r0] = pg >= 0 ? pg
-                                 : a.kv.table != nullptr ? __ldg(a.kv.table + (long long)b * a.kv.max_blocks + j)
-                                                         : b * a.kv.max_blocks + j;
+                if (pg < 0)
+                    pg = a.kv.table != nullptr ? __ldg(a.kv.table + b * a.kv.max_blocks + j) : b * a.kv.max_blocks + j;
+                s_rec[r - r0] = ((uint32_t)pg * a.Hkv + kvh) * (F::REC / 512);
             }
         };
 #pragma unroll
@@ -366,12 +384,13 @@ __global__ void __launch_bounds__(DecodeCfg<BITS, D>::W * 32, 1) decode_quant_ke
 
     const int n_units = 2 * (r1 - r0);              // half records
     uint8_t *my = ring + warp * ST * F::HALF;
+    const uint32_t my_bar = smem_u32(&s_bar[warp * ST]);
     auto issue = [&](int u, int st) {               // lane 0
         if (u >= n_units || 64 * s_block[u >> 1] + 32 * (u & 1) >= len)
             return;
-        const uint32_t bar = smem_u32(&s_bar[warp * ST + st]);
-        mbar_arrive_expect_tx(bar, F::HALF);
-        bulk_copy(smem_u32(my + st * F::HALF), kv_half<F>(a.kv, a.Hkv, s_page[u >> 1], kvh, u & 1), F::HALF, bar);
+        mbar_arrive_expect_tx(my_bar + 8 * st, F::HALF);
+        bulk_copy(smem_u32(my + st * F::HALF), a.kv.pages + (unsigned long long)s_rec[u >> 1] * 512 + (u & 1) * F::HALF,
+                  F::HALF, my_bar + 8 * st);
     };
     auto head_byte = [&](int u) {
         return u < n_units && lane < gt ? (int)__ldg(mrow + (long long)lane * a.nb + s_block[u >> 1]) : 0;
@@ -390,6 +409,15 @@ __global__ void __launch_bounds__(DecodeCfg<BITS, D>::W * 32, 1) decode_quant_ke
         zacc[gr][0] = zacc[gr][1] = 0.f;
     const float to_log2 = a.scale_log2 * 16777216.f;    // 2^24
 
+    // this lane's places in a half record: K row and params of tile row gid (row
+    // gid + 8 and the second tile a whole number of rows further, with the same
+    // swizzle), V words of tile columns 2 tig and 2 tig + 1
+    const int tr = tile_token(gid), t0 = tile_token(2 * tig), t1 = tile_token(2 * tig + 1);
+    const int at_k = tr * R + (BITS == 8 && D == 128 ? (tr & 1) * 64 + tig * 16 : tig * (R / 4));
+    const int at_p = tr * F::PAR, at_z = F::kParK + at_p + (tig < NG ? tig * 4 : 0);
+    const int at_v0 = F::kCodeV + t0 * R + (gid ^ F::v_swizzle(t0)) * (R / 8);
+    const int at_v1 = F::kCodeV + t1 * R + (gid ^ F::v_swizzle(t1)) * (R / 8);
+
     int mb = head_byte(warp);
     int it = 0;
     for (int u = warp; u < n_units; u += W, ++it) {
@@ -400,7 +428,7 @@ __global__ void __launch_bounds__(DecodeCfg<BITS, D>::W * 32, 1) decode_quant_ke
             break;                                  // the empty half of the last block: nothing follows
         const int st = it % ST;
         {
-            const uint32_t bar = smem_u32(&s_bar[warp * ST + st]), parity = (it / ST) & 1;
+            const uint32_t bar = my_bar + 8 * st, parity = (it / ST) & 1;
             bool done = mbar_test_wait(bar, parity);
             if (!done) {
                 const uint64_t t0 = globaltimer();
@@ -414,7 +442,7 @@ __global__ void __launch_bounds__(DecodeCfg<BITS, D>::W * 32, 1) decode_quant_ke
                     const int w = it + s;
                     const int uu = warp + w * W;
                     if (uu < n_units && 64 * s_block[uu >> 1] + 32 * (uu & 1) < len)
-                        mbar_drain(smem_u32(&s_bar[warp * ST + w % ST]), (w / ST) & 1, 200000000ull);
+                        mbar_drain(my_bar + 8 * (w % ST), (w / ST) & 1, 200000000ull);
                 }
                 m[0] = m[1] = -INFINITY;
                 l[0] = l[1] = 0.f;
@@ -427,45 +455,54 @@ __global__ void __launch_bounds__(DecodeCfg<BITS, D>::W * 32, 1) decode_quant_ke
         float s[2][4];
 #pragma unroll
         for (int mt = 0; mt < 2; ++mt) {
-            const int ra = 16 * mt + tile_token(gid), rb = ra + 8;
+            const uint8_t *ha = h + at_k + 16 * mt * R, *hp = h + F::kParK + at_p + 16 * mt * F::PAR;
             uint32_t ka[KW], kb[KW], pa[NG], pb[NG];
-            if constexpr (BITS == 8 && D == 128) {
+            if constexpr (BITS == 8 && D == 128) {  // the other half of the row is 64 bytes up or down
                 uint32_t (&a0)[4] = *reinterpret_cast<uint32_t (*)[4]>(ka);
                 uint32_t (&a1)[4] = *reinterpret_cast<uint32_t (*)[4]>(ka + 4);
                 uint32_t (&b0)[4] = *reinterpret_cast<uint32_t (*)[4]>(kb);
                 uint32_t (&b1)[4] = *reinterpret_cast<uint32_t (*)[4]>(kb + 4);
-                load_words(a0, h + ra * R + (ra & 1) * 64 + tig * 16);
-                load_words(a1, h + ra * R + (~ra & 1) * 64 + tig * 16);
-                load_words(b0, h + rb * R + (rb & 1) * 64 + tig * 16);
-                load_words(b1, h + rb * R + (~rb & 1) * 64 + tig * 16);
+                const uint8_t *hb = ha + (tr & 1 ? -64 : 64);
+                load_words(a0, ha);
+                load_words(a1, hb);
+                load_words(b0, ha + 8 * R);
+                load_words(b1, hb + 8 * R);
             } else {
-                load_words(ka, h + ra * R + tig * (R / 4));
-                load_words(kb, h + rb * R + tig * (R / 4));
+                load_words(ka, ha);
+                load_words(kb, ha + 8 * R);
             }
-            load_words(pa, h + F::kParK + ra * F::PAR);
-            load_words(pb, h + F::kParK + rb * F::PAR);
-            s[mt][0] = s[mt][1] = s[mt][2] = s[mt][3] = 0.f;
+            load_words(pa, hp);
+            load_words(pb, hp + 8 * F::PAR);
             {                                       // z sum(q) of the groups: the params themselves are the operand
-                const uint32_t wa = tig < NG ? *reinterpret_cast<const uint32_t *>(h + F::kParK + ra * F::PAR + tig * 4) : 0u;
-                const uint32_t wb = tig < NG ? *reinterpret_cast<const uint32_t *>(h + F::kParK + rb * F::PAR + tig * 4) : 0u;
-                mma16816_bf16(s[mt], wa, wb, wa, wb, qz[0], qz[1]);
+                                                    // (lanes past the last group: their q sums are 0)
+                const uint32_t wa = *reinterpret_cast<const uint32_t *>(h + at_z + 16 * mt * F::PAR);
+                const uint32_t wb = *reinterpret_cast<const uint32_t *>(h + at_z + (16 * mt + 8) * F::PAR);
+                mma16816_bf16_0(s[mt], wa, wb, wa, wb, qz[0], qz[1]);
                 mma16816_bf16(s[mt], wa, wb, 0u, 0u, qz[2], 0u);
             }
 #pragma unroll
             for (int gr = 0; gr < NG; ++gr) {
-                float c[4] = {0.f, 0.f, 0.f, 0.f};
+                float c[4];
 #pragma unroll
                 for (int i = 0; i < UPG; ++i) {
                     const int ks = gr * UPG + i;
+                    uint32_t x[4];
                     if (BITS == 4) {
                         const uint32_t wa = ka[ks / 2] >> (8 * (ks % 2)), wb = kb[ks / 2] >> (8 * (ks % 2));
-                        mma16816(c, wa & 0x000F000Fu, wb & 0x000F000Fu, wa & 0x00F000F0u, wb & 0x00F000F0u, qf[ks][0],
-                                 qf[ks][1]);
+                        x[0] = wa & 0x000F000Fu;
+                        x[1] = wb & 0x000F000Fu;
+                        x[2] = wa & 0x00F000F0u;
+                        x[3] = wb & 0x00F000F0u;
                     } else {
-                        const uint32_t wa = ka[ks], wb = kb[ks];
-                        mma16816(c, __byte_perm(wa, 0u, 0x4140), __byte_perm(wb, 0u, 0x4140),
-                                 __byte_perm(wa, 0u, 0x4342), __byte_perm(wb, 0u, 0x4342), qf[ks][0], qf[ks][1]);
+                        x[0] = __byte_perm(ka[ks], 0u, 0x4140);
+                        x[1] = __byte_perm(kb[ks], 0u, 0x4140);
+                        x[2] = __byte_perm(ka[ks], 0u, 0x4342);
+                        x[3] = __byte_perm(kb[ks], 0u, 0x4342);
                     }
+                    if (i == 0)
+                        mma16816_0(c, x[0], x[1], x[2], x[3], qf[ks][0], qf[ks][1]);
+                    else
+                        mma16816(c, x[0], x[1], x[2], x[3], qf[ks][0], qf[ks][1]);
                 }
                 const float sa = kv_scale(pa[gr]), sb = kv_scale(pb[gr]);
                 s[mt][0] = fmaf(sa, c[0], s[mt][0]);
@@ -484,7 +521,7 @@ __global__ void __launch_bounds__(DecodeCfg<BITS, D>::W * 32, 1) decode_quant_ke
             for (int mt = 0; mt < 2; ++mt)
 #pragma unroll
                 for (int e = 0; e < 4; ++e)
-                    if (16 * mt + tile_token(gid) + (e & 2) * 4 >= keys)
+                    if (16 * mt + tr + (e & 2) * 4 >= keys)
                         s[mt][e] = -INFINITY;
         }
 
@@ -494,19 +531,25 @@ __global__ void __launch_bounds__(DecodeCfg<BITS, D>::W * 32, 1) decode_quant_ke
 #pragma unroll
         for (int mt = 0; mt < 2; ++mt)
 #pragma unroll
-            for (int hf = 0; hf < 2; ++hf) {
-                const int t = 16 * mt + tile_token(gid) + 8 * hf;
-                load_words(vp[mt][hf], h + F::kParV + t * F::PAR);
-                if (keys < 32 && t >= keys)
+            for (int hf = 0; hf < 2; ++hf)
+                load_words(vp[mt][hf], h + F::kParV + at_p + (16 * mt + 8 * hf) * F::PAR);
+        if (keys < 32)
+#pragma unroll
+            for (int mt = 0; mt < 2; ++mt)
+#pragma unroll
+                for (int hf = 0; hf < 2; ++hf)
 #pragma unroll
                     for (int gr = 0; gr < NG; ++gr)
-                        vp[mt][hf][gr] = 0u;
-                if constexpr (NG == 1)
-                    vmax = __vmaxu2(vmax, vp[mt][hf][0]);
+                        if (16 * mt + tr + 8 * hf >= keys)
+                            vp[mt][hf][gr] = 0u;
 #pragma unroll
-                for (int gr = 0; gr + 1 < NG; gr += 2)
-                    vmax = __vimax3_u16x2(vmax, vp[mt][hf][gr], vp[mt][hf][gr + 1]);
-            }
+        for (int i = 0; i < 4; ++i) {
+            if constexpr (NG == 1)
+                vmax = __vmaxu2(vmax, vp[i / 2][i % 2][0]);
+#pragma unroll
+            for (int gr = 0; gr + 1 < NG; gr += 2)
+                vmax = __vimax3_u16x2(vmax, vp[i / 2][i % 2][gr], vp[i / 2][i % 2][gr + 1]);
+        }
         float mx[2];
 #pragma unroll
         for (int e = 0; e < 2; ++e)
@@ -561,15 +604,10 @@ __global__ void __launch_bounds__(DecodeCfg<BITS, D>::W * 32, 1) decode_quant_ke
             l[0] += p[0] + p[2];
             l[1] += p[1] + p[3];
             uint32_t v0[VW], v1[VW], v2[VW], v3[VW];
-            {
-                const int t0 = 16 * mt + tile_token(2 * tig), t1 = 16 * mt + tile_token(2 * tig + 1);
-                const int c0 = (gid ^ F::v_swizzle(t0)) * (R / 8), c1 = (gid ^ F::v_swizzle(t1)) * (R / 8);
-                const int c2 = (gid ^ F::v_swizzle(t0 + 8)) * (R / 8), c3 = (gid ^ F::v_swizzle(t1 + 8)) * (R / 8);
-                load_words(v0, h + F::kCodeV + t0 * R + c0);
-                load_words(v1, h + F::kCodeV + t1 * R + c1);
-                load_words(v2, h + F::kCodeV + (t0 + 8) * R + c2);
-                load_words(v3, h + F::kCodeV + (t1 + 8) * R + c3);
-            }
+            load_words(v0, h + at_v0 + 16 * mt * R);
+            load_words(v1, h + at_v1 + 16 * mt * R);
+            load_words(v2, h + at_v0 + (16 * mt + 8) * R);
+            load_words(v3, h + at_v1 + (16 * mt + 8) * R);
             float pu[4];
 #pragma unroll
             for (int e = 0; e < 4; ++e)
@@ -586,13 +624,13 @@ __global__ void __launch_bounds__(DecodeCfg<BITS, D>::W * 32, 1) decode_quant_ke
                     zacc[gr][1] = fmaf(p[1], za, fmaf(p[3], zb, zacc[gr][1]));
                 if constexpr (BITS == 4) {
                     const unsigned sel = gr & 1 ? 0x7632u : 0x5410u;
-                    uint32_t x01 = __byte_perm(v0[gr / 2], v1[gr / 2], sel), x23 = __byte_perm(v2[gr / 2], v3[gr / 2], sel);
+                    // lower rows: an element; upper rows: the byte, that element plus 16 times the next
+                    const uint32_t x01 = __byte_perm(v0[gr / 2], v1[gr / 2], sel), x23 = __byte_perm(v2[gr / 2], v3[gr / 2], sel);
 #pragma unroll
                     for (int i = 0; i < UPG; ++i) {
-                        mma16816(acc[gr * UPG + i], x01 & 0x000F000Fu, x01 & 0x00F000F0u, x23 & 0x000F000Fu,
-                                 x23 & 0x00F000F0u, b0, b1);
-                        x01 >>= 8;
-                        x23 >>= 8;
+                        const uint32_t y01 = i ? __byte_perm(x01, 0u, 0x4341) : x01 & 0x00FF00FFu;
+                        const uint32_t y23 = i ? __byte_perm(x23, 0u, 0x4341) : x23 & 0x00FF00FFu;
+                        mma16816(acc[gr * UPG + i], y01 & 0x000F000Fu, y01, y23 & 0x000F000Fu, y23, b0, b1);
                     }
                 } else {
 #pragma unroll
@@ -635,17 +673,20 @@ __global__ void __launch_bounds__(DecodeCfg<BITS, D>::W * 32, 1) decode_quant_ke
             for (int gr = 0; gr < NG; ++gr)
 #pragma unroll
                 for (int i = 0; i < UPG; i += 2) {
-                    float4 r;
-                    r.x = acc[gr * UPG + i][e] * un * 16777216.f + zacc[gr][e];
-                    r.y = acc[gr * UPG + i][e + 2] * un * (BITS == 4 ? 1048576.f : 16777216.f) + zacc[gr][e];
-                    r.z = acc[gr * UPG + i + 1][e] * un * 16777216.f + zacc[gr][e];
-                    r.w = acc[gr * UPG + i + 1][e + 2] * un * (BITS == 4 ? 1048576.f : 16777216.f) + zacc[gr][e];
+                    float v[4];
+#pragma unroll
+                    for (int k = 0; k < 2; ++k) {
+                        const float lo = acc[gr * UPG + i + k][e], hi = acc[gr * UPG + i + k][e + 2];
+                        v[2 * k] = lo * un * 16777216.f + zacc[gr][e];
+                        v[2 * k + 1] = (BITS == 4 ? (hi - lo) * un * 1048576.f : hi * un * 16777216.f) + zacc[gr][e];
+                    }
+                    const float4 r = make_float4(v[0], v[1], v[2], v[3]);
                     *reinterpret_cast<float4 *>(so + (2 * tig + e) * D + F::G * gr + gid * (F::G / 8) + 2 * i) = r;
                 }
     }
     __syncthreads();
-    if (warp < gt) {                                // the warps' weights for head `warp`
-        const float2 ml = lane < W ? s_ml[lane][warp] : make_float2(-INFINITY, 0.f);
+    for (int hh = warp; hh < gt; hh += W) {         // the warps' weights for a head
+        const float2 ml = lane < W ? s_ml[lane][hh] : make_float2(-INFINITY, 0.f);
         float M = ml.x;
 #pragma unroll
         for (int off = 16; off >= 1; off >>= 1)
@@ -656,9 +697,9 @@ __global__ void __launch_bounds__(DecodeCfg<BITS, D>::W * 32, 1) decode_quant_ke
         for (int off = 16; off >= 1; off >>= 1)
             lt += __shfl_xor_sync(0xffffffffu, lt, off);
         if (lane < W)
-            s_ml[lane][warp].x = wt;
+            s_ml[lane][hh].x = wt;
         if (lane == 0)
-            s_sum[warp] = make_float2(M, lt);
+            s_sum[hh] = make_float2(M, lt);
     }
     __syncthreads();
     for (int i = threadIdx.x; i < gt * D; i += W * 32) {
@@ -729,23 +770,30 @@ __global__ void __launch_bounds__(D)
         lse[bh] = log_sum(M, l);
 }
 
-// Splits of a unit (a KV head's head tile): the fewest whose grid fills 97 % of
-// its waves of one CTA per SM, else the best filling count; at least so many
-// that a split's block list fits.
+// Splits of a unit (a KV head's head tile): the count with the least estimated
+// time, in us, with half of the blocks active (the mask is on the device):
+//   a CTA's start and end     6 alone on its SM, 7.5 for two at once, per wave
+//   a block                   0.4 for a CTA alone, 0.31 of the SM for two
+//   the second kernel         2 and 0.04 a split
+// and at least a block for every second warp.  Measured (4 bits, D = 128): 8 units
+// of 512 blocks, all active: 9 splits 31.2 us, 18: 22.5, 36: 23.2; a tenth active: 15.7,
+// 13.4, 15.2; 128 units of 256: 1 split 104 us, 2: 89, 3: 96, 8: 94; 64 units of
+// 512 at most (a ragged batch): 2: 68, 4: 48, 6: 45, 12: 49.
 int decode_quant_splits(long long units, int nb, int sms)
 {
-    const int lo = (nb + kListMax - 2) / (kListMax - 1), cap = nb < kMaxDecodeSplits ? nb : kMaxDecodeSplits;
+    const int lo = (nb + kListMax - 2) / (kListMax - 1);              // a split's block list has to fit
+    const int cap = nb / 4 < kMaxDecodeSplits ? nb / 4 : kMaxDecodeSplits;
     int best = lo;
-    double best_eff = -1.0;
+    double best_us = 1e30;
     for (int ns = lo; ns <= cap; ++ns) {
-        const long long ctas = units * ns, waves = (ctas + sms - 1) / sms;
-        const double eff = (double)ctas / (double)(waves * sms);
-        if (eff > best_eff) {
-            best_eff = eff;
+        const long long ctas = units * ns, load = (ctas + sms - 1) / sms, waves = (load + 1) / 2;
+        const double blocks = 0.5 * nb / ns;
+        const double us = (load == 1 ? 6.0 + 0.4 * blocks : 7.5 * (double)waves + 0.31 * (double)load * blocks) +
+                          (ns > 1 ? 2.0 + 0.04 * ns : 0.0);
+        if (us < best_us) {
+            best_us = us;
             best = ns;
         }
-        if (eff >= 0.97)
-            break;
     }
     return best;
 }

@@ -210,6 +210,7 @@ struct DecodeArgs {
     const int32_t *lens;
     const uint8_t *mask;
     int Hq, Hkv, L, nb, tiles, per_tile, nsplit;
+    unsigned inv_split;
     float scale_log2;
     float *part;
     __nv_bfloat16 *o;
@@ -345,7 +346,8 @@ __global__ void __launch_bounds__(DecodeCfg<BITS, D>::W * 32, 2) decode_quant_ke
     // ---- this split's blocks: ranks [r0, r1) of the union
     int r0, r1;
     {
-        const int per = (nwords + 31) / 32;         // words of a lane
+        // words of a lane: a power of two (32 lanes cover the words)
+        const int lg = nwords > 32 ? 32 - __clz((nwords - 1) >> 5) : 0, per = 1 << lg;
         int cnt = 0;
         for (int k = 0; k < per; ++k)
             if (lane * per + k < nwords)
@@ -357,11 +359,15 @@ __global__ void __launch_bounds__(DecodeCfg<BITS, D>::W * 32, 2) decode_quant_ke
             inc += lane >= off ? v : 0;
         }
         const int total = __shfl_sync(0xffffffffu, inc, 31);
-        r0 = total * split / a.nsplit;
-        r1 = total * (split + 1) / a.nsplit;
+        // total * split / nsplit: at most 2^20, and inv_split is 2^32 / nsplit rounded
+        // up by less than 2^-26 of it, so the product's high word is the quotient
+        r0 = (int)__umulhi((unsigned)(total * split), a.inv_split);
+        r1 = split + 1 == a.nsplit ? total : (int)__umulhi((unsigned)(total * (split + 1)), a.inv_split);
+        if (a.nsplit == 1)
+            r0 = 0;
         auto list = [&](int c, int pg) {            // word c's blocks; pg < 0: look the page up
-            int base = __shfl_sync(0xffffffffu, inc - cnt, c / per);
-            for (int k = c / per * per; k < c; ++k)
+            int base = __shfl_sync(0xffffffffu, inc - cnt, c >> lg);
+            for (int k = c >> lg << lg; k < c; ++k)
                 base += __popc(s_words[k]);
             const unsigned w = s_words[c];
             const int r = base + __popc(w & ((1u << lane) - 1u));
@@ -815,6 +821,7 @@ cudaError_t launch(DecodeArgs a, int B, cudaStream_t stream)
         return e;
     const int units = B * a.Hkv * a.tiles;
     a.nsplit = decode_quant_splits(units, a.nb, sms);
+    a.inv_split = (unsigned)((0x100000000ull + a.nsplit - 1) / a.nsplit);     // (0 for one split, which has no use for it)
     decode_quant_kernel<BITS, D><<<dim3(a.nsplit, units), C::W * 32, C::ring, stream>>>(a);
     e = cudaGetLastError();
     if (e != cudaSuccess || a.nsplit == 1)

@@ -40,6 +40,7 @@ namespace {
 
 constexpr int kHeads = 8;                 // query heads of a CTA: the N of the MMA
 constexpr int kListMax = 513;             // blocks of a split (decode_quant_splits)
+constexpr int kNoPage = kMaxNb;           // flag of a list entry; block indices are below it
 
 __device__ __forceinline__ float exp2_approx(float x)
 {
@@ -269,50 +270,80 @@ __global__ void __launch_bounds__(DecodeCfg<BITS, D>::W * 32, 2) decode_quant_ke
     for (int h = warp; h < kHeads; h += W)
         prepare_q<BITS, D>(h < gt ? a.q_tok + ((long long)b * a.Hq + h0 + h) * D : nullptr, lane, &s_q[h]);
 
-    // ---- union of the heads' active blocks, one bit each: kMaskWords words of 32
-    // blocks a warp at a time, all their loads (the table's too, and the first
-    // ones before the length is known) in flight together
-    constexpr int kMaskWords = 4;
+    // ---- union of the heads' active blocks, one bit each.  Rows short enough for
+    // one round of kMaskWords words of 32 blocks a warp: a block a lane, and its
+    // table entry, all loads in flight together (and before the length is known).
+    // Longer rows: four blocks a lane, where the rows' alignment allows it, and
+    // the table is looked up for this split's blocks alone.
+    constexpr int kMaskWords = BITS == 8 && D == 128 ? 6 : 4;
     const int nblk = (len + 63) / 64, nwords = (nblk + 31) / 32;
+    const bool one_round = a.nb <= 32 * kMaskWords * W;
     int page[kMaskWords];
-    for (int c0 = warp; c0 < (c0 == warp ? (a.nb + 31) / 32 : nwords); c0 += kMaskWords * W) {
-        int raw[kMaskWords][kHeads], any[kMaskWords], pg[kMaskWords];
-        // (blocks past the row read its last one: the branches are the warp's)
+    if (one_round || a.nb % 4 != 0 || (reinterpret_cast<uintptr_t>(a.mask) & 3) != 0) {
+        for (int c0 = warp; c0 < (c0 == warp ? (a.nb + 31) / 32 : nwords); c0 += kMaskWords * W) {
+            int raw[kMaskWords][kHeads];
+            // (blocks past the row read its last one: the branches are the warp's)
 #pragma unroll
-        for (int i = 0; i < kMaskWords; ++i) {
-            any[i] = pg[i] = 0;
-            if (i > 0 && (c0 + i * W) * 32 >= a.nb)
-                continue;
-            const int j = min((c0 + i * W) * 32 + lane, a.nb - 1);
+            for (int i = 0; i < kMaskWords; ++i) {
+                if (i > 0 && (c0 + i * W) * 32 >= a.nb)
+                    continue;
+                const int j = min((c0 + i * W) * 32 + lane, a.nb - 1);
 #pragma unroll
-            for (int h = 0; h < kHeads; ++h) {
-                raw[i][h] = 0;
-                if (h < gt)
-                    raw[i][h] = __ldg(mrow + (long long)h * a.nb + j);
+                for (int h = 0; h < kHeads; ++h) {
+                    raw[i][h] = 0;
+                    if (h < gt)
+                        raw[i][h] = __ldg(mrow + (long long)h * a.nb + j);
+                }
+                if (one_round) {
+                    page[i] = b * a.kv.max_blocks + j;
+                    if (a.kv.table != nullptr)
+                        page[i] = __ldg(a.kv.table + page[i]);
+                }
             }
-            pg[i] = b * a.kv.max_blocks + j;
-            if (a.kv.table != nullptr)
-                pg[i] = __ldg(a.kv.table + pg[i]);
-        }
 #pragma unroll
-        for (int i = 0; i < kMaskWords; ++i)
-            if (i == 0 || (c0 + i * W) * 32 < a.nb)
+            for (int i = 0; i < kMaskWords; ++i) {
+                const int c = c0 + i * W;
+                if (c >= nwords)
+                    continue;
+                int any = 0;
 #pragma unroll
                 for (int h = 0; h < kHeads; ++h)
-                    any[i] |= raw[i][h];
-#pragma unroll
-        for (int i = 0; i < kMaskWords; ++i) {
-            if ((c0 + i * W) * 32 + lane >= nblk)
-                any[i] = 0;
-            if (any[i] != 0 && (pg[i] < 0 || pg[i] >= a.kv.n_pages)) {
-                set_status(a.status, kStatusPage);
-                any[i] = 0;
+                    any |= raw[i][h];
+                const unsigned bits = __ballot_sync(0xffffffffu, any != 0 && c * 32 + lane < nblk);
+                if (lane == 0)
+                    s_words[c] = bits;
             }
-            const unsigned bits = __ballot_sync(0xffffffffu, any[i] != 0);
-            if (lane == 0 && c0 + i * W < nwords)
-                s_words[c0 + i * W] = bits;
-            if (c0 == warp)
-                page[i] = pg[i];
+        }
+    } else {
+        for (int c0 = warp; c0 * 4 < nwords; c0 += 4 * W) {
+            uint32_t raw[4][kHeads];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int j = min((c0 + i * W) * 128 + 4 * lane, a.nb - 4);
+#pragma unroll
+                for (int h = 0; h < kHeads; ++h) {
+                    raw[i][h] = 0;
+                    if (h < gt)
+                        raw[i][h] = __ldg(reinterpret_cast<const uint32_t *>(mrow + (long long)h * a.nb + j));
+                }
+            }
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int j = (c0 + i * W) * 128 + 4 * lane;
+                uint32_t x = 0;
+#pragma unroll
+                for (int h = 0; h < kHeads; ++h)
+                    x |= raw[i][h];
+                // bytes that are not 0 -> four bits -> words of eight lanes
+                x = (((x & 0x7F7F7F7Fu) + 0x7F7F7F7Fu) | x) >> 7 & 0x01010101u;
+                x = x * 0x10204080u >> 28 & ((1u << max(0, min(4, nblk - j))) - 1u);
+                x <<= 4 * (lane & 7);
+                x |= __shfl_xor_sync(0xffffffffu, x, 1);
+                x |= __shfl_xor_sync(0xffffffffu, x, 2);
+                x |= __shfl_xor_sync(0xffffffffu, x, 4);
+                if ((lane & 7) == 0 && j / 32 < nwords)
+                    s_words[j / 32] = x;
+            }
         }
     }
     __syncthreads();
@@ -365,41 +396,58 @@ __global__ void __launch_bounds__(DecodeCfg<BITS, D>::W * 32, 2) decode_quant_ke
         r1 = split + 1 == a.nsplit ? total : (int)__umulhi((unsigned)(total * (split + 1)), a.inv_split);
         if (a.nsplit == 1)
             r0 = 0;
-        auto list = [&](int c, int pg) {            // word c's blocks; pg < 0: look the page up
+        // an entry: the block, with kNoPage where its table entry names no page
+        // (recorded; page 0 is copied in its place and none of its tokens counts)
+        auto entry = [&](int i, int j, int pg) {
+            const bool bad = pg < 0 || pg >= a.kv.n_pages;
+            if (bad)
+                set_status(a.status, kStatusPage);
+            s_block[i] = (uint16_t)(bad ? j | kNoPage : j);
+            s_rec[i] = ((uint32_t)(bad ? 0 : pg) * a.Hkv + kvh) * (F::REC / 512);
+        };
+        auto list = [&](int c, int pg) {            // this lane's block of word c
             int base = __shfl_sync(0xffffffffu, inc - cnt, c >> lg);
             for (int k = c >> lg << lg; k < c; ++k)
                 base += __popc(s_words[k]);
             const unsigned w = s_words[c];
             const int r = base + __popc(w & ((1u << lane) - 1u));
             if ((w >> lane & 1u) && r >= r0 && r < r1) {
-                const int j = c * 32 + lane;
-                s_block[r - r0] = (uint16_t)j;
-                if (pg < 0)
-                    pg = a.kv.table != nullptr ? __ldg(a.kv.table + b * a.kv.max_blocks + j) : b * a.kv.max_blocks + j;
-                s_rec[r - r0] = ((uint32_t)pg * a.Hkv + kvh) * (F::REC / 512);
+                if (one_round)
+                    entry(r - r0, c * 32 + lane, pg);
+                else
+                    s_block[r - r0] = (uint16_t)(c * 32 + lane);
             }
         };
+        if (one_round) {
 #pragma unroll
-        for (int i = 0; i < kMaskWords; ++i)
-            if (warp + i * W < nwords)
-                list(warp + i * W, page[i]);
-        for (int c = warp + kMaskWords * W; c < nwords; c += W)
-            list(c, -1);
+            for (int i = 0; i < kMaskWords; ++i)
+                if (warp + i * W < nwords)
+                    list(warp + i * W, page[i]);
+        } else {
+            for (int c = warp; c < nwords; c += W)
+                list(c, 0);
+            __syncthreads();
+            for (int i = threadIdx.x; i < r1 - r0; i += W * 32) {
+                const int j = s_block[i], at = b * a.kv.max_blocks + j;
+                entry(i, j, a.kv.table != nullptr ? __ldg(a.kv.table + at) : at);
+            }
+        }
     }
     __syncthreads();
 
     const int n_units = 2 * (r1 - r0);              // half records
     uint8_t *my = ring + warp * ST * F::HALF;
     const uint32_t my_bar = smem_u32(&s_bar[warp * ST]);
+    auto first_token = [&](int u) { return 64 * (s_block[u >> 1] & (kNoPage - 1)) + 32 * (u & 1); };
     auto issue = [&](int u, int st) {               // lane 0
-        if (u >= n_units || 64 * s_block[u >> 1] + 32 * (u & 1) >= len)
+        if (u >= n_units || first_token(u) >= len)
             return;
         mbar_arrive_expect_tx(my_bar + 8 * st, F::HALF);
         bulk_copy(smem_u32(my + st * F::HALF), a.kv.pages + (unsigned long long)s_rec[u >> 1] * 512 + (u & 1) * F::HALF,
                   F::HALF, my_bar + 8 * st);
     };
     auto head_byte = [&](int u) {
-        return u < n_units && lane < gt ? (int)__ldg(mrow + (long long)lane * a.nb + s_block[u >> 1]) : 0;
+        return u < n_units && lane < gt ? (int)__ldg(mrow + (long long)lane * a.nb + (s_block[u >> 1] & (kNoPage - 1))) : 0;
     };
     if (lane == 0)
         for (int s = 0; s < ST; ++s)
@@ -429,9 +477,11 @@ __global__ void __launch_bounds__(DecodeCfg<BITS, D>::W * 32, 2) decode_quant_ke
     for (int u = warp; u < n_units; u += W, ++it) {
         const unsigned hbits = __ballot_sync(0xffffffffu, mb != 0 || lane >= gt);
         mb = head_byte(u + W);
-        const int keys = len - (64 * s_block[u >> 1] + 32 * (u & 1));
+        int keys = len - first_token(u);
         if (keys <= 0)
             break;                                  // the empty half of the last block: nothing follows
+        if (s_block[u >> 1] & kNoPage)
+            keys = 0;
         const int st = it % ST;
         {
             const uint32_t bar = my_bar + 8 * st, parity = (it / ST) & 1;
@@ -447,7 +497,7 @@ __global__ void __launch_bounds__(DecodeCfg<BITS, D>::W * 32, 2) decode_quant_ke
                 for (int s = 0; s < ST; ++s) {
                     const int w = it + s;
                     const int uu = warp + w * W;
-                    if (uu < n_units && 64 * s_block[uu >> 1] + 32 * (uu & 1) < len)
+                    if (uu < n_units && first_token(uu) < len)
                         mbar_drain(my_bar + 8 * (w % ST), (w / ST) & 1, 200000000ull);
                 }
                 m[0] = m[1] = -INFINITY;

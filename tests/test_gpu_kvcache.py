@@ -326,6 +326,34 @@ def test_decode_long_and_split(bits, d):
 
 
 @pytest.mark.parametrize("bits,d", FORMATS)
+@pytest.mark.parametrize("nb", [1200, 1203])               # four blocks a lane where the rows are aligned, one where not
+def test_decode_long_rows_and_bad_pages(bits, d, nb):
+    """Rows of more blocks than a warp takes in one round, a short sequence beside a long one, and table entries of
+    active blocks that name no page: those blocks count as inactive, and the device status says so."""
+    B, Hq, Hkv, L = 2, 6, 2, 64 * nb
+    lens = [L - 70, 130]
+    cache, table = make_cache(B, Hkv, nb, d, bits, True, 3)
+    k, v = bf16((B, Hkv, L, d), 1), bf16((B, Hkv, L, d), 2)
+    seer.seer_kv_write(cache, k.cuda(), v.cuda(), count=dev32(lens))
+    q = bf16((B, Hq, d), 3)
+    mask = (torch.rand((B, Hq, nb), generator=torch.Generator().manual_seed(nb)) < 0.1).to(torch.uint8)
+    mask[:, :, [0, 1, 700, nb - 2]] = 1
+    held = parts(cache, table)
+    args = (q.cuda(), cache, mask.cuda(), L)
+    o, lse = seer.seer_block_sparse_decode_quant(*args, lens=dev32(lens), return_lse=True)
+    seer.seer_check_status()
+    check_decode(o, lse, q, held, mask, lens)
+    for j, bad in ((1, -1), (700, cache.pages.shape[0]), (nb - 2, 2 ** 30)):
+        cache.block_table[0, j] = bad
+    o, lse = seer.seer_block_sparse_decode_quant(*args, lens=dev32(lens), return_lse=True)
+    with pytest.raises(seer.SeerError):
+        seer.seer_check_status()
+    without = mask.clone()
+    without[0, :, [1, 700, nb - 2]] = 0
+    check_decode(o, lse, q, held, without, lens)
+
+
+@pytest.mark.parametrize("bits,d", FORMATS)
 @pytest.mark.parametrize("kscale,vscale,scale", [(30.0, 1.0, None), (1.0, 1e-12, None), (1.0, 1e12, None),
                                                  (1e-3, 1.0, 5.0), (1.0, 1.0, 1e-3)])
 def test_decode_ranges(bits, d, kscale, vscale, scale):

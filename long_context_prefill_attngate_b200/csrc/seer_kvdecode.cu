@@ -259,7 +259,6 @@ __global__ void __launch_bounds__(DecodeCfg<BITS, D>::W * 32, 2) decode_quant_ke
     const int len = a.lens != nullptr ? max(0, min(a.lens[b], a.L)) : a.L;
     const uint8_t *mrow = a.mask + ((long long)b * a.Hq + h0) * a.nb;
 
-    asm volatile("griddepcontrol.launch_dependents;");
     if (lane == 0) {
         for (int s = 0; s < ST; ++s)
             mbar_init(smem_u32(&s_bar[warp * ST + s]), 1);
@@ -790,7 +789,6 @@ __global__ void __launch_bounds__(D)
     decode_quant_merge_kernel(const float *part, int nsplit, __nv_bfloat16 *o, float *lse)
 {
     __shared__ float s_w[kMaxDecodeSplits];
-    asm volatile("griddepcontrol.wait;" ::: "memory");
     const long long bh = blockIdx.x;
     const float *pp = part + bh * nsplit * (D + 2);
     const int lane = threadIdx.x & 31;
@@ -876,16 +874,8 @@ cudaError_t launch(DecodeArgs a, int B, cudaStream_t stream)
     e = cudaGetLastError();
     if (e != cudaSuccess || a.nsplit == 1)
         return e;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(B * a.Hq);
-    cfg.blockDim = dim3(D);
-    cfg.stream = stream;
-    cudaLaunchAttribute attr[1];                    // the launch overlaps the first kernel; it waits for its end
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, decode_quant_merge_kernel<D>, (const float *)a.part, a.nsplit, a.o, a.lse);
+    decode_quant_merge_kernel<D><<<B * a.Hq, D, 0, stream>>>(a.part, a.nsplit, a.o, a.lse);
+    return cudaGetLastError();
 }
 
 } // namespace

@@ -205,6 +205,11 @@ __device__ __forceinline__ void prepare_q(const __nv_bfloat16 *qp, int lane, Hea
         out->inv = pow2_field(127 - qe);
 }
 
+// The scale of a param word as a float.  The integer and shift pipe is the busiest
+// of the loop (two cycles an instruction), so the shift is a multiplication by a
+// 2^16 that the compiler does not see.
+__device__ __forceinline__ float scale_of(uint32_t par, uint32_t two16) { return __uint_as_float(par * two16); }
+
 struct DecodeArgs {
     const __nv_bfloat16 *q_tok;
     KvView kv;
@@ -218,6 +223,7 @@ struct DecodeArgs {
     float *lse;
     int *status;
     uint64_t timeout_ns;
+    uint32_t two16;                      // 65536
 };
 
 // Warps of a CTA and half records in flight per warp.  Two CTAs share an SM, so
@@ -371,7 +377,12 @@ __global__ void __launch_bounds__(DecodeCfg<BITS, D>::W * 32, 2) decode_quant_ke
         for (int i = 0; i < 3; ++i)
             qz[i] = tig < NG ? (uint32_t)q.sum[i][tig] << 16 : 0u;
     }
-    const float qinv[2] = {s_q[2 * tig].inv, s_q[2 * tig + 1].inv};
+    // a score in units of log2: its raw sum times fac (kept off 0 and infinity, so
+    // that a masked score's -infinity stays one)
+    float fac[2];
+#pragma unroll
+    for (int e = 0; e < 2; ++e)
+        fac[e] = fminf(fmaxf(s_q[2 * tig + e].inv * (a.scale_log2 * 16777216.f), 1.2e-38f), 3e38f);
 
     // ---- this split's blocks: ranks [r0, r1) of the union
     int r0, r1;
@@ -460,7 +471,6 @@ __global__ void __launch_bounds__(DecodeCfg<BITS, D>::W * 32, 2) decode_quant_ke
 #pragma unroll
     for (int gr = 0; gr < NG; ++gr)
         zacc[gr][0] = zacc[gr][1] = 0.f;
-    const float to_log2 = a.scale_log2 * 16777216.f;    // 2^24
 
     // this lane's places in a half record: K row and params of tile row gid (row
     // gid + 8 and the second tile a whole number of rows further, with the same
@@ -506,7 +516,7 @@ __global__ void __launch_bounds__(DecodeCfg<BITS, D>::W * 32, 2) decode_quant_ke
         }
         const uint8_t *h = my + st * F::HALF;
 
-        // ---- scores of two 16-token tiles, log2 units
+        // ---- raw scores of two 16-token tiles
         float s[2][4];
 #pragma unroll
         for (int mt = 0; mt < 2; ++mt) {
@@ -559,19 +569,17 @@ __global__ void __launch_bounds__(DecodeCfg<BITS, D>::W * 32, 2) decode_quant_ke
                     else
                         mma16816(c, x[0], x[1], x[2], x[3], qf[ks][0], qf[ks][1]);
                 }
-                const float sa = kv_scale(pa[gr]), sb = kv_scale(pb[gr]);
+                const float sa = scale_of(pa[gr], a.two16), sb = scale_of(pb[gr], a.two16);
                 s[mt][0] = fmaf(sa, c[0], s[mt][0]);
                 s[mt][1] = fmaf(sa, c[1], s[mt][1]);
                 s[mt][2] = fmaf(sb, c[2], s[mt][2]);
                 s[mt][3] = fmaf(sb, c[3], s[mt][3]);
             }
-#pragma unroll
-            for (int e = 0; e < 4; ++e)
-                s[mt][e] = s[mt][e] * qinv[e & 1] * to_log2;
         }
         const bool all_heads = hbits == 0xffffffffu;
         const bool act0 = hbits >> (2 * tig) & 1u, act1 = hbits >> (2 * tig + 1) & 1u;
         if (keys < 32) {                            // the sequence's last tokens
+            __syncwarp();                           // (keeps this a branch)
 #pragma unroll
             for (int mt = 0; mt < 2; ++mt)
 #pragma unroll
@@ -588,7 +596,8 @@ __global__ void __launch_bounds__(DecodeCfg<BITS, D>::W * 32, 2) decode_quant_ke
 #pragma unroll
             for (int hf = 0; hf < 2; ++hf)
                 load_words(vp[mt][hf], h + F::kParV + at_p + (16 * mt + 8 * hf) * F::PAR);
-        if (keys < 32)
+        if (keys < 32) {
+            __syncwarp();
 #pragma unroll
             for (int mt = 0; mt < 2; ++mt)
 #pragma unroll
@@ -597,6 +606,7 @@ __global__ void __launch_bounds__(DecodeCfg<BITS, D>::W * 32, 2) decode_quant_ke
                     for (int gr = 0; gr < NG; ++gr)
                         if (16 * mt + tr + 8 * hf >= keys)
                             vp[mt][hf][gr] = 0u;
+        }
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             if constexpr (NG == 1)
@@ -616,16 +626,16 @@ __global__ void __launch_bounds__(DecodeCfg<BITS, D>::W * 32, 2) decode_quant_ke
             vmax = __vmaxu2(vmax, __shfl_xor_sync(0xffffffffu, vmax, off));
         }
         const int ve_new = max(ve, (int)(vmax >> 7 & 0xFFu));
-        float alpha[2], mu[2];
+        // a head that left the block out: its maximum stays and its p are 0
+        const bool more0 = act0 && mx[0] > m[0], more1 = act1 && mx[1] > m[1];
+        if (__any_sync(0xffffffffu, more0 || more1 || ve_new != ve)) {
+            float alpha[2];
+            const float m_new[2] = {more0 ? mx[0] : m[0], more1 ? mx[1] : m[1]};
 #pragma unroll
-        for (int e = 0; e < 2; ++e) {
-            // a head that left the block out: its maximum stays and its p are 0
-            const float mn = (e ? act1 : act0) ? fmaxf(m[e], mx[e]) : m[e];
-            mu[e] = mn == -INFINITY ? 0.f : mn;
-            alpha[e] = mn == -INFINITY ? 1.f : exp2_approx(m[e] - mu[e]);
-            m[e] = mn;
-        }
-        if (__any_sync(0xffffffffu, alpha[0] != 1.f || alpha[1] != 1.f || ve_new != ve)) {
+            for (int e = 0; e < 2; ++e) {
+                alpha[e] = m_new[e] == m[e] ? 1.f : exp2_approx((m[e] - m_new[e]) * fac[e]);
+                m[e] = m_new[e];
+            }
             const float down = ve - ve_new > -127 ? pow2_field(127 + ve - ve_new) : 0.f;
 #pragma unroll
             for (int i = 0; i < KS; ++i)
@@ -641,6 +651,7 @@ __global__ void __launch_bounds__(DecodeCfg<BITS, D>::W * 32, 2) decode_quant_ke
             l[1] *= alpha[1];
             ve = ve_new;
         }
+        const float mu[2] = {m[0] == -INFINITY ? 0.f : -m[0] * fac[0], m[1] == -INFINITY ? 0.f : -m[1] * fac[1]};
         const float up = pow2_field(268 - ve);      // 2^14 over the power of two below the largest scale
 
         // ---- P V
@@ -649,7 +660,7 @@ __global__ void __launch_bounds__(DecodeCfg<BITS, D>::W * 32, 2) decode_quant_ke
             float p[4];
 #pragma unroll
             for (int e = 0; e < 4; ++e)
-                p[e] = exp2_approx(s[mt][e] - mu[e & 1]);
+                p[e] = exp2_approx(fmaf(s[mt][e], fac[e & 1], mu[e & 1]));
             if (!all_heads) {
                 p[0] = act0 ? p[0] : 0.f;
                 p[1] = act1 ? p[1] : 0.f;
@@ -669,7 +680,7 @@ __global__ void __launch_bounds__(DecodeCfg<BITS, D>::W * 32, 2) decode_quant_ke
                 pu[e] = p[e] * up;
 #pragma unroll
             for (int gr = 0; gr < NG; ++gr) {
-                const float sa = kv_scale(vp[mt][0][gr]), sb = kv_scale(vp[mt][1][gr]);
+                const float sa = scale_of(vp[mt][0][gr], a.two16), sb = scale_of(vp[mt][1][gr], a.two16);
                 const float za = kv_zero(vp[mt][0][gr]), zb = kv_zero(vp[mt][1][gr]);
                 const uint32_t b0 = movmatrix(pack_half2(pu[0] * sa, pu[1] * sa));
                 const uint32_t b1 = movmatrix(pack_half2(pu[2] * sb, pu[3] * sb));
@@ -716,8 +727,8 @@ __global__ void __launch_bounds__(DecodeCfg<BITS, D>::W * 32, 2) decode_quant_ke
         }
     __syncwarp();
     if (gid == 0) {
-        s_ml[warp][2 * tig] = make_float2(m[0], l[0]);
-        s_ml[warp][2 * tig + 1] = make_float2(m[1], l[1]);
+        s_ml[warp][2 * tig] = make_float2(m[0] == -INFINITY ? m[0] : m[0] * fac[0], l[0]);
+        s_ml[warp][2 * tig + 1] = make_float2(m[1] == -INFINITY ? m[1] : m[1] * fac[1], l[1]);
     }
     float *so = reinterpret_cast<float *>(my);      // [kHeads][D], over this warp's ring
     {
@@ -899,6 +910,7 @@ cudaError_t launch_decode_quant(int bits, int B, int Hq, int Hkv, int L, int d, 
     a.lse = lse;
     a.status = status;
     a.timeout_ns = timeout_ns;
+    a.two16 = 65536u;
     if (bits == 4)
         return d == 128 ? launch<4, 128>(a, B, stream) : launch<4, 64>(a, B, stream);
     return d == 128 ? launch<8, 128>(a, B, stream) : launch<8, 64>(a, B, stream);

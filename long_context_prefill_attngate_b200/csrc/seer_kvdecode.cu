@@ -215,8 +215,8 @@ struct DecodeArgs {
     KvView kv;
     const int32_t *lens;
     const uint8_t *mask;
-    int Hq, Hkv, L, nb, tiles, per_tile, nsplit;
-    unsigned inv_split;
+    int B, Hq, Hkv, L, nb, tiles, per_tile, nsplit;
+    int slots;                           // of a head tile, shared out by length; 0: nsplit each
     float scale_log2;
     float *part;
     __nv_bfloat16 *o;
@@ -237,6 +237,84 @@ struct DecodeCfg {
     static constexpr int ring = W * ST * KvFmt<BITS, D>::HALF;
 };
 
+// The CTAs of a head tile: nsplit for every sequence or, with lengths given (and
+// few enough sequences for one look at them), a number of slots of which every
+// sequence has one and a share of the others in proportion to its blocks, so
+// that a batch of unequal lengths ends together.  slot_of: the sequence that a
+// slot serves, which of its splits it is and how many there are (one warp; false:
+// it serves nothing).
+constexpr int kBalanced = 64;             // sequences
+
+__device__ __forceinline__ int blocks_of(const DecodeArgs &a, int b)
+{
+    return b < a.B ? (max(0, min(__ldg(a.lens + b), a.L)) + 63) / 64 : 0;
+}
+
+struct Shares {
+    int first[2], count[2];               // slots of sequences lane, lane + 32
+};
+
+__device__ __forceinline__ Shares shares(const DecodeArgs &a, int lane)
+{
+    int n[2], before[2], total = 0;
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+        n[i] = blocks_of(a, lane + 32 * i);
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        int inc = n[i];
+#pragma unroll
+        for (int off = 1; off < 32; off <<= 1) {
+            const int v = __shfl_up_sync(0xffffffffu, inc, off);
+            inc += lane >= off ? v : 0;
+        }
+        before[i] = total + inc - n[i];
+        total += __shfl_sync(0xffffffffu, inc, 31);
+    }
+    // a rising function of the blocks before, so the shares neither overlap nor leave gaps
+    const float rate = total > 0 ? (float)(a.slots - a.B) / (float)total : 0.f;
+    Shares s;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        s.first[i] = lane + 32 * i + (int)((float)before[i] * rate);
+        s.count[i] = lane + 32 * i + 1 + (int)((float)(before[i] + n[i]) * rate) - s.first[i];
+    }
+    return s;
+}
+
+__device__ __forceinline__ bool slot_of(const DecodeArgs &a, int lane, int &b, int &split, int &ns)
+{
+    const int c = blockIdx.x;
+    if (a.slots == 0) {
+        b = blockIdx.z;
+        split = c;
+        ns = a.nsplit;
+        return true;
+    }
+    const Shares s = shares(a, lane);
+    b = -1;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        const unsigned hit =
+            __ballot_sync(0xffffffffu, lane + 32 * i < a.B && c >= s.first[i] && c < s.first[i] + s.count[i]);
+        if (hit != 0) {
+            const int src = __ffs(hit) - 1;
+            b = src + 32 * i;
+            split = c - __shfl_sync(0xffffffffu, s.first[i], src);
+            ns = min(__shfl_sync(0xffffffffu, s.count[i], src), kMaxDecodeSplits);
+        }
+    }
+    return b >= 0 && split < ns;
+}
+
+__device__ __forceinline__ int splits_of(const DecodeArgs &a, int b, int lane)
+{
+    if (a.slots == 0)
+        return a.nsplit;
+    const Shares s = shares(a, lane);
+    return min(__shfl_sync(0xffffffffu, b < 32 ? s.count[0] : s.count[1], b & 31), kMaxDecodeSplits);
+}
+
 template <int BITS, int D>
 __global__ void __launch_bounds__(DecodeCfg<BITS, D>::W * 32, 2) decode_quant_kernel(const DecodeArgs a)
 {
@@ -256,9 +334,10 @@ __global__ void __launch_bounds__(DecodeCfg<BITS, D>::W * 32, 2) decode_quant_ke
 
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int gid = lane >> 2, tig = lane & 3;
-    const int split = blockIdx.x;
-    const int tile = blockIdx.y % a.tiles, bk = blockIdx.y / a.tiles;
-    const int b = bk / a.Hkv, kvh = bk % a.Hkv;
+    int b, split, ns;
+    if (!slot_of(a, lane, b, split, ns))
+        return;
+    const int tile = blockIdx.y % a.tiles, kvh = blockIdx.y / a.tiles;
     const int g = a.Hq / a.Hkv;
     const int h0 = kvh * g + tile * a.per_tile;     // first query head, and how many
     const int gt = min(a.per_tile, g - tile * a.per_tile);
@@ -400,12 +479,12 @@ __global__ void __launch_bounds__(DecodeCfg<BITS, D>::W * 32, 2) decode_quant_ke
             inc += lane >= off ? v : 0;
         }
         const int total = __shfl_sync(0xffffffffu, inc, 31);
-        // total * split / nsplit: at most 2^20, and inv_split is 2^32 / nsplit rounded
-        // up by less than 2^-26 of it, so the product's high word is the quotient
-        r0 = (int)__umulhi((unsigned)(total * split), a.inv_split);
-        r1 = split + 1 == a.nsplit ? total : (int)__umulhi((unsigned)(total * (split + 1)), a.inv_split);
-        if (a.nsplit == 1)
-            r0 = 0;
+        // total * split / ns: at most 2^20, and inv is 2^32 / ns rounded up by less
+        // than 2^-26 of it, so the product's high word is the quotient (one split:
+        // inv is 0 and so is r0)
+        const unsigned inv = 0xFFFFFFFFu / (unsigned)ns + 1u;
+        r0 = (int)__umulhi((unsigned)(total * split), inv);
+        r1 = split + 1 == ns ? total : (int)__umulhi((unsigned)(total * (split + 1)), inv);
         // an entry: the block, with kNoPage where its table entry names no page
         // (recorded; page 0 is copied in its place and none of its tokens counts)
         auto entry = [&](int i, int j, int pg) {
@@ -779,12 +858,12 @@ __global__ void __launch_bounds__(DecodeCfg<BITS, D>::W * 32, 2) decode_quant_ke
                 sum = fmaf(wt, *reinterpret_cast<const float *>(ring + w * ST * F::HALF + i * 4), sum);
         }
         const long long bh = (long long)b * a.Hq + h0 + hh;
-        if (a.nsplit == 1) {
+        if (ns == 1) {
             a.o[bh * D + c] = __float2bfloat16_rn(lt == 0.f ? 0.f : sum / lt);
             if (c == 0 && a.lse != nullptr)
                 a.lse[bh] = log_sum(s_sum[hh].x, lt);
         } else {
-            float *out = a.part + (bh * a.nsplit + split) * (D + 2);
+            float *out = a.part + (bh * kMaxDecodeSplits + split) * (D + 2);
             out[c] = sum;
             if (c == 0) {
                 out[D] = s_sum[hh].x;
@@ -796,13 +875,17 @@ __global__ void __launch_bounds__(DecodeCfg<BITS, D>::W * 32, 2) decode_quant_ke
 
 // The splits of one head: weights 2^(m_s - M), o = sum w o / sum w l.
 template <int D>
-__global__ void __launch_bounds__(D)
-    decode_quant_merge_kernel(const float *part, int nsplit, __nv_bfloat16 *o, float *lse)
+__global__ void __launch_bounds__(D) decode_quant_merge_kernel(const DecodeArgs a)
 {
     __shared__ float s_w[kMaxDecodeSplits];
     const long long bh = blockIdx.x;
-    const float *pp = part + bh * nsplit * (D + 2);
     const int lane = threadIdx.x & 31;
+    const int nsplit = splits_of(a, blockIdx.x / a.Hq, lane);
+    if (nsplit == 1)
+        return;                                     // written by its one split
+    const float *pp = a.part + bh * kMaxDecodeSplits * (D + 2);
+    __nv_bfloat16 *o = a.o;
+    float *lse = a.lse;
     float ms[2], ls[2], M = -INFINITY;
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
@@ -835,36 +918,64 @@ __global__ void __launch_bounds__(D)
         lse[bh] = log_sum(M, l);
 }
 
-// Splits of a unit (a KV head's head tile): the count with the least estimated
-// time, in us, with half of the blocks active (the mask is on the device):
+// Estimated time, in us, of `ctas` CTAs with `blocks` blocks each:
 //   a CTA's start and end     6 alone on its SM, 7.5 for two at once, per wave
 //   a block                   0.4 for a CTA alone, 0.31 of the SM for two
 //   the second kernel         2 and 0.04 a split
-// and at least a block for every second warp.  Measured (4 bits, D = 128): 8 units
-// of 512 blocks, all active: 9 splits 31.2 us, 18: 22.5, 36: 23.2; a tenth active: 15.7,
-// 13.4, 15.2; 128 units of 256: 1 split 104 us, 2: 89, 3: 96, 8: 94; 64 units of
-// 512 at most (a ragged batch): 2: 68, 4: 48, 6: 45, 12: 49.
-int decode_quant_splits(long long units, int nb, int sms)
+// Measured (4 bits, D = 128): 8 units (a sequence's head tile) of 512 blocks, all
+// active: 9 splits 31.2 us, 18: 22.5, 36: 23.2; a tenth active: 15.7, 13.4, 15.2;
+// 128 units of 256: 1 split 104 us, 2: 89, 3: 96, 8: 94.
+double decode_quant_us(long long ctas, double blocks, double splits, int sms)
 {
-    const int lo = (nb + kListMax - 2) / (kListMax - 1);              // a split's block list has to fit
-    const int cap = nb / 4 < kMaxDecodeSplits ? nb / 4 : kMaxDecodeSplits;
-    int best = lo;
+    const long long load = (ctas + sms - 1) / sms, waves = (load + 1) / 2;
+    return (load == 1 ? 6.0 + 0.4 * blocks : 7.5 * (double)waves + 0.31 * (double)load * blocks) +
+           (splits > 1.0 ? 2.0 + 0.04 * splits : 0.0);
+}
+
+// How a call is split (nsplit, slots): the least estimated time with half of the
+// blocks active (the mask is on the device) and at least a block for every
+// second warp.  Lengths given: one or two CTAs per SM in all, where there are
+// enough for every sequence's tiles, shared out by length: a batch of 8 from 32k
+// tokens down took 48 us with 4 splits each, 42 so.  Not for two or three
+// sequences, whose CTAs pair up on the SMs (64k and 37k tokens at 8 bits: 42 us with
+// 18 splits each, 45 shared out), and in whole splits where a sequence has few
+// (16 of 16k tokens: 88 us with two each, 90 with 37 slots).
+void decode_quant_split(DecodeArgs &a, int sms)
+{
+    const int tiles = a.Hkv * a.tiles;
+    const int lo = (a.nb + kListMax - 2) / (kListMax - 1);            // a split's block list has to fit
+    const int cap = a.nb / 4 < kMaxDecodeSplits ? a.nb / 4 : kMaxDecodeSplits;
     double best_us = 1e30;
+    a.nsplit = lo;
+    a.slots = 0;
     for (int ns = lo; ns <= cap; ++ns) {
-        const long long ctas = units * ns, load = (ctas + sms - 1) / sms, waves = (load + 1) / 2;
-        const double blocks = 0.5 * nb / ns;
-        const double us = (load == 1 ? 6.0 + 0.4 * blocks : 7.5 * (double)waves + 0.31 * (double)load * blocks) +
-                          (ns > 1 ? 2.0 + 0.04 * ns : 0.0);
+        const double us = decode_quant_us((long long)a.B * tiles * ns, 0.5 * a.nb / ns, ns, sms);
         if (us < best_us) {
             best_us = us;
-            best = ns;
+            a.nsplit = ns;
         }
     }
-    return best;
+    if (a.lens == nullptr || a.B < 4 || a.B > kBalanced)
+        return;
+    best_us = 1e30;
+    for (int load = 1; load <= 2; ++load) {
+        int slots = load * sms / tiles;
+        if (slots < 4 * a.B)
+            slots -= slots % a.B;
+        // a sequence's share of slots - B is at least that of its blocks in B * nb
+        if (slots < a.B * (1 + lo) || slots > a.B * (1 + cap))
+            continue;
+        const double each = (double)slots / a.B;
+        const double us = decode_quant_us((long long)slots * tiles, 0.5 * a.nb / each, each, sms);
+        if (us < best_us) {
+            best_us = us;
+            a.slots = slots;
+        }
+    }
 }
 
 template <int BITS, int D>
-cudaError_t launch(DecodeArgs a, int B, cudaStream_t stream)
+cudaError_t launch(DecodeArgs a, cudaStream_t stream)
 {
     using C = DecodeCfg<BITS, D>;
     const int g = a.Hq / a.Hkv;
@@ -878,14 +989,13 @@ cudaError_t launch(DecodeArgs a, int B, cudaStream_t stream)
         e = cudaFuncSetAttribute(decode_quant_kernel<BITS, D>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::ring);
     if (e != cudaSuccess)
         return e;
-    const int units = B * a.Hkv * a.tiles;
-    a.nsplit = decode_quant_splits(units, a.nb, sms);
-    a.inv_split = (unsigned)((0x100000000ull + a.nsplit - 1) / a.nsplit);     // (0 for one split, which has no use for it)
-    decode_quant_kernel<BITS, D><<<dim3(a.nsplit, units), C::W * 32, C::ring, stream>>>(a);
+    decode_quant_split(a, sms);
+    const dim3 grid(a.slots > 0 ? a.slots : a.nsplit, a.Hkv * a.tiles, a.slots > 0 ? 1 : a.B);
+    decode_quant_kernel<BITS, D><<<grid, C::W * 32, C::ring, stream>>>(a);
     e = cudaGetLastError();
-    if (e != cudaSuccess || a.nsplit == 1)
+    if (e != cudaSuccess || (a.slots == 0 && a.nsplit == 1))
         return e;
-    decode_quant_merge_kernel<D><<<B * a.Hq, D, 0, stream>>>(a.part, a.nsplit, a.o, a.lse);
+    decode_quant_merge_kernel<D><<<a.B * a.Hq, D, 0, stream>>>(a);
     return cudaGetLastError();
 }
 
@@ -900,6 +1010,7 @@ cudaError_t launch_decode_quant(int bits, int B, int Hq, int Hkv, int L, int d, 
     a.kv = kv;
     a.lens = lens;
     a.mask = mask;
+    a.B = B;
     a.Hq = Hq;
     a.Hkv = Hkv;
     a.L = L;
@@ -912,8 +1023,8 @@ cudaError_t launch_decode_quant(int bits, int B, int Hq, int Hkv, int L, int d, 
     a.timeout_ns = timeout_ns;
     a.two16 = 65536u;
     if (bits == 4)
-        return d == 128 ? launch<4, 128>(a, B, stream) : launch<4, 64>(a, B, stream);
-    return d == 128 ? launch<8, 128>(a, B, stream) : launch<8, 64>(a, B, stream);
+        return d == 128 ? launch<4, 128>(a, stream) : launch<4, 64>(a, stream);
+    return d == 128 ? launch<8, 128>(a, stream) : launch<8, 64>(a, stream);
 }
 
 } // namespace seer

@@ -319,6 +319,21 @@ def test_decode_ragged_batch(bits, d, p):
     attend(bits, d, 6, 8, 2, 2000, p, lens=[2000, 1337, 1, 0, 5000, -3], seed=11)
 
 
+@pytest.mark.parametrize("bits,d,Hq,Hkv,L,lens", [
+    (4, 128, 16, 8, 9000, [9000, 0, 64, 5000, 7]),
+    (4, 64, 12, 6, 6000, [1, 6000, 1, 1]),
+    (8, 128, 8, 8, 3000, [3000] * 4),
+    (8, 64, 9, 1, 2500, [0] * 7),                           # nothing anywhere, groups of nine
+    (4, 128, 2, 1, 1500, [(97 * i) % 1501 for i in range(64)]),   # as many sequences as are shared out
+    (4, 128, 2, 1, 1200, [(97 * i) % 1201 for i in range(65)]),   # one more
+    (8, 128, 4, 2, 3500, [3500 - 90 * i for i in range(37)]),
+    (4, 64, 1, 1, 64 * 600, [64 * 600, 3, 0, 64 * 300, 64 * 600 - 1]),
+])
+def test_decode_batches_shared_out_by_length(bits, d, Hq, Hkv, L, lens):
+    """CTAs in proportion to the lengths, which only the device knows."""
+    attend(bits, d, len(lens), Hq, Hkv, L, 0.4, lens=lens, seed=len(lens))
+
+
 @pytest.mark.parametrize("bits,d", FORMATS)
 def test_decode_long_and_split(bits, d):
     """More blocks than one pass of the list takes, one KV head: many splits."""

@@ -21,15 +21,18 @@ namespace {
 
 constexpr int kRowThreads = 256;
 
-// A lane holds eight elements of a row (one 16-byte access on the bf16 side):
-// 16 lanes a row at D = 128, 8 at D = 64.
-template <int BITS, int D>
+// A lane holds E elements of a row.  Reading, eight: one 16-byte store each,
+// which leaves the kernel at 87 % of the copy rate.  Writing is bound by its
+// instructions, not by HBM, so there a lane has sixteen, over which the group's
+// extrema, scale and addresses are shared (37 us against 45 with eight for
+// a 32k prompt of 8 heads).
+template <int BITS, int D, int E>
 struct RowMap {
     using F = KvFmt<BITS, D>;
-    static constexpr int CH = D / 8;                     // lanes of a row
+    static constexpr int CH = D / E;                     // lanes of a row
     static constexpr int RPW = 32 / CH;                  // rows of a warp's access
-    static constexpr int GL = F::G / 8;                  // lanes of a group
-    static constexpr int NW = BITS / 4;                  // code words of a lane
+    static constexpr int GL = F::G / E;                  // lanes of a group
+    static constexpr int NW = E * BITS / 32;             // code words of a lane
 };
 
 // A CTA has one page of one head, 64 positions of which the call's rows cover
@@ -99,9 +102,9 @@ __device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c)
 }
 __device__ __forceinline__ float2 both(float x) { return make_float2(x, x); }
 
-// The code words of a V row change lanes between element order (lane c: the
-// words of elements 8c .. 8c+7) and the order they lie in (lane c: four bytes
-// at offset v_place at 4 bits, eight at 8).  At 4 bits a lane's word is two
+// Reading: the code words of a V row change lanes from the order they lie in
+// (lane c: four bytes at offset v_place at 4 bits, eight at 8) to element order
+// (lane c: the words of elements 8c .. 8c+7).  At 4 bits a lane's word is two
 // 16-bit runs of chunks 2q and 2q + 1 (q = c % 4) of group c / 4, and a stored
 // word is two groups of one chunk: a 2 x 2 exchange within the row.
 template <int BITS, int D>
@@ -116,42 +119,23 @@ __device__ __forceinline__ int v_place(int t, int c)
 }
 
 template <int D>
-__device__ __forceinline__ uint32_t v4_exchange(uint32_t w, int lane, bool store)
+__device__ __forceinline__ uint32_t v4_exchange(uint32_t w, int lane)
 {
     const int base = lane & ~(D / 8 - 1), c = lane & (D / 8 - 1), i = c / 4, q = c % 4;
-    int s0, s1, half;
-    if (D == 128) {
-        s0 = store ? 2 * (i & 1) : i >> 1;
-        s1 = store ? s0 + 1 : s0 + 2;
-        half = store ? i >> 1 : i & 1;
-    } else {
-        s0 = 0;
-        s1 = 1;
-        half = i;
-    }
+    const int s0 = D == 128 ? i >> 1 : 0, s1 = D == 128 ? s0 + 2 : 1, half = D == 128 ? i & 1 : i;
     const uint32_t v0 = __shfl_sync(0xffffffffu, w, base + 4 * s0 + q), v1 = __shfl_sync(0xffffffffu, w, base + 4 * s1 + q);
     return __byte_perm(v0, v1, half ? 0x7632 : 0x5410);
 }
 
-// At 8 bits a K row's word c lies at 16 p + 4 (c % 4) + (c / 4) % 4: lane c
-// stores or loads eight bytes, the words (j, t) and (j + 1, t) with j = c / 2
-// of the sixteen elements' index, against words 2c and 2c + 1 in element order.
+// At 8 bits a K row's word c lies at 16 p + 4 (c % 4) + (c / 4) % 4: lane c loads
+// eight bytes, the words (j, t) and (j + 1, t) with j = c / 2 of the sixteen
+// elements' index, against words 2c and 2c + 1 in element order.
 template <int D>
 __device__ __forceinline__ int k8_place(int tok, int c)
 {
     using F = KvFmt<8, D>;
     const int p = D == 128 ? (c / 8) ^ (tok & 1) : 0;
     return tok * F::R + p * 64 + (c % 8) / 2 * 16 + (c % 2) * 8;
-}
-
-template <int D>
-__device__ __forceinline__ uint2 k8_to_store(uint2 w, int lane)
-{
-    const int base = lane & ~(D / 8 - 1), c = lane & (D / 8 - 1);
-    const int t = (c % 8) / 2, src = base + 2 * (4 * (c / 8) + 2 * (c % 2)) + t / 2;
-    const uint32_t x0 = __shfl_sync(0xffffffffu, w.x, src), y0 = __shfl_sync(0xffffffffu, w.y, src);
-    const uint32_t x1 = __shfl_sync(0xffffffffu, w.x, src + 2), y1 = __shfl_sync(0xffffffffu, w.y, src + 2);
-    return t & 1 ? make_uint2(y0, y1) : make_uint2(x0, x1);
 }
 
 template <int D>
@@ -165,22 +149,23 @@ __device__ __forceinline__ uint2 k8_from_store(uint2 w, int lane)
     return j & 1 ? make_uint2(y0, y1) : make_uint2(x0, x1);
 }
 
-// The code words and the param of eight elements.  t / s is divided as IEEE
-// division would (quotient by the reciprocal, then one step with the exact
+// The code words and the param of a lane's sixteen elements.  t / s is divided as
+// IEEE division would (quotient by the reciprocal, then one step with the exact
 // remainder), which puts a half where it is one: bf16 differences and an 8-bit s
 // keep every other quotient further from a half than 2^-24 of it.
 template <int BITS, int D>
-__device__ __forceinline__ uint32_t quantise8(const uint4 in, uint32_t (&code)[BITS / 4])
+__device__ __forceinline__ uint32_t quantise16(const uint4 (&in)[2], uint32_t (&code)[BITS / 2])
 {
     using F = KvFmt<BITS, D>;
-    constexpr int GL = RowMap<BITS, D>::GL;
-    const uint32_t w[4] = {in.x, in.y, in.z, in.w};
-    __nv_bfloat162 p[4];
+    constexpr int GL = RowMap<BITS, D, 16>::GL;
+    const uint32_t w[8] = {in[0].x, in[0].y, in[0].z, in[0].w, in[1].x, in[1].y, in[1].z, in[1].w};
+    __nv_bfloat162 mn, mx;
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
-        p[i] = *reinterpret_cast<const __nv_bfloat162 *>(&w[i]);
-    __nv_bfloat162 mn = __hmin2_nan(__hmin2_nan(p[0], p[1]), __hmin2_nan(p[2], p[3]));
-    __nv_bfloat162 mx = __hmax2_nan(__hmax2_nan(p[0], p[1]), __hmax2_nan(p[2], p[3]));
+    for (int i = 0; i < 8; ++i) {
+        const __nv_bfloat162 p = *reinterpret_cast<const __nv_bfloat162 *>(&w[i]);
+        mn = i == 0 ? p : __hmin2_nan(mn, p);
+        mx = i == 0 ? p : __hmax2_nan(mx, p);
+    }
 #pragma unroll
     for (int off = 1; off < GL; off <<= 1) {
         mn = __hmin2_nan(mn, __shfl_xor_sync(0xffffffffu, mn, off));
@@ -200,9 +185,9 @@ __device__ __forceinline__ uint32_t quantise8(const uint4 in, uint32_t (&code)[B
     inv = s > 0.f ? inv : 0.f;
     const float zr = ok ? lo : 0.f;
     constexpr uint32_t kMagic = 0x4B400000u;             // 1.5 2^23: adding it leaves the integer in the low bits
-    uint32_t pair[4];                                    // n of two elements in the low bits
+    uint32_t pair[8];                                    // n of two elements in the low bits
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
+    for (int i = 0; i < 8; ++i) {
         const float2 v = make_float2(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xFFFF0000u));
         const float2 t = add2(v, both(-zr));
         float2 q = mul2(t, both(inv));
@@ -212,15 +197,19 @@ __device__ __forceinline__ uint32_t quantise8(const uint4 in, uint32_t (&code)[B
         const float2 m = add2(q, both(__uint_as_float(kMagic)));
         pair[i] = __float_as_uint(m.y) * (1u << BITS) + __float_as_uint(m.x);
     }
-    if constexpr (BITS == 4)
-        code[0] = __byte_perm(__byte_perm(pair[0], pair[1], 0x0040), __byte_perm(pair[2], pair[3], 0x0040), 0x5410);
-    else {
-        code[0] = __byte_perm(pair[0], pair[1], 0x5410);
-        code[1] = __byte_perm(pair[2], pair[3], 0x5410);
+    if constexpr (BITS == 4) {
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+            code[i] = __byte_perm(__byte_perm(pair[4 * i], pair[4 * i + 1], 0x0040),
+                                  __byte_perm(pair[4 * i + 2], pair[4 * i + 3], 0x0040), 0x5410);
+    } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            code[i] = __byte_perm(pair[2 * i], pair[2 * i + 1], 0x5410);
     }
     if (!ok)
 #pragma unroll
-        for (int i = 0; i < BITS / 4; ++i)
+        for (int i = 0; i < BITS / 2; ++i)
             code[i] = 0u;
     return (uint32_t)__bfloat16_as_ushort(sb) | (ok ? (uint32_t)__bfloat16_as_ushort(lob) : 0x7FC0u) << 16;
 }
@@ -230,25 +219,28 @@ __global__ void __launch_bounds__(kRowThreads) kv_write_kernel(KvView kv, KvRows
                                                                const int32_t *count, int start_pos, int *status)
 {
     using F = KvFmt<BITS, D>;
-    using M = RowMap<BITS, D>;
-    constexpr int NI = 64 / (kRowThreads / 32 * M::RPW);  // accesses of a lane for each of K and V
+    using M = RowMap<BITS, D, 16>;
+    constexpr int NI = 64 / (kRowThreads / 32 * M::RPW);  // rows of a lane for each of K and V
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, c = lane % M::CH;
     const int b = blockIdx.y / Hkv, kvh = blockIdx.y % Hkv;
     const PageRows r = page_rows<F>(kv, Hkv, b, kvh, n, start, count, start_pos, status);
     if (r.record == nullptr)
         return;
     const __nv_bfloat16 *src[2] = {
-        static_cast<const __nv_bfloat16 *>(x.k) + b * x.k_stride_b + kvh * x.k_stride_h + r.row0 * x.k_stride_t + 8 * c,
-        static_cast<const __nv_bfloat16 *>(x.v) + b * x.v_stride_b + kvh * x.v_stride_h + r.row0 * x.v_stride_t + 8 * c};
-    uint4 in[2][NI];
+        static_cast<const __nv_bfloat16 *>(x.k) + b * x.k_stride_b + kvh * x.k_stride_h + r.row0 * x.k_stride_t + 16 * c,
+        static_cast<const __nv_bfloat16 *>(x.v) + b * x.v_stride_b + kvh * x.v_stride_h + r.row0 * x.v_stride_t + 16 * c};
+    uint4 in[2][NI][2];
 #pragma unroll
     for (int is_v = 0; is_v < 2; ++is_v)
 #pragma unroll
         for (int i = 0; i < NI; ++i) {
             const int t = (i * (kRowThreads / 32) + warp) * M::RPW + lane / M::CH;
-            in[is_v][i] = make_uint4(0u, 0u, 0u, 0u);
-            if (t >= r.lo && t < r.hi)
-                in[is_v][i] = __ldg(reinterpret_cast<const uint4 *>(src[is_v] + t * (is_v ? x.v_stride_t : x.k_stride_t)));
+            in[is_v][i][0] = in[is_v][i][1] = make_uint4(0u, 0u, 0u, 0u);
+            if (t >= r.lo && t < r.hi) {
+                const uint4 *at = reinterpret_cast<const uint4 *>(src[is_v] + t * (is_v ? x.v_stride_t : x.k_stride_t));
+                in[is_v][i][0] = __ldg(at);
+                in[is_v][i][1] = __ldg(at + 1);
+            }
         }
 #pragma unroll
     for (int is_v = 0; is_v < 2; ++is_v)
@@ -258,20 +250,43 @@ __global__ void __launch_bounds__(kRowThreads) kv_write_kernel(KvView kv, KvRows
             if (tw + M::RPW <= r.lo || tw >= r.hi)
                 continue;                                // the whole warp
             uint32_t code[M::NW];
-            const uint32_t par = quantise8<BITS, D>(in[is_v][i], code);
+            const uint32_t par = quantise16<BITS, D>(in[is_v][i], code);
             const int tok = t % 32;
-            uint8_t *half = r.record + t / 32 * F::HALF, *base = half + (is_v ? F::kCodeV : 0);
+            uint8_t *half = r.record + t / 32 * F::HALF, *row = half + (is_v ? F::kCodeV : 0) + tok * F::R;
             const bool mine = t >= r.lo && t < r.hi;
             if constexpr (BITS == 4) {
-                const uint32_t out = is_v ? v4_exchange<D>(code[0], lane, true) : code[0];
-                if (mine)
-                    *reinterpret_cast<uint32_t *>(base + (is_v ? v_place<4, D>(tok, c) : F::k_off(tok, 4 * c))) = out;
-            } else {
-                uint2 out = make_uint2(code[0], code[1]);
-                if (!is_v)
-                    out = k8_to_store<D>(out, lane);
-                if (mine)
-                    *reinterpret_cast<uint2 *>(base + (is_v ? v_place<8, D>(tok, c) : k8_place<D>(tok, c))) = out;
+                if (!is_v) {                             // words 2c and 2c + 1
+#pragma unroll
+                    for (int k = 0; k < 2; ++k)
+                        if (mine)
+                            *reinterpret_cast<uint32_t *>(row + (((2 * c + k) % 4) * F::NG + c / 2) * 4) = code[k];
+                } else {
+                    // 16-bit runs of chunks 4h .. 4h + 3 (h = c % 2) of group c / 2; a stored
+                    // word is two groups of one chunk: the lanes of an even and an odd
+                    // group trade the two upper and the two lower chunks
+                    const int gr = c / 2, h = c % 2, odd = gr & 1;
+                    const uint32_t got = __shfl_xor_sync(0xffffffffu, odd ? code[0] : code[1], 2);
+                    const uint32_t lo = odd ? got : code[0], hi = odd ? code[1] : got;    // even group, odd group
+#pragma unroll
+                    for (int k = 0; k < 2; ++k) {
+                        const int chunk = 4 * h + 2 * odd + k;
+                        if (mine)
+                            *reinterpret_cast<uint32_t *>(row + (chunk ^ F::v_swizzle(tok)) * (2 * F::NG) + (gr >> 1) * 4) =
+                                __byte_perm(lo, hi, k ? 0x7632 : 0x5410);
+                    }
+                }
+            } else if (!is_v) {                          // words 4c .. 4c + 3, sixteen bytes apart
+                const int p = D == 128 ? (c / 4) ^ (tok & 1) : 0;
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+                    if (mine)
+                        *reinterpret_cast<uint32_t *>(row + (p * 16 + k * 4 + c % 4) * 4) = code[k];
+            } else {                                     // runs of chunks 2c and 2c + 1 (of eight) of group c / 4
+#pragma unroll
+                for (int k = 0; k < 2; ++k)
+                    if (mine)
+                        *reinterpret_cast<uint2 *>(row + ((2 * c % 8 + k) ^ F::v_swizzle(tok)) * (8 * F::NG) + c / 4 * 8) =
+                            make_uint2(code[2 * k], code[2 * k + 1]);
             }
             if (mine && c % M::GL == 0)
                 *reinterpret_cast<uint32_t *>(half + (is_v ? F::kParV : F::kParK) + tok * F::PAR + c / M::GL * 4) = par;
@@ -284,7 +299,7 @@ __global__ void __launch_bounds__(kRowThreads) kv_read_kernel(KvView kv, int Hkv
                                                               __nv_bfloat16 *k, __nv_bfloat16 *v, int *status)
 {
     using F = KvFmt<BITS, D>;
-    using M = RowMap<BITS, D>;
+    using M = RowMap<BITS, D, 8>;
     constexpr int NI = 64 / (kRowThreads / 32 * M::RPW);
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, c = lane % M::CH;
     const int b = blockIdx.y / Hkv, kvh = blockIdx.y % Hkv;
@@ -324,7 +339,7 @@ __global__ void __launch_bounds__(kRowThreads) kv_read_kernel(KvView kv, int Hkv
             uint32_t(&w)[M::NW] = code[is_v][i];
             if constexpr (BITS == 4) {
                 if (is_v)
-                    w[0] = v4_exchange<D>(w[0], lane, false);
+                    w[0] = v4_exchange<D>(w[0], lane);
             } else if (!is_v) {
                 const uint2 x = k8_from_store<D>(make_uint2(w[0], w[1]), lane);
                 w[0] = x.x;

@@ -205,11 +205,6 @@ __device__ __forceinline__ void prepare_q(const __nv_bfloat16 *qp, int lane, Hea
         out->inv = pow2_field(127 - qe);
 }
 
-// The scale of a param word as a float.  The integer and shift pipe is the busiest
-// of the loop (two cycles an instruction), so the shift is a multiplication by a
-// 2^16 that the compiler does not see.
-__device__ __forceinline__ float scale_of(uint32_t par, uint32_t two16) { return __uint_as_float(par * two16); }
-
 struct DecodeArgs {
     const __nv_bfloat16 *q_tok;
     KvView kv;
@@ -223,7 +218,6 @@ struct DecodeArgs {
     float *lse;
     int *status;
     uint64_t timeout_ns;
-    uint32_t two16;                      // 65536
 };
 
 // Warps of a CTA and half records in flight per warp.  Two CTAs share an SM, so
@@ -431,7 +425,7 @@ __global__ void __launch_bounds__(DecodeCfg<BITS, D>::W * 32, 2) decode_quant_ke
         }
     }
     __syncthreads();
-    uint32_t qf[KS][2], qz[3];                      // operands of column gid
+    uint32_t qf[KS][2];                             // operands of column gid
     {
         const HeadQ<D> &q = s_q[gid];
 #pragma unroll
@@ -451,10 +445,6 @@ __global__ void __launch_bounds__(DecodeCfg<BITS, D>::W * 32, 2) decode_quant_ke
                 }
             }
         }
-        // the params' operand is (s, z) of group tig: 0 for s and the sum for z
-#pragma unroll
-        for (int i = 0; i < 3; ++i)
-            qz[i] = tig < NG ? (uint32_t)q.sum[i][tig] << 16 : 0u;
     }
     // a score in units of log2: its raw sum times fac (kept off 0 and infinity, so
     // that a masked score's -infinity stays one)
@@ -594,6 +584,12 @@ __global__ void __launch_bounds__(DecodeCfg<BITS, D>::W * 32, 2) decode_quant_ke
             }
         }
         const uint8_t *h = my + st * F::HALF;
+        // the operand against the params as they lie, (s, z) of group tig: 0 for s and
+        // q's sum for z (read again here: a register less in the loop)
+        uint32_t qz[3];
+#pragma unroll
+        for (int i = 0; i < 3; ++i)
+            qz[i] = tig < NG ? (uint32_t)s_q[gid].sum[i][tig] << 16 : 0u;
 
         // ---- raw scores of two 16-token tiles
         float s[2][4];
@@ -648,7 +644,7 @@ __global__ void __launch_bounds__(DecodeCfg<BITS, D>::W * 32, 2) decode_quant_ke
                     else
                         mma16816(c, x[0], x[1], x[2], x[3], qf[ks][0], qf[ks][1]);
                 }
-                const float sa = scale_of(pa[gr], a.two16), sb = scale_of(pb[gr], a.two16);
+                const float sa = kv_scale(pa[gr]), sb = kv_scale(pb[gr]);
                 s[mt][0] = fmaf(sa, c[0], s[mt][0]);
                 s[mt][1] = fmaf(sa, c[1], s[mt][1]);
                 s[mt][2] = fmaf(sb, c[2], s[mt][2]);
@@ -759,7 +755,7 @@ __global__ void __launch_bounds__(DecodeCfg<BITS, D>::W * 32, 2) decode_quant_ke
                 pu[e] = p[e] * up;
 #pragma unroll
             for (int gr = 0; gr < NG; ++gr) {
-                const float sa = scale_of(vp[mt][0][gr], a.two16), sb = scale_of(vp[mt][1][gr], a.two16);
+                const float sa = kv_scale(vp[mt][0][gr]), sb = kv_scale(vp[mt][1][gr]);
                 const float za = kv_zero(vp[mt][0][gr]), zb = kv_zero(vp[mt][1][gr]);
                 const uint32_t b0 = movmatrix(pack_half2(pu[0] * sa, pu[1] * sa));
                 const uint32_t b1 = movmatrix(pack_half2(pu[2] * sb, pu[3] * sb));
@@ -873,27 +869,38 @@ __global__ void __launch_bounds__(DecodeCfg<BITS, D>::W * 32, 2) decode_quant_ke
     }
 }
 
-// The splits of one head: weights 2^(m_s - M), o = sum w o / sum w l.
-template <int D>
-__global__ void __launch_bounds__(D) decode_quant_merge_kernel(const DecodeArgs a)
+// The splits of one head: weights 2^(m_s - M), o = sum w o / sum w l.  Q threads
+// share an output element, every Q-th split each, and their first loads are in
+// flight before a weight is known.  Four from nine splits on: one latency, not
+// one per eight splits (128k tokens, 37 splits: 2.7 us less of 40.8); one for few
+// (1024 heads of two splits: 90 us a call, 96 with four).
+template <int D, int Q>
+__global__ void __launch_bounds__(Q * D) decode_quant_merge_kernel(const DecodeArgs a)
 {
-    __shared__ float s_w[kMaxDecodeSplits];
+    constexpr int N = Q == 4 ? kMaxDecodeSplits / 4 : 8;
+    __shared__ float s_w[kMaxDecodeSplits], s_part[Q][D];
     const long long bh = blockIdx.x;
-    const int lane = threadIdx.x & 31;
+    const int lane = threadIdx.x & 31, c = threadIdx.x % D, q = threadIdx.x / D;
     const int nsplit = splits_of(a, blockIdx.x / a.Hq, lane);
     if (nsplit == 1)
         return;                                     // written by its one split
     const float *pp = a.part + bh * kMaxDecodeSplits * (D + 2);
-    __nv_bfloat16 *o = a.o;
-    float *lse = a.lse;
-    float ms[2], ls[2], M = -INFINITY;
+    float v[N], ms[2], ls[2], M = -INFINITY;
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
         const int s = lane + 32 * i;
         ms[i] = s < nsplit ? pp[s * (D + 2) + D] : -INFINITY;
         ls[i] = s < nsplit ? pp[s * (D + 2) + D + 1] : 0.f;
-        M = fmaxf(M, ms[i]);
     }
+    auto load = [&](int s0) {
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            const int s = s0 + Q * i + q;
+            v[i] = s < nsplit ? pp[s * (D + 2) + c] : 0.f;
+        }
+    };
+    load(0);
+    M = fmaxf(ms[0], ms[1]);
 #pragma unroll
     for (int off = 16; off >= 1; off >>= 1)
         M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, off));
@@ -902,20 +909,34 @@ __global__ void __launch_bounds__(D) decode_quant_merge_kernel(const DecodeArgs 
     for (int i = 0; i < 2; ++i) {
         const float w = split_weight(ms[i], ls[i], M);
         l = fmaf(w, ls[i], l);
-        if (threadIdx.x < 32 && lane + 32 * i < nsplit)
-            s_w[lane + 32 * i] = w;
+        if (threadIdx.x < 32)
+            s_w[lane + 32 * i] = w;                 // 0 past the last split
     }
 #pragma unroll
     for (int off = 16; off >= 1; off >>= 1)
         l += __shfl_xor_sync(0xffffffffu, l, off);
     __syncthreads();
     float acc = 0.f;
-#pragma unroll 8
-    for (int s = 0; s < nsplit; ++s)
-        acc = fmaf(s_w[s], pp[s * (D + 2) + threadIdx.x], acc);
-    o[bh * D + threadIdx.x] = __float2bfloat16_rn(l == 0.f ? 0.f : acc / l);
-    if (lse != nullptr && threadIdx.x == 0)
-        lse[bh] = log_sum(M, l);
+    for (int s0 = 0; s0 < nsplit; s0 += N * Q) {
+        if (s0 > 0)
+            load(s0);
+#pragma unroll
+        for (int i = 0; i < N; ++i)
+            acc = fmaf(s_w[s0 + Q * i + q], v[i], acc);
+    }
+    if constexpr (Q > 1) {
+        s_part[q][c] = acc;
+        __syncthreads();
+        if (q != 0)
+            return;
+        acc = 0.f;
+#pragma unroll
+        for (int i = 0; i < Q; ++i)
+            acc += s_part[i][c];
+    }
+    a.o[bh * D + c] = __float2bfloat16_rn(l == 0.f ? 0.f : acc / l);
+    if (a.lse != nullptr && c == 0)
+        a.lse[bh] = log_sum(M, l);
 }
 
 // Estimated time, in us, of `ctas` CTAs with `blocks` blocks each:
@@ -995,7 +1016,10 @@ cudaError_t launch(DecodeArgs a, cudaStream_t stream)
     e = cudaGetLastError();
     if (e != cudaSuccess || (a.slots == 0 && a.nsplit == 1))
         return e;
-    decode_quant_merge_kernel<D><<<a.B * a.Hq, D, 0, stream>>>(a);
+    if ((a.slots > 0 ? a.slots / a.B : a.nsplit) > 8)
+        decode_quant_merge_kernel<D, 4><<<a.B * a.Hq, 4 * D, 0, stream>>>(a);
+    else
+        decode_quant_merge_kernel<D, 1><<<a.B * a.Hq, D, 0, stream>>>(a);
     return cudaGetLastError();
 }
 
@@ -1021,7 +1045,6 @@ cudaError_t launch_decode_quant(int bits, int B, int Hq, int Hkv, int L, int d, 
     a.lse = lse;
     a.status = status;
     a.timeout_ns = timeout_ns;
-    a.two16 = 65536u;
     if (bits == 4)
         return d == 128 ? launch<4, 128>(a, stream) : launch<4, 64>(a, stream);
     return d == 128 ? launch<8, 128>(a, stream) : launch<8, 64>(a, stream);

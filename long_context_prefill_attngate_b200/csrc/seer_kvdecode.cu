@@ -425,27 +425,6 @@ __global__ void __launch_bounds__(DecodeCfg<BITS, D>::W * 32, 2) decode_quant_ke
         }
     }
     __syncthreads();
-    uint32_t qf[KS][2];                             // operands of column gid
-    {
-        const HeadQ<D> &q = s_q[gid];
-#pragma unroll
-        for (int i = 0; i < KS; i += 2) {
-            if (BITS == 4) {                        // a word's eight elements: two MMA steps
-                const uint4 u = *reinterpret_cast<const uint4 *>(q.f16 + 16 * i + 8 * tig);
-                qf[i][0] = u.x;
-                qf[i][1] = u.y;
-                qf[i + 1][0] = u.z;
-                qf[i + 1][1] = u.w;
-            } else {
-#pragma unroll
-                for (int k = 0; k < 2; ++k) {
-                    const uint2 u = *reinterpret_cast<const uint2 *>(q.f16 + 16 * (i + k) + 4 * tig);
-                    qf[i + k][0] = u.x;
-                    qf[i + k][1] = u.y;
-                }
-            }
-        }
-    }
     // a score in units of log2: its raw sum times fac (kept off 0 and infinity, so
     // that a masked score's -infinity stays one)
     float fac[2];
@@ -584,12 +563,33 @@ __global__ void __launch_bounds__(DecodeCfg<BITS, D>::W * 32, 2) decode_quant_ke
             }
         }
         const uint8_t *h = my + st * F::HALF;
-        // the operand against the params as they lie, (s, z) of group tig: 0 for s and
-        // q's sum for z (read again here: a register less in the loop)
-        uint32_t qz[3];
+        // q's operands of column gid (read for every half record: the registers are
+        // P V's afterwards) and the one against the params as they lie, (s, z) of
+        // group tig: 0 for s, q's sum for z
+        uint32_t qf[KS][2], qz[3];
+        {
+            const HeadQ<D> &q = s_q[gid];
 #pragma unroll
-        for (int i = 0; i < 3; ++i)
-            qz[i] = tig < NG ? (uint32_t)s_q[gid].sum[i][tig] << 16 : 0u;
+            for (int i = 0; i < KS; i += 2) {
+                if (BITS == 4) {                    // a word's eight elements: two MMA steps
+                    const uint4 x = *reinterpret_cast<const uint4 *>(q.f16 + 16 * i + 8 * tig);
+                    qf[i][0] = x.x;
+                    qf[i][1] = x.y;
+                    qf[i + 1][0] = x.z;
+                    qf[i + 1][1] = x.w;
+                } else {
+#pragma unroll
+                    for (int k = 0; k < 2; ++k) {
+                        const uint2 x = *reinterpret_cast<const uint2 *>(q.f16 + 16 * (i + k) + 4 * tig);
+                        qf[i + k][0] = x.x;
+                        qf[i + k][1] = x.y;
+                    }
+                }
+            }
+#pragma unroll
+            for (int i = 0; i < 3; ++i)
+                qz[i] = tig < NG ? (uint32_t)q.sum[i][tig] << 16 : 0u;
+        }
 
         // ---- raw scores of two 16-token tiles
         float s[2][4];

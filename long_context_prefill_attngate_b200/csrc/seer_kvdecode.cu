@@ -28,6 +28,14 @@
 //    lane's register pair: movmatrix turns each 8 x 8 piece.
 //  * Split over the union's blocks by rank, so splits differ by one block at
 //    most; a second kernel joins them.
+//
+// What bounds it: with 8 bits and long caches HBM (128k tokens at density 0.17: the loop
+// itself reads 7 TB/s; 37.7 us a call with start, end and join, 22.8 at the copy
+// rate).  With 4 bits the instructions of the loop: some 350 a tile of 16 tokens
+// and warp, 160 of them on the integer pipe at two cycles each, against 6 cycles
+// a token that HBM allows (32k tokens of a layer, all active: 20.7 us, 6.4 at the
+// copy rate).  Short ones: a CTA's start and end, some 8,000 cycles of latencies,
+// and the join (32k at density 0.1: 11.8 us; 200 tokens: 4.8).
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -39,7 +47,7 @@ namespace seer {
 namespace {
 
 constexpr int kHeads = 8;                 // query heads of a CTA: the N of the MMA
-constexpr int kListMax = 513;             // blocks of a split (decode_quant_splits)
+constexpr int kListMax = 513;             // blocks of a split (decode_quant_split)
 constexpr int kNoPage = kMaxNb;           // flag of a list entry; block indices are below it
 
 __device__ __forceinline__ float exp2_approx(float x)
@@ -944,8 +952,8 @@ __global__ void __launch_bounds__(Q * D) decode_quant_merge_kernel(const DecodeA
 //   a block                   0.4 for a CTA alone, 0.31 of the SM for two
 //   the second kernel         2 and 0.04 a split
 // Measured (4 bits, D = 128): 8 units (a sequence's head tile) of 512 blocks, all
-// active: 9 splits 31.2 us, 18: 22.5, 36: 23.2; a tenth active: 15.7, 13.4, 15.2;
-// 128 units of 256: 1 split 104 us, 2: 89, 3: 96, 8: 94.
+// active: 18 splits 20.7 us, 24: 23.8, 37: 19.8; a tenth active: 9: 15.2, 18: 11.8,
+// 37: 12.4; 128 units of 256: 1 split 97 us, 2: 86, 4: 91.
 double decode_quant_us(long long ctas, double blocks, double splits, int sms)
 {
     const long long load = (ctas + sms - 1) / sms, waves = (load + 1) / 2;
@@ -957,7 +965,7 @@ double decode_quant_us(long long ctas, double blocks, double splits, int sms)
 // blocks active (the mask is on the device) and at least a block for every
 // second warp.  Lengths given: one or two CTAs per SM in all, where there are
 // enough for every sequence's tiles, shared out by length: a batch of 8 from 32k
-// tokens down took 48 us with 4 splits each, 42 so.  Not for two or three
+// tokens down takes 45 us with 4 splits each, 39 so.  Not for two or three
 // sequences, whose CTAs pair up on the SMs (64k and 37k tokens at 8 bits: 42 us with
 // 18 splits each, 45 shared out), and in whole splits where a sequence has few
 // (16 of 16k tokens: 88 us with two each, 90 with 37 slots).

@@ -18,6 +18,11 @@
 //    fp32 as with plain fp32 FMAs.
 //  * Rotation as in the bf16 cache's key rows: frequency and angle in double,
 //    reduced modulo 2 pi, then fp32.
+//
+// 512 blocks of 8 heads at 4 bits (D = d_gate = 128): 11.1 us for 23 MB, of which the
+// pooling of a warp's two blocks, one after the other, is 60 % (latency and
+// instructions; HBM alone would be 3.6 us), the projection and the rotation 8 % each;
+// the last block of 4 sequences (max+min, 8 bits): 5.1 us, all latency.
 #include <cmath>
 
 #include <cuda_bf16.h>

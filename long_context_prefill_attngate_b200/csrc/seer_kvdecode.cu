@@ -4,14 +4,15 @@
 //   o[b,h] = sum over t < len in active blocks of softmax(q . k_t * scale) v_t,
 //   k_t = z + s n (per group of the row), v_t likewise.
 //
-// Each active block crosses HBM once per GQA group: a CTA serves up to eight
-// query heads of one KV head over the union of their active blocks (a head
-// without a block gets p = 0 there).  At 4 bits a token's K and V are 160 bytes
+// Each active block crosses HBM once per GQA group: a CTA serves up to eight, or
+// sixteen, query heads of one KV head over the union of their active blocks (a
+// head without a block gets p = 0 there).  At 4 bits a token's K and V are 160 bytes
 // for 4 D flops per head, so with CUDA-core products the arithmetic, not HBM,
 // would set the time (at D = 128 and four heads 2048 flops per 160 bytes); the
 // products are mma.sync m16n8k16 with the keys on M (K Q^T) or the output
-// elements on M (V^T P) and the heads on N.  Decode has at most eight columns
-// of N, which leaves a tcgen05 tile nothing to gain.
+// elements on M (V^T P) and the heads on N; with more than eight heads the other
+// way round (Sums<.., 16>).  Sixteen rows at most leave a tcgen05 tile nothing to
+// gain.
 //
 //  * The codes enter the MMA as they are: n <= 255 in the low bits of an fp16 is
 //    the subnormal n 2^-24, so one mask (4 bits) or byte permute (8 bits) makes
@@ -19,9 +20,11 @@
 //      q . k   = sum_g s_g (q_g . n_g) + z_g sum(q_g)        per key; the second by an
 //                MMA of the params as they lie with sum(q_g) in three bf16 parts
 //      sum p v = sum_t (p_t s_t,g) n_t + sum_t p_t z_t,g      p s rounded to fp16
-//    q is exact in fp16 after a power of two per head; p s <= 2^15 after a power
+//    q is exact in fp16 after a power of two per head; p s < 2^15 after a power
 //    of two that follows the largest scale seen (as a running maximum, so it
 //    holds for any range of V).  p z, the row sums and all accumulators are fp32.
+//  * The running maximum moves when a score is 2^6 above it, so the accumulators
+//    are rescaled a few times per warp, and p reaches 2^6 at most.
 //  * Work of a warp: half records of 32 tokens, each one contiguous bulk copy
 //    into the warp's own ring, so no warp waits for another until the end.
 //  * P leaves K Q^T with keys across lanes and enters V^T P with keys across a
@@ -46,8 +49,8 @@ namespace seer {
 
 namespace {
 
-constexpr int kHeads = 8;                 // query heads of a CTA: the N of the MMA
 constexpr int kListMax = 513;             // blocks of a split (decode_quant_split)
+constexpr int kSlack = 6;                  // a maximum moves when a score is 2^kSlack above it
 constexpr int kNoPage = kMaxNb;           // flag of a list entry; block indices are below it
 
 __device__ __forceinline__ float exp2_approx(float x)
@@ -153,65 +156,98 @@ __device__ __forceinline__ void load_words(uint32_t (&w)[N], const uint8_t *p)
 // a V fragment reads at once differ in the bits its swizzle uses.
 __device__ __forceinline__ int tile_token(int r) { return r ^ ((r >> 1) & 1); }
 
-// q of one head for the MMAs, by one warp: its elements in fp16 times 2^qe, in
-// the order of the codes' operands (at 4 bits a word's elements 0,4,1,5,2,6,3,7
-// with the odd ones times 2^-4, as the codes' masks give them), its group sums in
-// three bf16 parts (for the products with z), and 2^-qe.
-template <int D>
-struct HeadQ {
-    uint16_t f16[D];
-    uint16_t sum[3][4];
-    float inv;
-    uint32_t pad;
-};
+// q for the MMAs: row gid of w holds head gid, or heads gid and gid + 8.  First
+// its elements in fp16 times 2^qe in the order of the codes' operands (at 4 bits
+// a word's elements 0,4,1,5,2,6,3,7 with the odd ones times 2^-4, as the codes'
+// masks give them), 16 bytes a lane at a time: two steps' B operands of eight
+// heads, one step's A operand of sixteen.  Then its group sums in three bf16
+// parts for the products with z: an operand step meets the params' words (s, z)
+// of a token as they lie, 0 in the place of s and a part in that of z.  Rows are
+// 16 banks apart, so eight lanes read 16 bytes each without a conflict.
+template <int BITS, int D, int H>
+struct QShared {
+    static constexpr int NG = KvFmt<BITS, D>::NG, P = H / 8;
+    static constexpr int STEPS = NG == 4 ? 2 : 1;   // MMA steps of z sum(q)
+    static constexpr int kSum = P * D / 2;
+    static constexpr int LEN = kSum + P * 8 * STEPS;
+    uint32_t w[8][LEN + (48 - LEN % 32) % 32];
+    float inv[H];                                   // 2^-qe
 
-template <int BITS, int D>
-__device__ __forceinline__ void prepare_q(const __nv_bfloat16 *qp, int lane, HeadQ<D> *out)
-{
-    constexpr int N = D / 32, GL = KvFmt<BITS, D>::G / N;   // elements of a lane, lanes of a group
-    float f[N];
-    if constexpr (N == 4) {
-        const uint2 u = qp != nullptr ? __ldg(reinterpret_cast<const uint2 *>(qp) + lane) : make_uint2(0u, 0u);
-        f[0] = __uint_as_float(u.x << 16);
-        f[1] = __uint_as_float(u.x & 0xFFFF0000u);
-        f[2] = __uint_as_float(u.y << 16);
-        f[3] = __uint_as_float(u.y & 0xFFFF0000u);
-    } else {
-        const uint32_t u = qp != nullptr ? __ldg(reinterpret_cast<const uint32_t *>(qp) + lane) : 0u;
-        f[0] = __uint_as_float(u << 16);
-        f[1] = __uint_as_float(u & 0xFFFF0000u);
+    // Element e's half word.
+    __device__ __forceinline__ static int at(int h, int e)
+    {
+        const int ks = BITS == 4 ? e / 32 * 2 + (e >> 1 & 1) : e / 16, tig = BITS == 4 ? e / 8 % 4 : e / 4 % 4;
+        const int reg = BITS == 4 ? e & 1 : e >> 1 & 1, half = BITS == 4 ? e >> 2 & 1 : e & 1;
+        const int word = P == 1 ? (ks / 2 * 4 + tig) * 4 + ks % 2 * 2 + reg : (ks * 4 + tig) * 4 + reg * 2 + h / 8;
+        return 2 * word + half;
     }
-    float mx = 0.f;
-#pragma unroll
-    for (int i = 0; i < N; ++i)
-        mx = fmaxf(mx, fabsf(f[i]));
-    // max |q| 2^qe in [2^14, 2^15) where 2^qe is a float; no scaling for infinity
-    const int eb = (int)(__reduce_max_sync(0xffffffffu, __float_as_uint(mx)) >> 23);
-    const int qe = eb == 255 ? 0 : min(141 - eb, 126);
-    const float up = pow2_field(127 + qe);
-    float s = 0.f;
-#pragma unroll
-    for (int i = 0; i < N; ++i) {
-        f[i] *= up;
-        s += f[i];
-        const int e = N * lane + i;
-        const int at = BITS == 4 ? (e & ~7) + (e & 3) * 2 + (e >> 2 & 1) : e;
-        out->f16[at] = __half_as_ushort(__float2half_rn(BITS == 4 && e & 1 ? f[i] * 0.0625f : f[i]));
+    // The word of register r of a step that meets group gr's params: part i, or 0 for the places left.
+    static constexpr int kPlaces = NG == 1 ? 8 : 4;
+    __device__ __forceinline__ static int at_sum(int h, int gr, int i)
+    {
+        const int step = NG == 4 ? i >> 1 : 0;
+        const int tig = NG == 4 ? (gr >> 1) + 2 * (i & 1) : NG == 2 ? i : i >> 1;
+        const int r = NG == 4 ? gr & 1 : NG == 2 ? gr : i & 1;
+        return kSum + (P == 1 ? (tig * STEPS + step) * 2 + r : (tig * STEPS + step) * 4 + r * 2 + h / 8);
     }
-#pragma unroll
-    for (int off = 1; off < GL; off <<= 1)
-        s += __shfl_xor_sync(0xffffffffu, s, off);
-    s *= 5.9604644775390625e-8f;                    // 2^-24: the unit of the codes' products
-    if (lane % GL == 0)
-#pragma unroll
-        for (int i = 0; i < 3; ++i) {
-            const __nv_bfloat16 part = __float2bfloat16_rn(s);
-            out->sum[i][lane / GL] = __bfloat16_as_ushort(part);
-            s -= __bfloat162float(part);
+    // The byte, within a token's params, of the word that lane tig's register r meets.
+    __device__ __forceinline__ static int par_at(int tig, int r) { return NG == 4 ? 8 * (tig & 1) + 4 * r : NG == 2 ? 4 * r : 0; }
+
+    // Head h by one warp: a lane's elements from memory (0 where qp is null) ...
+    static constexpr int N = D / 32;
+    using Raw = uint32_t[N / 2];
+    __device__ __forceinline__ static void fetch(Raw &u, const __nv_bfloat16 *qp, int lane)
+    {
+        if constexpr (N == 4) {
+            const uint2 x = qp != nullptr ? __ldg(reinterpret_cast<const uint2 *>(qp) + lane) : make_uint2(0u, 0u);
+            u[0] = x.x;
+            u[1] = x.y;
+        } else {
+            u[0] = qp != nullptr ? __ldg(reinterpret_cast<const uint32_t *>(qp) + lane) : 0u;
         }
-    if (lane == 0)
-        out->inv = pow2_field(127 - qe);
-}
+    }
+    // ... and into its row.
+    __device__ __forceinline__ void prepare(const Raw &u, int h, int lane)
+    {
+        constexpr int GL = KvFmt<BITS, D>::G / N;   // lanes of a group
+        float f[N];
+#pragma unroll
+        for (int i = 0; i < N / 2; ++i) {
+            f[2 * i] = __uint_as_float(u[i] << 16);
+            f[2 * i + 1] = __uint_as_float(u[i] & 0xFFFF0000u);
+        }
+        float mx = 0.f;
+#pragma unroll
+        for (int i = 0; i < N; ++i)
+            mx = fmaxf(mx, fabsf(f[i]));
+        // max |q| 2^qe in [2^14, 2^15) where 2^qe is a float; no scaling for infinity
+        const int eb = (int)(__reduce_max_sync(0xffffffffu, __float_as_uint(mx)) >> 23);
+        const int qe = eb == 255 ? 0 : min(141 - eb, 126);
+        const float up = pow2_field(127 + qe);
+        uint32_t *row = w[h % 8];
+        uint16_t *half = reinterpret_cast<uint16_t *>(row);
+        float s = 0.f;
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            f[i] *= up;
+            s += f[i];
+            half[at(h, N * lane + i)] = __half_as_ushort(__float2half_rn(BITS == 4 && i & 1 ? f[i] * 0.0625f : f[i]));
+        }
+#pragma unroll
+        for (int off = 1; off < GL; off <<= 1)
+            s += __shfl_xor_sync(0xffffffffu, s, off);
+        s *= 5.9604644775390625e-8f;                // 2^-24: the unit of the codes' products
+        if (lane % GL == 0)
+#pragma unroll
+            for (int i = 0; i < kPlaces; ++i) {
+                const __nv_bfloat16 part = __float2bfloat16_rn(s);
+                row[at_sum(h, lane / GL, i)] = i < 3 ? (uint32_t)__bfloat16_as_ushort(part) << 16 : 0u;
+                s -= __bfloat162float(part);
+            }
+        if (lane == 0)
+            inv[h] = pow2_field(127 - qe);
+    }
+};
 
 struct DecodeArgs {
     const __nv_bfloat16 *q_tok;
@@ -231,10 +267,12 @@ struct DecodeArgs {
 // Warps of a CTA and half records in flight per warp.  Two CTAs share an SM, so
 // that one's start and end (some 8,000 cycles of latencies) pass under the
 // other's products; their rings hold 70 to 200 KB, where the SM's share of HBM
-// (24 bytes a cycle) needs some 40 KB in flight.
-template <int BITS, int D>
+// (24 bytes a cycle) needs some 40 KB in flight.  Sixteen heads: at D = 128 the
+// accumulators leave four warps their registers (64 units of 256 blocks at 4 bits:
+// 72 us, 74 with six warps, which spill; at 8 bits 59 and 65), at D = 64 six.
+template <int BITS, int D, int H>
 struct DecodeCfg {
-    static constexpr int W = BITS == 8 && D == 128 ? 6 : 8;
+    static constexpr int W = H == 16 ? (D == 128 ? 4 : 6) : BITS == 8 && D == 128 ? 6 : 8;
     static constexpr int ST = BITS == 4 && D == 64 ? 4 : 2;
     static constexpr int ring = W * ST * KvFmt<BITS, D>::HALF;
 };
@@ -317,287 +355,74 @@ __device__ __forceinline__ int splits_of(const DecodeArgs &a, int b, int lane)
     return min(__shfl_sync(0xffffffffu, b < 32 ? s.count[0] : s.count[1], b & 31), kMaxDecodeSplits);
 }
 
+// What a warp sums up for the heads of its CTA, half record by half record.
+template <int BITS, int D, int H>
+struct Sums;
+
+// Up to eight heads: on N, keys or output elements on M.
 template <int BITS, int D>
-__global__ void __launch_bounds__(DecodeCfg<BITS, D>::W * 32, 2) decode_quant_kernel(const DecodeArgs a)
-{
+struct Sums<BITS, D, 8> {
     using F = KvFmt<BITS, D>;
-    using C = DecodeCfg<BITS, D>;
-    constexpr int W = C::W, ST = C::ST, NG = F::NG, R = F::R;
-    constexpr int KS = D / 16;                      // MMA steps of a score; also MMA rows of an output / 16
-    constexpr int KW = R / 16, VW = R / 32;         // 32-bit words of a lane's K row, V row
-    constexpr int UPG = KS / NG;                    // MMAs of a group
-    extern __shared__ __align__(128) uint8_t ring[];
-    __shared__ __align__(8) uint64_t s_bar[W * ST];
-    __shared__ float2 s_ml[W][kHeads], s_sum[kHeads];
-    __shared__ uint32_t s_words[kMaxNb / 32];
-    __shared__ uint32_t s_rec[kListMax];            // a block's record from the start of the pages, in 512 bytes
-    __shared__ uint16_t s_block[kListMax];
-    __shared__ __align__(16) HeadQ<D> s_q[kHeads];
+    static constexpr int NG = F::NG, R = F::R;
+    static constexpr int KS = D / 16;               // MMA steps of a score; also MMA rows of an output / 16
+    static constexpr int KW = R / 16, VW = R / 32;  // 32-bit words of a lane's K row, V row
+    static constexpr int UPG = KS / NG;             // MMAs of a group
+    using Q = QShared<BITS, D, 8>;
 
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int gid = lane >> 2, tig = lane & 3;
-    int b, split, ns;
-    if (!slot_of(a, lane, b, split, ns))
-        return;
-    const int tile = blockIdx.y % a.tiles, kvh = blockIdx.y / a.tiles;
-    const int g = a.Hq / a.Hkv;
-    const int h0 = kvh * g + tile * a.per_tile;     // first query head, and how many
-    const int gt = min(a.per_tile, g - tile * a.per_tile);
-    const int len = a.lens != nullptr ? max(0, min(a.lens[b], a.L)) : a.L;
-    const uint8_t *mrow = a.mask + ((long long)b * a.Hq + h0) * a.nb;
+    float m[2], l[2], zacc[NG][2], acc[KS][4], fac[2];
+    int ve;                                         // exponent field of V's largest scale so far
+    int gid, tig, tr, at_k, at_p, at_z, at_v0, at_v1;
 
-    if (lane == 0) {
-        for (int s = 0; s < ST; ++s)
-            mbar_init(smem_u32(&s_bar[warp * ST + s]), 1);
-        fence_mbar_init();
-    }
-
-    // ---- q, a warp per head (0 where there is none)
-    for (int h = warp; h < kHeads; h += W)
-        prepare_q<BITS, D>(h < gt ? a.q_tok + ((long long)b * a.Hq + h0 + h) * D : nullptr, lane, &s_q[h]);
-
-    // ---- union of the heads' active blocks, one bit each.  Rows short enough for
-    // one round of kMaskWords words of 32 blocks a warp: a block a lane, and its
-    // table entry, all loads in flight together (and before the length is known).
-    // Longer rows: four blocks a lane, where the rows' alignment allows it, and
-    // the table is looked up for this split's blocks alone.
-    constexpr int kMaskWords = BITS == 8 && D == 128 ? 6 : 4;
-    const int nblk = (len + 63) / 64, nwords = (nblk + 31) / 32;
-    const bool one_round = a.nb <= 32 * kMaskWords * W;
-    int page[kMaskWords];
-    if (one_round || a.nb % 4 != 0 || (reinterpret_cast<uintptr_t>(a.mask) & 3) != 0) {
-        for (int c0 = warp; c0 < (c0 == warp ? (a.nb + 31) / 32 : nwords); c0 += kMaskWords * W) {
-            int raw[kMaskWords][kHeads];
-            // (blocks past the row read its last one: the branches are the warp's)
-#pragma unroll
-            for (int i = 0; i < kMaskWords; ++i) {
-                if (i > 0 && (c0 + i * W) * 32 >= a.nb)
-                    continue;
-                const int j = min((c0 + i * W) * 32 + lane, a.nb - 1);
-#pragma unroll
-                for (int h = 0; h < kHeads; ++h) {
-                    raw[i][h] = 0;
-                    if (h < gt)
-                        raw[i][h] = __ldg(mrow + (long long)h * a.nb + j);
-                }
-                if (one_round) {
-                    page[i] = b * a.kv.max_blocks + j;
-                    if (a.kv.table != nullptr)
-                        page[i] = __ldg(a.kv.table + page[i]);
-                }
-            }
-#pragma unroll
-            for (int i = 0; i < kMaskWords; ++i) {
-                const int c = c0 + i * W;
-                if (c >= nwords)
-                    continue;
-                int any = 0;
-#pragma unroll
-                for (int h = 0; h < kHeads; ++h)
-                    any |= raw[i][h];
-                const unsigned bits = __ballot_sync(0xffffffffu, any != 0 && c * 32 + lane < nblk);
-                if (lane == 0)
-                    s_words[c] = bits;
-            }
-        }
-    } else {
-        for (int c0 = warp; c0 * 4 < nwords; c0 += 4 * W) {
-            uint32_t raw[4][kHeads];
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const int j = min((c0 + i * W) * 128 + 4 * lane, a.nb - 4);
-#pragma unroll
-                for (int h = 0; h < kHeads; ++h) {
-                    raw[i][h] = 0;
-                    if (h < gt)
-                        raw[i][h] = __ldg(reinterpret_cast<const uint32_t *>(mrow + (long long)h * a.nb + j));
-                }
-            }
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const int j = (c0 + i * W) * 128 + 4 * lane;
-                uint32_t x = 0;
-#pragma unroll
-                for (int h = 0; h < kHeads; ++h)
-                    x |= raw[i][h];
-                // bytes that are not 0 -> four bits -> words of eight lanes
-                x = (((x & 0x7F7F7F7Fu) + 0x7F7F7F7Fu) | x) >> 7 & 0x01010101u;
-                x = x * 0x10204080u >> 28 & ((1u << max(0, min(4, nblk - j))) - 1u);
-                x <<= 4 * (lane & 7);
-                x |= __shfl_xor_sync(0xffffffffu, x, 1);
-                x |= __shfl_xor_sync(0xffffffffu, x, 2);
-                x |= __shfl_xor_sync(0xffffffffu, x, 4);
-                if ((lane & 7) == 0 && j / 32 < nwords)
-                    s_words[j / 32] = x;
-            }
-        }
-    }
-    __syncthreads();
-    // a score in units of log2: its raw sum times fac (kept off 0 and infinity, so
-    // that a masked score's -infinity stays one)
-    float fac[2];
-#pragma unroll
-    for (int e = 0; e < 2; ++e)
-        fac[e] = fminf(fmaxf(s_q[2 * tig + e].inv * (a.scale_log2 * 16777216.f), 1.2e-38f), 3e38f);
-
-    // ---- this split's blocks: ranks [r0, r1) of the union
-    int r0, r1;
+    __device__ __forceinline__ void clear()
     {
-        // words of a lane: a power of two (32 lanes cover the words)
-        const int lg = nwords > 32 ? 32 - __clz((nwords - 1) >> 5) : 0, per = 1 << lg;
-        int cnt = 0;
-        for (int k = 0; k < per; ++k)
-            if (lane * per + k < nwords)
-                cnt += __popc(s_words[lane * per + k]);
-        int inc = cnt;
-#pragma unroll
-        for (int off = 1; off < 32; off <<= 1) {
-            const int v = __shfl_up_sync(0xffffffffu, inc, off);
-            inc += lane >= off ? v : 0;
-        }
-        const int total = __shfl_sync(0xffffffffu, inc, 31);
-        // total * split / ns: at most 2^20, and inv is 2^32 / ns rounded up by less
-        // than 2^-26 of it, so the product's high word is the quotient (one split:
-        // inv is 0 and so is r0)
-        const unsigned inv = 0xFFFFFFFFu / (unsigned)ns + 1u;
-        r0 = (int)__umulhi((unsigned)(total * split), inv);
-        r1 = split + 1 == ns ? total : (int)__umulhi((unsigned)(total * (split + 1)), inv);
-        // an entry: the block, with kNoPage where its table entry names no page
-        // (recorded; page 0 is copied in its place and none of its tokens counts)
-        auto entry = [&](int i, int j, int pg) {
-            const bool bad = pg < 0 || pg >= a.kv.n_pages;
-            if (bad)
-                set_status(a.status, kStatusPage);
-            s_block[i] = (uint16_t)(bad ? j | kNoPage : j);
-            s_rec[i] = ((uint32_t)(bad ? 0 : pg) * a.Hkv + kvh) * (F::REC / 512);
-        };
-        auto list = [&](int c, int pg) {            // this lane's block of word c
-            int base = __shfl_sync(0xffffffffu, inc - cnt, c >> lg);
-            for (int k = c >> lg << lg; k < c; ++k)
-                base += __popc(s_words[k]);
-            const unsigned w = s_words[c];
-            const int r = base + __popc(w & ((1u << lane) - 1u));
-            if ((w >> lane & 1u) && r >= r0 && r < r1) {
-                if (one_round)
-                    entry(r - r0, c * 32 + lane, pg);
-                else
-                    s_block[r - r0] = (uint16_t)(c * 32 + lane);
-            }
-        };
-        if (one_round) {
-#pragma unroll
-            for (int i = 0; i < kMaskWords; ++i)
-                if (warp + i * W < nwords)
-                    list(warp + i * W, page[i]);
-        } else {
-            for (int c = warp; c < nwords; c += W)
-                list(c, 0);
-            __syncthreads();
-            for (int i = threadIdx.x; i < r1 - r0; i += W * 32) {
-                const int j = s_block[i], at = b * a.kv.max_blocks + j;
-                entry(i, j, a.kv.table != nullptr ? __ldg(a.kv.table + at) : at);
-            }
-        }
+        m[0] = m[1] = -INFINITY;
+        l[0] = l[1] = 0.f;
     }
-    __syncthreads();
 
-    const int n_units = 2 * (r1 - r0);              // half records
-    uint8_t *my = ring + warp * ST * F::HALF;
-    const uint32_t my_bar = smem_u32(&s_bar[warp * ST]);
-    auto first_token = [&](int u) { return 64 * (s_block[u >> 1] & (kNoPage - 1)) + 32 * (u & 1); };
-    auto issue = [&](int u, int st) {               // lane 0
-        if (u >= n_units || first_token(u) >= len)
-            return;
-        mbar_arrive_expect_tx(my_bar + 8 * st, F::HALF);
-        bulk_copy(smem_u32(my + st * F::HALF), a.kv.pages + (unsigned long long)s_rec[u >> 1] * 512 + (u & 1) * F::HALF,
-                  F::HALF, my_bar + 8 * st);
-    };
-    auto head_byte = [&](int u) {
-        return u < n_units && lane < gt ? (int)__ldg(mrow + (long long)lane * a.nb + (s_block[u >> 1] & (kNoPage - 1))) : 0;
-    };
-    if (lane == 0)
-        for (int s = 0; s < ST; ++s)
-            issue(warp + s * W, s);
-
-    float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f}, zacc[NG][2], acc[KS][4];
-    int ve = 27;                                    // exponent field of V's largest scale so far
+    __device__ __forceinline__ void init(const Q &sq, float scale, int lane)
+    {
+        gid = lane >> 2;
+        tig = lane & 3;
+        // a score in units of log2: its raw sum times fac (kept off 0 and infinity, so
+        // that a masked score's -infinity stays one)
 #pragma unroll
-    for (int i = 0; i < KS; ++i)
-        acc[i][0] = acc[i][1] = acc[i][2] = acc[i][3] = 0.f;
+        for (int e = 0; e < 2; ++e)
+            fac[e] = fminf(fmaxf(sq.inv[2 * tig + e] * scale, 1.2e-38f), 3e38f);
+        clear();
+        ve = 27;
 #pragma unroll
-    for (int gr = 0; gr < NG; ++gr)
-        zacc[gr][0] = zacc[gr][1] = 0.f;
+        for (int i = 0; i < KS; ++i)
+            acc[i][0] = acc[i][1] = acc[i][2] = acc[i][3] = 0.f;
+#pragma unroll
+        for (int gr = 0; gr < NG; ++gr)
+            zacc[gr][0] = zacc[gr][1] = 0.f;
+        // this lane's places in a half record: K row and params of tile row gid (row
+        // gid + 8 and the second tile a whole number of rows further, with the same
+        // swizzle), V words of tile columns 2 tig and 2 tig + 1
+        tr = tile_token(gid);
+        const int t0 = tile_token(2 * tig), t1 = tile_token(2 * tig + 1);
+        at_k = tr * R + (BITS == 8 && D == 128 ? (tr & 1) * 64 + tig * 16 : tig * (R / 4));
+        at_p = tr * F::PAR;
+        at_z = F::kParK + at_p + Q::par_at(tig, 0);
+        at_v0 = F::kCodeV + t0 * R + (gid ^ F::v_swizzle(t0)) * (R / 8);
+        at_v1 = F::kCodeV + t1 * R + (gid ^ F::v_swizzle(t1)) * (R / 8);
+    }
 
-    // this lane's places in a half record: K row and params of tile row gid (row
-    // gid + 8 and the second tile a whole number of rows further, with the same
-    // swizzle), V words of tile columns 2 tig and 2 tig + 1
-    const int tr = tile_token(gid), t0 = tile_token(2 * tig), t1 = tile_token(2 * tig + 1);
-    const int at_k = tr * R + (BITS == 8 && D == 128 ? (tr & 1) * 64 + tig * 16 : tig * (R / 4));
-    const int at_p = tr * F::PAR, at_z = F::kParK + at_p + (tig < NG ? tig * 4 : 0);
-    const int at_v0 = F::kCodeV + t0 * R + (gid ^ F::v_swizzle(t0)) * (R / 8);
-    const int at_v1 = F::kCodeV + t1 * R + (gid ^ F::v_swizzle(t1)) * (R / 8);
-
-    int mb = head_byte(warp);
-    int it = 0;
-    for (int u = warp; u < n_units; u += W, ++it) {
-        const unsigned hbits = __ballot_sync(0xffffffffu, mb != 0 || lane >= gt);
-        mb = head_byte(u + W);
-        int keys = len - first_token(u);
-        if (keys <= 0)
-            break;                                  // the empty half of the last block: nothing follows
-        if (s_block[u >> 1] & kNoPage)
-            keys = 0;
-        const int st = it % ST;
-        {
-            const uint32_t bar = my_bar + 8 * st, parity = (it / ST) & 1;
-            bool done = mbar_test_wait(bar, parity);
-            if (!done) {
-                const uint64_t t0 = globaltimer();
-                while (!done && globaltimer() - t0 < a.timeout_ns)
-                    done = mbar_try_wait_sleep(bar, parity, 20000u);
-            }
-            if (!__all_sync(0xffffffffu, done)) {
-                // give up: wait for this warp's copies in flight, contribute nothing
-                set_status(a.status, kStatusTimeout);
-                for (int s = 0; s < ST; ++s) {
-                    const int w = it + s;
-                    const int uu = warp + w * W;
-                    if (uu < n_units && first_token(uu) < len)
-                        mbar_drain(my_bar + 8 * (w % ST), (w / ST) & 1, 200000000ull);
-                }
-                m[0] = m[1] = -INFINITY;
-                l[0] = l[1] = 0.f;
-                break;
-            }
-        }
-        const uint8_t *h = my + st * F::HALF;
+    // half record h, of which the first `keys` tokens count; hbits: the heads that chose its block
+    __device__ __forceinline__ void step(const uint8_t *h, const Q &sq, unsigned hbits, int keys)
+    {
         // q's operands of column gid (read for every half record: the registers are
-        // P V's afterwards) and the one against the params as they lie, (s, z) of
-        // group tig: 0 for s, q's sum for z
-        uint32_t qf[KS][2], qz[3];
-        {
-            const HeadQ<D> &q = s_q[gid];
+        // P V's afterwards)
+        uint32_t qf[KS][2], qz[2 * Q::STEPS];
 #pragma unroll
-            for (int i = 0; i < KS; i += 2) {
-                if (BITS == 4) {                    // a word's eight elements: two MMA steps
-                    const uint4 x = *reinterpret_cast<const uint4 *>(q.f16 + 16 * i + 8 * tig);
-                    qf[i][0] = x.x;
-                    qf[i][1] = x.y;
-                    qf[i + 1][0] = x.z;
-                    qf[i + 1][1] = x.w;
-                } else {
-#pragma unroll
-                    for (int k = 0; k < 2; ++k) {
-                        const uint2 x = *reinterpret_cast<const uint2 *>(q.f16 + 16 * (i + k) + 4 * tig);
-                        qf[i + k][0] = x.x;
-                        qf[i + k][1] = x.y;
-                    }
-                }
-            }
-#pragma unroll
-            for (int i = 0; i < 3; ++i)
-                qz[i] = tig < NG ? (uint32_t)q.sum[i][tig] << 16 : 0u;
+        for (int i = 0; i < KS; i += 2) {
+            const uint4 x = *reinterpret_cast<const uint4 *>(&sq.w[gid][8 * i + 4 * tig]);
+            qf[i][0] = x.x;
+            qf[i][1] = x.y;
+            qf[i + 1][0] = x.z;
+            qf[i + 1][1] = x.w;
         }
+        load_words(qz, reinterpret_cast<const uint8_t *>(&sq.w[gid][Q::kSum + 2 * Q::STEPS * tig]));
 
         // ---- raw scores of two 16-token tiles
         float s[2][4];
@@ -622,11 +447,13 @@ __global__ void __launch_bounds__(DecodeCfg<BITS, D>::W * 32, 2) decode_quant_ke
             load_words(pa, hp);
             load_words(pb, hp + 8 * F::PAR);
             {                                       // z sum(q) of the groups: the params themselves are the operand
-                                                    // (lanes past the last group: their q sums are 0)
-                const uint32_t wa = *reinterpret_cast<const uint32_t *>(h + at_z + 16 * mt * F::PAR);
-                const uint32_t wb = *reinterpret_cast<const uint32_t *>(h + at_z + (16 * mt + 8) * F::PAR);
-                mma16816_bf16_0(s[mt], wa, wb, wa, wb, qz[0], qz[1]);
-                mma16816_bf16(s[mt], wa, wb, 0u, 0u, qz[2], 0u);
+                uint32_t x[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    x[i] = *reinterpret_cast<const uint32_t *>(h + at_z + (16 * mt + 8 * (i & 1)) * F::PAR + Q::par_at(0, i >> 1));
+                mma16816_bf16_0(s[mt], x[0], x[1], x[2], x[3], qz[0], qz[1]);
+                if constexpr (Q::STEPS == 2)
+                    mma16816_bf16(s[mt], x[0], x[1], x[2], x[3], qz[2], qz[3]);
             }
 #pragma unroll
             for (int gr = 0; gr < NG; ++gr) {
@@ -710,7 +537,7 @@ __global__ void __launch_bounds__(DecodeCfg<BITS, D>::W * 32, 2) decode_quant_ke
         }
         const int ve_new = max(ve, (int)(vmax >> 7 & 0xFFu));
         // a head that left the block out: its maximum stays and its p are 0
-        const bool more0 = act0 && mx[0] > m[0], more1 = act1 && mx[1] > m[1];
+        const bool more0 = act0 && (mx[0] - m[0]) * fac[0] > kSlack, more1 = act1 && (mx[1] - m[1]) * fac[1] > kSlack;
         if (__any_sync(0xffffffffu, more0 || more1 || ve_new != ve)) {
             float alpha[2];
             const float m_new[2] = {more0 ? mx[0] : m[0], more1 ? mx[1] : m[1]};
@@ -735,7 +562,7 @@ __global__ void __launch_bounds__(DecodeCfg<BITS, D>::W * 32, 2) decode_quant_ke
             ve = ve_new;
         }
         const float mu[2] = {m[0] == -INFINITY ? 0.f : -m[0] * fac[0], m[1] == -INFINITY ? 0.f : -m[1] * fac[1]};
-        const float up = pow2_field(268 - ve);      // 2^14 over the power of two below the largest scale
+        const float up = pow2_field(268 - kSlack - ve);        // 2^(14 - kSlack) over the power of two below the largest scale
 
         // ---- P V
 #pragma unroll
@@ -793,29 +620,25 @@ __global__ void __launch_bounds__(DecodeCfg<BITS, D>::W * 32, 2) decode_quant_ke
                 }
             }
         }
-        __syncwarp();
-        if (lane == 0)
-            issue(u + ST * W, st);
     }
 
-    // ---- sums over the lanes that share a head, then over the warps
-#pragma unroll
-    for (int off = 4; off < 32; off <<= 1)
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-            l[e] += __shfl_xor_sync(0xffffffffu, l[e], off);
-#pragma unroll
-            for (int gr = 0; gr < NG; ++gr)
-                zacc[gr][e] += __shfl_xor_sync(0xffffffffu, zacc[gr][e], off);
-        }
-    __syncwarp();
-    if (gid == 0) {
-        s_ml[warp][2 * tig] = make_float2(m[0] == -INFINITY ? m[0] : m[0] * fac[0], l[0]);
-        s_ml[warp][2 * tig + 1] = make_float2(m[1] == -INFINITY ? m[1] : m[1] * fac[1], l[1]);
-    }
-    float *so = reinterpret_cast<float *>(my);      // [kHeads][D], over this warp's ring
+    // over the lanes that share a head: maxima and sums to ml[8], outputs to so[8][D]
+    __device__ __forceinline__ void finish(float *so, float2 *ml)
     {
-        const float un = pow2_field(ve - 14);       // with 2^24 the inverse of `up` and the codes' unit
+#pragma unroll
+        for (int off = 4; off < 32; off <<= 1)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                l[e] += __shfl_xor_sync(0xffffffffu, l[e], off);
+#pragma unroll
+                for (int gr = 0; gr < NG; ++gr)
+                    zacc[gr][e] += __shfl_xor_sync(0xffffffffu, zacc[gr][e], off);
+            }
+        if (gid == 0) {
+            ml[2 * tig] = make_float2(m[0] == -INFINITY ? m[0] : m[0] * fac[0], l[0]);
+            ml[2 * tig + 1] = make_float2(m[1] == -INFINITY ? m[1] : m[1] * fac[1], l[1]);
+        }
+        const float un = pow2_field(ve - 14 + kSlack);       // with 2^24 the inverse of `up` and the codes' unit
 #pragma unroll
         for (int e = 0; e < 2; ++e)
 #pragma unroll
@@ -833,6 +656,566 @@ __global__ void __launch_bounds__(DecodeCfg<BITS, D>::W * 32, 2) decode_quant_ke
                     *reinterpret_cast<float4 *>(so + (2 * tig + e) * D + F::G * gr + gid * (F::G / 8) + 2 * i) = r;
                 }
     }
+};
+
+// Nine to sixteen heads: on M, keys or output elements on N.  The codes are the
+// same operands (an A of sixteen rows is a B of rows 0 to 7 and one of the
+// others), unpacked once for twice the heads, and P leaves the scores as V's A
+// operand, so nothing is turned.
+template <int BITS, int D>
+struct Sums<BITS, D, 16> {
+    using F = KvFmt<BITS, D>;
+    using Q = QShared<BITS, D, 16>;
+    static constexpr int NG = F::NG, R = F::R;
+    static constexpr int KS = D / 16, KW = R / 16, VW = R / 32, UPG = KS / NG;
+
+    float m[2], l[2], zacc[NG][2], acc[KS][2][4], fac[2];
+    int ve;                                         // exponent field of V's largest scale so far
+    int lane, gid, tig, t0, t1, at_k, at_z, at_v0, at_v1;
+
+    __device__ __forceinline__ void clear()
+    {
+        m[0] = m[1] = -INFINITY;
+        l[0] = l[1] = 0.f;
+    }
+
+    __device__ __forceinline__ void init(const Q &sq, float scale, int lane_)
+    {
+        lane = lane_;
+        gid = lane >> 2;
+        tig = lane & 3;
+#pragma unroll
+        for (int hh = 0; hh < 2; ++hh)
+            fac[hh] = fminf(fmaxf(sq.inv[gid + 8 * hh] * scale, 1.2e-38f), 3e38f);
+        clear();
+        ve = 27;
+#pragma unroll
+        for (int i = 0; i < KS; ++i)
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                acc[i][0][e] = acc[i][1][e] = 0.f;
+#pragma unroll
+        for (int gr = 0; gr < NG; ++gr)
+            zacc[gr][0] = zacc[gr][1] = 0.f;
+        const int tr = tile_token(gid);
+        t0 = tile_token(2 * tig);
+        t1 = tile_token(2 * tig + 1);
+        at_k = tr * R + (BITS == 8 && D == 128 ? (tr & 1) * 64 + tig * 16 : tig * (R / 4));
+        at_z = F::kParK + tr * F::PAR + Q::par_at(tig, 0);
+        at_v0 = F::kCodeV + t0 * R + (gid ^ F::v_swizzle(t0)) * (R / 8);
+        at_v1 = F::kCodeV + t1 * R + (gid ^ F::v_swizzle(t1)) * (R / 8);
+    }
+
+    __device__ __forceinline__ void step(const uint8_t *h, const Q &sq, unsigned hbits, int keys)
+    {
+        const uint32_t *q = sq.w[gid] + 4 * tig;
+        // ---- raw scores of two 16-token tiles, eight keys each time
+        float s[2][2][4];
+#pragma unroll
+        for (int mt = 0; mt < 2; ++mt) {
+            const uint8_t *ha = h + at_k + 16 * mt * R;
+            uint32_t ka[KW], kb[KW];
+            if constexpr (BITS == 8 && D == 128) {  // the other half of the row is 64 bytes up or down
+                uint32_t (&a0)[4] = *reinterpret_cast<uint32_t (*)[4]>(ka);
+                uint32_t (&a1)[4] = *reinterpret_cast<uint32_t (*)[4]>(ka + 4);
+                uint32_t (&b0)[4] = *reinterpret_cast<uint32_t (*)[4]>(kb);
+                uint32_t (&b1)[4] = *reinterpret_cast<uint32_t (*)[4]>(kb + 4);
+                const uint8_t *hb = ha + (gid >> 1 & 1 ^ gid & 1 ? -64 : 64);
+                load_words(a0, ha);
+                load_words(a1, hb);
+                load_words(b0, ha + 8 * R);
+                load_words(b1, hb + 8 * R);
+            } else {
+                load_words(ka, ha);
+                load_words(kb, ha + 8 * R);
+            }
+#pragma unroll
+            for (int st = 0; st < Q::STEPS; ++st) { // z sum(q) of the groups, the params as they lie
+                const uint4 x = *reinterpret_cast<const uint4 *>(sq.w[gid] + Q::kSum + (tig * Q::STEPS + st) * 4);
+#pragma unroll
+                for (int nt = 0; nt < 2; ++nt) {
+                    uint32_t w[2];
+                    const uint8_t *at = h + at_z + (16 * mt + 8 * nt) * F::PAR;
+                    if constexpr (NG == 1)
+                        w[0] = w[1] = *reinterpret_cast<const uint32_t *>(at);
+                    else
+                        load_words(w, at);
+                    if (st == 0)
+                        mma16816_bf16_0(s[mt][nt], x.x, x.y, x.z, x.w, w[0], w[1]);
+                    else
+                        mma16816_bf16(s[mt][nt], x.x, x.y, x.z, x.w, w[0], w[1]);
+                }
+            }
+            uint32_t par[4][NG];                    // of this lane's keys 2 tig, 2 tig + 1 and 8 further
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                load_words(par[i], h + F::kParK + (16 * mt + (i & 1 ? t1 : t0) + (i >> 1) * 8) * F::PAR);
+#pragma unroll
+            for (int gr = 0; gr < NG; ++gr) {
+                float c[2][4];
+#pragma unroll
+                for (int i = 0; i < UPG; ++i) {
+                    const int ks = gr * UPG + i;
+                    uint32_t x[4];
+                    const uint4 qk = *reinterpret_cast<const uint4 *>(q + 16 * ks);
+                    if (BITS == 4) {
+                        const uint32_t wa = ka[ks / 2] >> (8 * (ks % 2)), wb = kb[ks / 2] >> (8 * (ks % 2));
+                        x[0] = wa & 0x000F000Fu;
+                        x[1] = wb & 0x000F000Fu;
+                        x[2] = wa & 0x00F000F0u;
+                        x[3] = wb & 0x00F000F0u;
+                    } else {
+                        x[0] = __byte_perm(ka[ks], 0u, 0x4140);
+                        x[1] = __byte_perm(kb[ks], 0u, 0x4140);
+                        x[2] = __byte_perm(ka[ks], 0u, 0x4342);
+                        x[3] = __byte_perm(kb[ks], 0u, 0x4342);
+                    }
+                    if (i == 0) {
+                        mma16816_0(c[0], qk.x, qk.y, qk.z, qk.w, x[0], x[2]);
+                        mma16816_0(c[1], qk.x, qk.y, qk.z, qk.w, x[1], x[3]);
+                    } else {
+                        mma16816(c[0], qk.x, qk.y, qk.z, qk.w, x[0], x[2]);
+                        mma16816(c[1], qk.x, qk.y, qk.z, qk.w, x[1], x[3]);
+                    }
+                }
+#pragma unroll
+                for (int nt = 0; nt < 2; ++nt) {
+                    const float sa = kv_scale(par[2 * nt][gr]), sb = kv_scale(par[2 * nt + 1][gr]);
+                    s[mt][nt][0] = fmaf(sa, c[nt][0], s[mt][nt][0]);
+                    s[mt][nt][1] = fmaf(sb, c[nt][1], s[mt][nt][1]);
+                    s[mt][nt][2] = fmaf(sa, c[nt][2], s[mt][nt][2]);
+                    s[mt][nt][3] = fmaf(sb, c[nt][3], s[mt][nt][3]);
+                }
+            }
+        }
+        const bool all_heads = hbits == 0xffffffffu;
+        const bool act0 = hbits >> gid & 1u, act1 = hbits >> (gid + 8) & 1u;
+        if (keys < 32) {                            // the sequence's last tokens
+            __syncwarp();                           // (keeps this a branch)
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    if (8 * i + (e & 1 ? t1 : t0) >= keys)
+                        s[i / 2][i % 2][e] = -INFINITY;
+        }
+
+        // ---- the power of two for p s (a token a lane), the maxima
+        uint32_t vmax = 0;
+        {
+            uint32_t w[NG];
+            load_words(w, h + F::kParV + lane * F::PAR);
+#pragma unroll
+            for (int gr = 0; gr < NG; ++gr)
+                vmax = __vmaxu2(vmax, w[gr]);
+            vmax = __reduce_max_sync(0xffffffffu, lane < keys ? vmax & 0xFFFFu : 0u);
+        }
+        float mx[2];
+#pragma unroll
+        for (int hh = 0; hh < 2; ++hh) {
+            mx[hh] = fmaxf(s[0][0][2 * hh], s[0][0][2 * hh + 1]);
+#pragma unroll
+            for (int i = 1; i < 4; ++i)
+                mx[hh] = fmaxf(mx[hh], fmaxf(s[i / 2][i % 2][2 * hh], s[i / 2][i % 2][2 * hh + 1]));
+        }
+#pragma unroll
+        for (int off = 1; off < 4; off <<= 1) {
+            mx[0] = fmaxf(mx[0], __shfl_xor_sync(0xffffffffu, mx[0], off));
+            mx[1] = fmaxf(mx[1], __shfl_xor_sync(0xffffffffu, mx[1], off));
+        }
+        const int ve_new = max(ve, (int)(vmax >> 7));
+        // a head that left the block out: its maximum stays and its p are 0
+        const bool more0 = act0 && (mx[0] - m[0]) * fac[0] > kSlack, more1 = act1 && (mx[1] - m[1]) * fac[1] > kSlack;
+        if (__any_sync(0xffffffffu, more0 || more1 || ve_new != ve)) {
+            float alpha[2];
+            const float m_new[2] = {more0 ? mx[0] : m[0], more1 ? mx[1] : m[1]};
+#pragma unroll
+            for (int hh = 0; hh < 2; ++hh) {
+                alpha[hh] = m_new[hh] == m[hh] ? 1.f : exp2_approx((m[hh] - m_new[hh]) * fac[hh]);
+                m[hh] = m_new[hh];
+            }
+            const float down = ve - ve_new > -127 ? pow2_field(127 + ve - ve_new) : 0.f;
+#pragma unroll
+            for (int i = 0; i < KS; ++i)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    acc[i][0][e] *= alpha[e >> 1] * down;
+                    acc[i][1][e] *= alpha[e >> 1] * down;
+                }
+#pragma unroll
+            for (int gr = 0; gr < NG; ++gr) {
+                zacc[gr][0] *= alpha[0];
+                zacc[gr][1] *= alpha[1];
+            }
+            l[0] *= alpha[0];
+            l[1] *= alpha[1];
+            ve = ve_new;
+        }
+        const float mu[2] = {m[0] == -INFINITY ? 0.f : -m[0] * fac[0], m[1] == -INFINITY ? 0.f : -m[1] * fac[1]};
+        const float up = pow2_field(268 - kSlack - ve);        // 2^(14 - kSlack) over the power of two below the largest scale
+
+        // ---- P V
+#pragma unroll
+        for (int mt = 0; mt < 2; ++mt) {
+            float p[2][4], pu[2][4];
+#pragma unroll
+            for (int nt = 0; nt < 2; ++nt) {
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    p[nt][e] = exp2_approx(fmaf(s[mt][nt][e], fac[e >> 1], mu[e >> 1]));
+                if (!all_heads) {
+                    p[nt][0] = act0 ? p[nt][0] : 0.f;
+                    p[nt][1] = act0 ? p[nt][1] : 0.f;
+                    p[nt][2] = act1 ? p[nt][2] : 0.f;
+                    p[nt][3] = act1 ? p[nt][3] : 0.f;
+                }
+                l[0] += p[nt][0] + p[nt][1];
+                l[1] += p[nt][2] + p[nt][3];
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    pu[nt][e] = p[nt][e] * up;
+            }
+            uint32_t par[4][NG], v0[VW], v1[VW], v2[VW], v3[VW];
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                load_words(par[i], h + F::kParV + (16 * mt + (i & 1 ? t1 : t0) + (i >> 1) * 8) * F::PAR);
+            if (keys < 32) {                        // zero behind the length
+                __syncwarp();
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+#pragma unroll
+                    for (int gr = 0; gr < NG; ++gr)
+                        if (16 * mt + (i & 1 ? t1 : t0) + (i >> 1) * 8 >= keys)
+                            par[i][gr] = 0u;
+            }
+            load_words(v0, h + at_v0 + 16 * mt * R);
+            load_words(v1, h + at_v1 + 16 * mt * R);
+            load_words(v2, h + at_v0 + (16 * mt + 8) * R);
+            load_words(v3, h + at_v1 + (16 * mt + 8) * R);
+#pragma unroll
+            for (int gr = 0; gr < NG; ++gr) {
+                uint32_t a[4];
+#pragma unroll
+                for (int nt = 0; nt < 2; ++nt) {
+                    const float sa = kv_scale(par[2 * nt][gr]), sb = kv_scale(par[2 * nt + 1][gr]);
+                    const float za = kv_zero(par[2 * nt][gr]), zb = kv_zero(par[2 * nt + 1][gr]);
+                    a[2 * nt] = pack_half2(pu[nt][0] * sa, pu[nt][1] * sb);
+                    a[2 * nt + 1] = pack_half2(pu[nt][2] * sa, pu[nt][3] * sb);
+                    if (act0)                       // a NaN of V stays out of heads that left the block out
+                        zacc[gr][0] = fmaf(p[nt][0], za, fmaf(p[nt][1], zb, zacc[gr][0]));
+                    if (act1)
+                        zacc[gr][1] = fmaf(p[nt][2], za, fmaf(p[nt][3], zb, zacc[gr][1]));
+                }
+                if constexpr (BITS == 4) {
+                    const unsigned sel = gr & 1 ? 0x7632u : 0x5410u;
+                    // an element; and the byte, that element plus 16 times the next
+                    const uint32_t x01 = __byte_perm(v0[gr / 2], v1[gr / 2], sel), x23 = __byte_perm(v2[gr / 2], v3[gr / 2], sel);
+#pragma unroll
+                    for (int i = 0; i < UPG; ++i) {
+                        const uint32_t y01 = i ? __byte_perm(x01, 0u, 0x4341) : x01 & 0x00FF00FFu;
+                        const uint32_t y23 = i ? __byte_perm(x23, 0u, 0x4341) : x23 & 0x00FF00FFu;
+                        mma16816(acc[gr * UPG + i][0], a[0], a[1], a[2], a[3], y01 & 0x000F000Fu, y23 & 0x000F000Fu);
+                        mma16816(acc[gr * UPG + i][1], a[0], a[1], a[2], a[3], y01, y23);
+                    }
+                } else {
+#pragma unroll
+                    for (int i = 0; i < UPG; ++i) {
+                        const int w = 2 * gr + i / 2;
+                        const unsigned sel = i & 1 ? 0x7632u : 0x5410u;
+                        const uint32_t x01 = __byte_perm(v0[w], v1[w], sel), x23 = __byte_perm(v2[w], v3[w], sel);
+                        mma16816(acc[gr * UPG + i][0], a[0], a[1], a[2], a[3], __byte_perm(x01, 0u, 0x4240),
+                                 __byte_perm(x23, 0u, 0x4240));
+                        mma16816(acc[gr * UPG + i][1], a[0], a[1], a[2], a[3], __byte_perm(x01, 0u, 0x4341),
+                                 __byte_perm(x23, 0u, 0x4341));
+                    }
+                }
+            }
+        }
+    }
+
+    // over the lanes that share a head: maxima and sums to ml[16], outputs to so[16][D]
+    __device__ __forceinline__ void finish(float *so, float2 *ml)
+    {
+#pragma unroll
+        for (int off = 1; off < 4; off <<= 1)
+#pragma unroll
+            for (int hh = 0; hh < 2; ++hh) {
+                l[hh] += __shfl_xor_sync(0xffffffffu, l[hh], off);
+#pragma unroll
+                for (int gr = 0; gr < NG; ++gr)
+                    zacc[gr][hh] += __shfl_xor_sync(0xffffffffu, zacc[gr][hh], off);
+            }
+        if (tig == 0) {
+            ml[gid] = make_float2(m[0] == -INFINITY ? m[0] : m[0] * fac[0], l[0]);
+            ml[gid + 8] = make_float2(m[1] == -INFINITY ? m[1] : m[1] * fac[1], l[1]);
+        }
+        const float un = pow2_field(ve - 14 + kSlack);       // with 2^24 the inverse of `up` and the codes' unit
+#pragma unroll
+        for (int hh = 0; hh < 2; ++hh)
+#pragma unroll
+            for (int e = 0; e < 2; ++e)
+#pragma unroll
+                for (int gr = 0; gr < NG; ++gr)
+#pragma unroll
+                    for (int i = 0; i < UPG; i += 2) {
+                        float v[4];
+#pragma unroll
+                        for (int k = 0; k < 2; ++k) {
+                            const float lo = acc[gr * UPG + i + k][0][2 * hh + e], hi = acc[gr * UPG + i + k][1][2 * hh + e];
+                            v[2 * k] = lo * un * 16777216.f + zacc[gr][hh];
+                            v[2 * k + 1] = (BITS == 4 ? (hi - lo) * un * 1048576.f : hi * un * 16777216.f) + zacc[gr][hh];
+                        }
+                        *reinterpret_cast<float4 *>(so + (gid + 8 * hh) * D + F::G * gr + (2 * tig + e) * (F::G / 8) + 2 * i) =
+                            make_float4(v[0], v[1], v[2], v[3]);
+                    }
+    }
+};
+
+template <int BITS, int D, int H>
+__global__ void __launch_bounds__(DecodeCfg<BITS, D, H>::W * 32, 2) decode_quant_kernel(const DecodeArgs a)
+{
+    using F = KvFmt<BITS, D>;
+    using C = DecodeCfg<BITS, D, H>;
+    constexpr int W = C::W, ST = C::ST;
+    extern __shared__ __align__(128) uint8_t ring[];
+    __shared__ __align__(8) uint64_t s_bar[W * ST];
+    __shared__ float2 s_ml[W][H], s_sum[H];
+    __shared__ uint32_t s_words[kMaxNb / 32];
+    __shared__ uint32_t s_rec[kListMax];            // a block's record from the start of the pages, in 512 bytes
+    __shared__ uint16_t s_block[kListMax];
+    __shared__ __align__(16) QShared<BITS, D, H> s_q;
+
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    int b, split, ns;
+    if (!slot_of(a, lane, b, split, ns))
+        return;
+    const int tile = blockIdx.y % a.tiles, kvh = blockIdx.y / a.tiles;
+    const int g = a.Hq / a.Hkv;
+    const int h0 = kvh * g + tile * a.per_tile;     // first query head, and how many
+    const int gt = min(a.per_tile, g - tile * a.per_tile);
+    const int len = a.lens != nullptr ? max(0, min(a.lens[b], a.L)) : a.L;
+    const uint8_t *mrow = a.mask + ((long long)b * a.Hq + h0) * a.nb;
+
+    if (lane == 0) {
+        for (int s = 0; s < ST; ++s)
+            mbar_init(smem_u32(&s_bar[warp * ST + s]), 1);
+        fence_mbar_init();
+    }
+
+    // ---- q, a warp per head (0 where there is none), its loads in flight together
+    {
+        typename QShared<BITS, D, H>::Raw raw[(H + W - 1) / W];
+#pragma unroll
+        for (int i = 0; i < (H + W - 1) / W; ++i) {
+            const int h = warp + i * W;
+            QShared<BITS, D, H>::fetch(raw[i], h < gt ? a.q_tok + ((long long)b * a.Hq + h0 + h) * D : nullptr, lane);
+        }
+#pragma unroll
+        for (int i = 0; i < (H + W - 1) / W; ++i)
+            if (warp + i * W < H)
+                s_q.prepare(raw[i], warp + i * W, lane);
+    }
+
+    // ---- union of the heads' active blocks, one bit each.  Rows short enough for
+    // one round of kMaskWords words of 32 blocks a warp: a block a lane, and its
+    // table entry, all loads in flight together (and before the length is known).
+    // Longer rows: four blocks a lane, where the rows' alignment allows it, and
+    // the table is looked up for this split's blocks alone.
+    constexpr int kMaskWords = H == 8 && W < 8 ? 6 : 4;
+    const int nblk = (len + 63) / 64, nwords = (nblk + 31) / 32;
+    const bool one_round = a.nb <= 32 * kMaskWords * W;
+    int page[kMaskWords];
+    if (one_round || a.nb % 4 != 0 || (reinterpret_cast<uintptr_t>(a.mask) & 3) != 0) {
+        for (int c0 = warp; c0 < (c0 == warp ? (a.nb + 31) / 32 : nwords); c0 += kMaskWords * W) {
+            int raw[kMaskWords][H];
+            // (blocks past the row read its last one: the branches are the warp's)
+#pragma unroll
+            for (int i = 0; i < kMaskWords; ++i) {
+                if (i > 0 && (c0 + i * W) * 32 >= a.nb)
+                    continue;
+                const int j = min((c0 + i * W) * 32 + lane, a.nb - 1);
+#pragma unroll
+                for (int h = 0; h < H; ++h) {
+                    raw[i][h] = 0;
+                    if (h < gt)
+                        raw[i][h] = __ldg(mrow + (long long)h * a.nb + j);
+                }
+                if (one_round) {
+                    page[i] = b * a.kv.max_blocks + j;
+                    if (a.kv.table != nullptr)
+                        page[i] = __ldg(a.kv.table + page[i]);
+                }
+            }
+#pragma unroll
+            for (int i = 0; i < kMaskWords; ++i) {
+                const int c = c0 + i * W;
+                if (c >= nwords)
+                    continue;
+                int any = 0;
+#pragma unroll
+                for (int h = 0; h < H; ++h)
+                    any |= raw[i][h];
+                const unsigned bits = __ballot_sync(0xffffffffu, any != 0 && c * 32 + lane < nblk);
+                if (lane == 0)
+                    s_words[c] = bits;
+            }
+        }
+    } else {
+        for (int c0 = warp; c0 * 4 < nwords; c0 += 4 * W) {
+            uint32_t raw[4][H];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int j = min((c0 + i * W) * 128 + 4 * lane, a.nb - 4);
+#pragma unroll
+                for (int h = 0; h < H; ++h) {
+                    raw[i][h] = 0;
+                    if (h < gt)
+                        raw[i][h] = __ldg(reinterpret_cast<const uint32_t *>(mrow + (long long)h * a.nb + j));
+                }
+            }
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int j = (c0 + i * W) * 128 + 4 * lane;
+                uint32_t x = 0;
+#pragma unroll
+                for (int h = 0; h < H; ++h)
+                    x |= raw[i][h];
+                // bytes that are not 0 -> four bits -> words of eight lanes
+                x = (((x & 0x7F7F7F7Fu) + 0x7F7F7F7Fu) | x) >> 7 & 0x01010101u;
+                x = x * 0x10204080u >> 28 & ((1u << max(0, min(4, nblk - j))) - 1u);
+                x <<= 4 * (lane & 7);
+                x |= __shfl_xor_sync(0xffffffffu, x, 1);
+                x |= __shfl_xor_sync(0xffffffffu, x, 2);
+                x |= __shfl_xor_sync(0xffffffffu, x, 4);
+                if ((lane & 7) == 0 && j / 32 < nwords)
+                    s_words[j / 32] = x;
+            }
+        }
+    }
+    __syncthreads();
+    // ---- this split's blocks: ranks [r0, r1) of the union
+    int r0, r1;
+    {
+        // words of a lane: a power of two (32 lanes cover the words)
+        const int lg = nwords > 32 ? 32 - __clz((nwords - 1) >> 5) : 0, per = 1 << lg;
+        int cnt = 0;
+        for (int k = 0; k < per; ++k)
+            if (lane * per + k < nwords)
+                cnt += __popc(s_words[lane * per + k]);
+        int inc = cnt;
+#pragma unroll
+        for (int off = 1; off < 32; off <<= 1) {
+            const int v = __shfl_up_sync(0xffffffffu, inc, off);
+            inc += lane >= off ? v : 0;
+        }
+        const int total = __shfl_sync(0xffffffffu, inc, 31);
+        // total * split / ns: at most 2^20, and inv is 2^32 / ns rounded up by less
+        // than 2^-26 of it, so the product's high word is the quotient (one split:
+        // inv is 0 and so is r0)
+        const unsigned inv = 0xFFFFFFFFu / (unsigned)ns + 1u;
+        r0 = (int)__umulhi((unsigned)(total * split), inv);
+        r1 = split + 1 == ns ? total : (int)__umulhi((unsigned)(total * (split + 1)), inv);
+        // an entry: the block, with kNoPage where its table entry names no page
+        // (recorded; page 0 is copied in its place and none of its tokens counts)
+        auto entry = [&](int i, int j, int pg) {
+            const bool bad = pg < 0 || pg >= a.kv.n_pages;
+            if (bad)
+                set_status(a.status, kStatusPage);
+            s_block[i] = (uint16_t)(bad ? j | kNoPage : j);
+            s_rec[i] = ((uint32_t)(bad ? 0 : pg) * a.Hkv + kvh) * (F::REC / 512);
+        };
+        auto list = [&](int c, int pg) {            // this lane's block of word c
+            int base = __shfl_sync(0xffffffffu, inc - cnt, c >> lg);
+            for (int k = c >> lg << lg; k < c; ++k)
+                base += __popc(s_words[k]);
+            const unsigned w = s_words[c];
+            const int r = base + __popc(w & ((1u << lane) - 1u));
+            if ((w >> lane & 1u) && r >= r0 && r < r1) {
+                if (one_round)
+                    entry(r - r0, c * 32 + lane, pg);
+                else
+                    s_block[r - r0] = (uint16_t)(c * 32 + lane);
+            }
+        };
+        if (one_round) {
+#pragma unroll
+            for (int i = 0; i < kMaskWords; ++i)
+                if (warp + i * W < nwords)
+                    list(warp + i * W, page[i]);
+        } else {
+            for (int c = warp; c < nwords; c += W)
+                list(c, 0);
+            __syncthreads();
+            for (int i = threadIdx.x; i < r1 - r0; i += W * 32) {
+                const int j = s_block[i], at = b * a.kv.max_blocks + j;
+                entry(i, j, a.kv.table != nullptr ? __ldg(a.kv.table + at) : at);
+            }
+        }
+    }
+    __syncthreads();
+
+    const int n_units = 2 * (r1 - r0);              // half records
+    uint8_t *my = ring + warp * ST * F::HALF;
+    const uint32_t my_bar = smem_u32(&s_bar[warp * ST]);
+    auto first_token = [&](int u) { return 64 * (s_block[u >> 1] & (kNoPage - 1)) + 32 * (u & 1); };
+    auto issue = [&](int u, int st) {               // lane 0
+        if (u >= n_units || first_token(u) >= len)
+            return;
+        mbar_arrive_expect_tx(my_bar + 8 * st, F::HALF);
+        bulk_copy(smem_u32(my + st * F::HALF), a.kv.pages + (unsigned long long)s_rec[u >> 1] * 512 + (u & 1) * F::HALF,
+                  F::HALF, my_bar + 8 * st);
+    };
+    auto head_byte = [&](int u) {
+        return u < n_units && lane < gt ? (int)__ldg(mrow + (long long)lane * a.nb + (s_block[u >> 1] & (kNoPage - 1))) : 0;
+    };
+    if (lane == 0)
+        for (int s = 0; s < ST; ++s)
+            issue(warp + s * W, s);
+
+    Sums<BITS, D, H> sums;
+    sums.init(s_q, a.scale_log2 * 16777216.f, lane);
+
+    int mb = head_byte(warp);
+    int it = 0;
+    for (int u = warp; u < n_units; u += W, ++it) {
+        const unsigned hbits = __ballot_sync(0xffffffffu, mb != 0 || lane >= gt);
+        mb = head_byte(u + W);
+        int keys = len - first_token(u);
+        if (keys <= 0)
+            break;                                  // the empty half of the last block: nothing follows
+        if (s_block[u >> 1] & kNoPage)
+            keys = 0;
+        const int st = it % ST;
+        {
+            const uint32_t bar = my_bar + 8 * st, parity = (it / ST) & 1;
+            bool done = mbar_test_wait(bar, parity);
+            if (!done) {
+                const uint64_t t0 = globaltimer();
+                while (!done && globaltimer() - t0 < a.timeout_ns)
+                    done = mbar_try_wait_sleep(bar, parity, 20000u);
+            }
+            if (!__all_sync(0xffffffffu, done)) {
+                // give up: wait for this warp's copies in flight, contribute nothing
+                set_status(a.status, kStatusTimeout);
+                for (int s = 0; s < ST; ++s) {
+                    const int w = it + s;
+                    const int uu = warp + w * W;
+                    if (uu < n_units && first_token(uu) < len)
+                        mbar_drain(my_bar + 8 * (w % ST), (w / ST) & 1, 200000000ull);
+                }
+                sums.clear();
+                break;
+            }
+        }
+        sums.step(my + st * F::HALF, s_q, hbits, keys);
+        __syncwarp();
+        if (lane == 0)
+            issue(u + ST * W, st);
+    }
+
+    // ---- sums over the lanes that share a head, then over the warps
+    __syncwarp();
+    sums.finish(reinterpret_cast<float *>(my), s_ml[warp]);              // over this warp's ring
     __syncthreads();
     for (int hh = warp; hh < gt; hh += W) {         // the warps' weights for a head
         const float2 ml = lane < W ? s_ml[lane][hh] : make_float2(-INFINITY, 0.f);
@@ -947,21 +1330,27 @@ __global__ void __launch_bounds__(Q * D) decode_quant_merge_kernel(const DecodeA
         a.lse[bh] = log_sum(M, l);
 }
 
-// Estimated time, in us, of `ctas` CTAs with `blocks` blocks each:
-//   a CTA's start and end     6 alone on its SM, 7.5 for two at once, per wave
-//   a block                   0.4 for a CTA alone, 0.31 of the SM for two
+// Estimated time, in us, of `ctas` CTAs of H heads with `blocks` blocks each:
+//                            eight heads  sixteen
+//   a CTA's start and end          6         8     alone on its SM
+//                                  7.5       9.5   for two at once, per wave
+//   a block                        0.4       0.65  for a CTA alone
+//                                  0.31      0.46  of the SM for two
 //   the second kernel         2 and 0.04 a split
 // Measured (4 bits, D = 128): 8 units (a sequence's head tile) of 512 blocks, all
 // active: 18 splits 20.7 us, 24: 23.8, 37: 19.8; a tenth active: 9: 15.2, 18: 11.8,
-// 37: 12.4; 128 units of 256: 1 split 97 us, 2: 86, 4: 91.
-double decode_quant_us(long long ctas, double blocks, double splits, int sms)
+// 37: 12.4; 128 units of 256: 1 split 97 us, 2: 86, 4: 91.  Sixteen heads, 64 units
+// of 256 blocks: 1 split 172 us, 2: 93, 4: 70; of 64 blocks: 50, 32, 27.
+double decode_quant_us(int H, long long ctas, double blocks, double splits, int sms)
 {
+    const bool two = H == 16;
     const long long load = (ctas + sms - 1) / sms, waves = (load + 1) / 2;
-    return (load == 1 ? 6.0 + 0.4 * blocks : 7.5 * (double)waves + 0.31 * (double)load * blocks) +
+    return (load == 1 ? (two ? 8.0 : 6.0) + (two ? 0.65 : 0.4) * blocks
+                      : (two ? 9.5 : 7.5) * (double)waves + (two ? 0.46 : 0.31) * (double)load * blocks) +
            (splits > 1.0 ? 2.0 + 0.04 * splits : 0.0);
 }
 
-// How a call is split (nsplit, slots): the least estimated time with half of the
+// How a call is split for H heads a CTA (nsplit, slots), and its time: the least estimated time with half of the
 // blocks active (the mask is on the device) and at least a block for every
 // second warp.  Lengths given: one or two CTAs per SM in all, where there are
 // enough for every sequence's tiles, shared out by length: a batch of 8 from 32k
@@ -969,8 +1358,11 @@ double decode_quant_us(long long ctas, double blocks, double splits, int sms)
 // sequences, whose CTAs pair up on the SMs (64k and 37k tokens at 8 bits: 42 us with
 // 18 splits each, 45 shared out), and in whole splits where a sequence has few
 // (16 of 16k tokens: 88 us with two each, 90 with 37 slots).
-void decode_quant_split(DecodeArgs &a, int sms)
+double decode_quant_split(DecodeArgs &a, int H, int sms)
 {
+    const int g = a.Hq / a.Hkv;
+    a.tiles = (g + H - 1) / H;
+    a.per_tile = (g + a.tiles - 1) / a.tiles;
     const int tiles = a.Hkv * a.tiles;
     const int lo = (a.nb + kListMax - 2) / (kListMax - 1);            // a split's block list has to fit
     const int cap = a.nb / 4 < kMaxDecodeSplits ? a.nb / 4 : kMaxDecodeSplits;
@@ -978,15 +1370,15 @@ void decode_quant_split(DecodeArgs &a, int sms)
     a.nsplit = lo;
     a.slots = 0;
     for (int ns = lo; ns <= cap; ++ns) {
-        const double us = decode_quant_us((long long)a.B * tiles * ns, 0.5 * a.nb / ns, ns, sms);
+        const double us = decode_quant_us(H, (long long)a.B * tiles * ns, 0.5 * a.nb / ns, ns, sms);
         if (us < best_us) {
             best_us = us;
             a.nsplit = ns;
         }
     }
     if (a.lens == nullptr || a.B < 4 || a.B > kBalanced)
-        return;
-    best_us = 1e30;
+        return best_us;
+    double shared_us = 1e30;
     for (int load = 1; load <= 2; ++load) {
         int slots = load * sms / tiles;
         if (slots < 4 * a.B)
@@ -995,32 +1387,25 @@ void decode_quant_split(DecodeArgs &a, int sms)
         if (slots < a.B * (1 + lo) || slots > a.B * (1 + cap))
             continue;
         const double each = (double)slots / a.B;
-        const double us = decode_quant_us((long long)slots * tiles, 0.5 * a.nb / each, each, sms);
-        if (us < best_us) {
-            best_us = us;
+        const double us = decode_quant_us(H, (long long)slots * tiles, 0.5 * a.nb / each, each, sms);
+        if (us < shared_us) {
+            shared_us = us;
             a.slots = slots;
         }
     }
+    return a.slots > 0 ? shared_us : best_us;
 }
 
-template <int BITS, int D>
-cudaError_t launch(DecodeArgs a, cudaStream_t stream)
+template <int BITS, int D, int H>
+cudaError_t launch(const DecodeArgs &a, cudaStream_t stream)
 {
-    using C = DecodeCfg<BITS, D>;
-    const int g = a.Hq / a.Hkv;
-    a.tiles = (g + kHeads - 1) / kHeads;
-    a.per_tile = (g + a.tiles - 1) / a.tiles;
-    int dev = 0, sms = 0;
-    cudaError_t e = cudaGetDevice(&dev);
-    if (e == cudaSuccess)
-        e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
-    if (e == cudaSuccess)
-        e = cudaFuncSetAttribute(decode_quant_kernel<BITS, D>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::ring);
+    using C = DecodeCfg<BITS, D, H>;
+    cudaError_t e = cudaFuncSetAttribute(decode_quant_kernel<BITS, D, H>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                         C::ring);
     if (e != cudaSuccess)
         return e;
-    decode_quant_split(a, sms);
     const dim3 grid(a.slots > 0 ? a.slots : a.nsplit, a.Hkv * a.tiles, a.slots > 0 ? 1 : a.B);
-    decode_quant_kernel<BITS, D><<<grid, C::W * 32, C::ring, stream>>>(a);
+    decode_quant_kernel<BITS, D, H><<<grid, C::W * 32, C::ring, stream>>>(a);
     e = cudaGetLastError();
     if (e != cudaSuccess || (a.slots == 0 && a.nsplit == 1))
         return e;
@@ -1053,9 +1438,22 @@ cudaError_t launch_decode_quant(int bits, int B, int Hq, int Hkv, int L, int d, 
     a.lse = lse;
     a.status = status;
     a.timeout_ns = timeout_ns;
-    if (bits == 4)
-        return d == 128 ? launch<4, 128>(a, stream) : launch<4, 64>(a, stream);
-    return d == 128 ? launch<8, 128>(a, stream) : launch<8, 64>(a, stream);
+    int dev = 0, sms = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e == cudaSuccess)
+        e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+    if (e != cudaSuccess)
+        return e;
+    // More than eight heads of a KV head: tiles of sixteen where they are estimated
+    // faster, as they are for enough blocks (groups of 16, 64 units of 256 blocks, all
+    // active: 71 us, 88 by eights; 8 of 512, a tenth active: 24 and 21).
+    const double us = decode_quant_split(a, 8, sms);
+    DecodeArgs wide = a;
+    if (Hq / Hkv > 8 && decode_quant_split(wide, 16, sms) < us)
+        return bits == 4 ? (d == 128 ? launch<4, 128, 16>(wide, stream) : launch<4, 64, 16>(wide, stream))
+                         : (d == 128 ? launch<8, 128, 16>(wide, stream) : launch<8, 64, 16>(wide, stream));
+    return bits == 4 ? (d == 128 ? launch<4, 128, 8>(a, stream) : launch<4, 64, 8>(a, stream))
+                     : (d == 128 ? launch<8, 128, 8>(a, stream) : launch<8, 64, 8>(a, stream));
 }
 
 } // namespace seer

@@ -430,6 +430,115 @@ def test_decode_nan_stays_where_it_is(bits, d):
     check_decode(o2[:, 2:], lse2[:, 2:], q2[:, 2:], held, mask[:, 2:, :1], [64])
 
 
+def shared(cache, B):
+    """B sequences that all read the one sequence of `cache`."""
+    return seer.SeerKVCache(cache.pages, cache.d, cache.bits, block_table=cache.block_table.repeat(B, 1))
+
+
+def check_shared(o, lse, q, kv, mask, lens, which, scale=None):
+    for b in which:
+        check_decode(o[b:b + 1], lse[b:b + 1], q[b:b + 1], kv, mask[b:b + 1], lens[b:b + 1], scale)
+
+
+# Batches large enough for sixteen heads a CTA where a KV head has more than eight.
+
+@pytest.mark.parametrize("bits,d", FORMATS)
+@pytest.mark.parametrize("Hq,Hkv", [(9, 1), (16, 1), (20, 1), (34, 2)])
+@pytest.mark.parametrize("p", [0.05, 0.5, 1.0])
+def test_decode_wide_groups(bits, d, Hq, Hkv, p):
+    B, L = 150, 450
+    cache, table = make_cache(1, Hkv, 9, d, bits, True, Hq)
+    k, v = bf16((1, Hkv, L, d), 1), bf16((1, Hkv, L, d), 2)
+    seer.seer_kv_write(cache, k.cuda(), v.cuda())
+    lens = [(i * 67) % 460 for i in range(B)]
+    lens[:4] = [450, 0, 1, 32]
+    q = bf16((B, Hq, d), 3)
+    mask = (torch.rand((B, Hq, 8), generator=torch.Generator().manual_seed(Hq)) < p).to(torch.uint8) * 64
+    o, lse = seer.seer_block_sparse_decode_quant(q.cuda(), shared(cache, B), mask.cuda(), L, lens=dev32(lens), return_lse=True)
+    seer.seer_check_status()
+    check_shared(o, lse, q, parts(cache, table), mask, [min(x, L) for x in lens], range(B))
+
+
+@pytest.mark.parametrize("bits,d", FORMATS)
+def test_decode_wide_groups_shared_out_by_length(bits, d):
+    B, Hq, Hkv, L = 20, 52, 4, 4000
+    cache, table = make_cache(1, Hkv, 63, d, bits, True, 1)
+    k, v = bf16((1, Hkv, L, d), 1), bf16((1, Hkv, L, d), 2)
+    seer.seer_kv_write(cache, k.cuda(), v.cuda())
+    lens = [L, 0, 17, L] + [200 * i for i in range(B - 4)]
+    q = bf16((B, Hq, d), 3)
+    mask = (torch.rand((B, Hq, 63), generator=torch.Generator().manual_seed(5)) < 0.3).to(torch.uint8)
+    o, lse = seer.seer_block_sparse_decode_quant(q.cuda(), shared(cache, B), mask.cuda(), L, lens=dev32(lens), return_lse=True)
+    seer.seer_check_status()
+    check_shared(o, lse, q, parts(cache, table), mask, lens, range(B))
+
+
+@pytest.mark.parametrize("bits,d", FORMATS)
+@pytest.mark.parametrize("nb", [800, 803])
+def test_decode_wide_groups_long_rows_and_bad_pages(bits, d, nb):
+    B, Hq, Hkv, L = 16, 16, 1, 64 * nb
+    one, table = make_cache(1, Hkv, nb, d, bits, True, 3)
+    k, v = bf16((1, Hkv, L, d), 1), bf16((1, Hkv, L, d), 2)
+    seer.seer_kv_write(one, k.cuda(), v.cuda())
+    cache, held = shared(one, B), parts(one, table)
+    q = bf16((B, Hq, d), 3)
+    mask = (torch.rand((B, Hq, nb), generator=torch.Generator().manual_seed(nb)) < 0.05).to(torch.uint8)
+    mask[:, :, [1, 700, nb - 1]] = 1
+    o, lse = seer.seer_block_sparse_decode_quant(q.cuda(), cache, mask.cuda(), L, return_lse=True)
+    seer.seer_check_status()
+    check_shared(o, lse, q, held, mask, [L] * B, (0, 15))
+    cache.block_table[15, 1], cache.block_table[15, 700], cache.block_table[15, nb - 1] = -1, one.pages.shape[0], 2 ** 30
+    o, lse = seer.seer_block_sparse_decode_quant(q.cuda(), cache, mask.cuda(), L, return_lse=True)
+    with pytest.raises(seer.SeerError):
+        seer.seer_check_status()
+    mask[15, :, [1, 700, nb - 1]] = 0
+    check_shared(o, lse, q, held, mask, [L] * B, (0, 15))
+
+
+@pytest.mark.parametrize("bits,d", FORMATS)
+def test_decode_wide_groups_nan_stays_where_it_is(bits, d):
+    B, Hq, L, G = 150, 16, 450, ref.group(bits)
+    one, table = make_cache(1, 1, 8, d, bits, True, 0)
+    k, v = bf16((1, 1, L, d), 1), bf16((1, 1, L, d), 2)
+    k[0, 0, 70, 3] = float("nan")                           # block 1
+    v[0, 0, 140, d - 1] = float("inf")                      # block 2, the last group
+    seer.seer_kv_write(one, k.cuda(), v.cuda())
+    mask = torch.ones((B, Hq, 8), dtype=torch.uint8)        # by h % 4: all, without block 1, without block 2, without both
+    mask[:, 1::4, 1] = 0
+    mask[:, 2::4, 2] = 0
+    mask[:, 3::4, 1:3] = 0
+    q = bf16((B, Hq, d), 3)
+    q[:, 7, 5] = float("nan")
+    o, lse = seer.seer_block_sparse_decode_quant(q.cuda(), shared(one, B), mask.cuda(), L, return_lse=True)
+    seer.seer_check_status()
+    held = parts(one, table)
+    assert torch.isnan(o[:, 0::4]).all() and torch.isnan(o[:, 2::4]).all() and torch.isnan(o[:, 7]).all()
+    assert torch.isnan(o[:, 1::4, d - G:]).all() and torch.isfinite(o[:, 1::4, :d - G]).all()
+    h = [3, 11, 15]
+    check_shared(o[:, h], lse[:, h], q[:, h], held, mask[:, h], [L] * B, (0, 77, 149))
+
+
+@pytest.mark.parametrize("bits,d", FORMATS)
+@pytest.mark.parametrize("Hq,B", [(4, 1), (16, 150)])
+@pytest.mark.parametrize("step", [0.001, 0.01, 0.1, 3.0, -0.1])
+def test_decode_scores_rising_along_the_cache(bits, d, Hq, B, step):
+    """Maxima that move by less and by more than a step of the running maximum, token after token."""
+    L = 450
+    one, table = make_cache(1, 1, 8, d, bits, True, 0)
+    q = bf16((B, Hq, d), 3)
+    along = torch.zeros(d)
+    along[0::8] = 1.0
+    q[..., 0::8] = q[..., 0::8].abs() + 0.5                 # every head's scores rise
+    k = (bf16((1, 1, L, d), 1).float() * 0.1 + step * torch.arange(L).view(1, 1, L, 1) * along).to(torch.bfloat16)
+    v = bf16((1, 1, L, d), 2)
+    v = (v.float() * 2.0 ** (torch.arange(L) % 7 * 3.0 - 9).view(1, 1, L, 1)).to(torch.bfloat16)
+    seer.seer_kv_write(one, k.cuda(), v.cuda())
+    mask = torch.ones((B, Hq, 8), dtype=torch.uint8)
+    o, lse = seer.seer_block_sparse_decode_quant(q.cuda(), shared(one, B), mask.cuda(), L, return_lse=True)
+    seer.seer_check_status()
+    check_shared(o, lse, q, parts(one, table), mask, [L] * B, (0, B - 1))
+
+
 def test_decode_outputs_written_over_poison_and_repeatable():
     cache, q, mask, o, lse = attend(4, 128, 2, 8, 2, 900, 0.3, seed=21)
     o2, l2 = torch.full_like(o, float("nan")), torch.full_like(lse, float("nan"))

@@ -33,12 +33,12 @@
 //    most; a second kernel joins them.
 //
 // What bounds it: with 8 bits and long caches HBM (128k tokens at density 0.17: the loop
-// itself reads 7 TB/s; 37.7 us a call with start, end and join, 22.8 at the copy
+// itself reads 7 TB/s; 35.5 us a call with start, end and join, 22.8 at the copy
 // rate).  With 4 bits the instructions of the loop: some 350 a tile of 16 tokens
 // and warp, 160 of them on the integer pipe at two cycles each, against 6 cycles
-// a token that HBM allows (32k tokens of a layer, all active: 20.7 us, 6.4 at the
+// a token that HBM allows (32k tokens of a layer, all active: 19.5 us, 6.4 at the
 // copy rate).  Short ones: a CTA's start and end, some 8,000 cycles of latencies,
-// and the join (32k at density 0.1: 11.8 us; 200 tokens: 4.8).
+// and the join (32k at density 0.1: 11.8 us; 200 tokens: 5).
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -264,15 +264,16 @@ struct DecodeArgs {
     uint64_t timeout_ns;
 };
 
-// Warps of a CTA and half records in flight per warp.  Two CTAs share an SM, so
-// that one's start and end (some 8,000 cycles of latencies) pass under the
-// other's products; their rings hold 70 to 200 KB, where the SM's share of HBM
-// (24 bytes a cycle) needs some 40 KB in flight.  Sixteen heads: at D = 128 the
-// accumulators leave four warps their registers (64 units of 256 blocks at 4 bits:
-// 72 us, 74 with six warps, which spill; at 8 bits 59 and 65), at D = 64 six.
-template <int BITS, int D, int H>
+// Warps of a CTA, for P CTAs per SM, and half records in flight per warp.  Of two
+// CTAs one's start and end (some 8,000 cycles of latencies) pass under the other's
+// products; one has twice the warps for its list and half the splits to join.  The
+// rings hold 70 to 200 KB, where the SM's share of HBM (24 bytes a cycle) needs some
+// 40 KB in flight.  Sixteen heads: at D = 128 the accumulators leave eight warps of an
+// SM their registers (64 units of 256 blocks at 4 bits: 72 us, 74 with twelve, which
+// spill; at 8 bits 59 and 65), at D = 64 twelve.
+template <int BITS, int D, int H, int P>
 struct DecodeCfg {
-    static constexpr int W = H == 16 ? (D == 128 ? 4 : 6) : BITS == 8 && D == 128 ? 6 : 8;
+    static constexpr int W = (H == 16 ? (D == 128 ? 4 : 6) : BITS == 8 && D == 128 ? 6 : 8) * (P == 1 ? 2 : 1);
     static constexpr int ST = BITS == 4 && D == 64 ? 4 : 2;
     static constexpr int ring = W * ST * KvFmt<BITS, D>::HALF;
 };
@@ -971,11 +972,11 @@ struct Sums<BITS, D, 16> {
     }
 };
 
-template <int BITS, int D, int H>
-__global__ void __launch_bounds__(DecodeCfg<BITS, D, H>::W * 32, 2) decode_quant_kernel(const DecodeArgs a)
+template <int BITS, int D, int H, int P>
+__global__ void __launch_bounds__(DecodeCfg<BITS, D, H, P>::W * 32, P) decode_quant_kernel(const DecodeArgs a)
 {
     using F = KvFmt<BITS, D>;
-    using C = DecodeCfg<BITS, D, H>;
+    using C = DecodeCfg<BITS, D, H, P>;
     constexpr int W = C::W, ST = C::ST;
     extern __shared__ __align__(128) uint8_t ring[];
     __shared__ __align__(8) uint64_t s_bar[W * ST];
@@ -1021,7 +1022,7 @@ __global__ void __launch_bounds__(DecodeCfg<BITS, D, H>::W * 32, 2) decode_quant
     // table entry, all loads in flight together (and before the length is known).
     // Longer rows: four blocks a lane, where the rows' alignment allows it, and
     // the table is looked up for this split's blocks alone.
-    constexpr int kMaskWords = H == 8 && W < 8 ? 6 : 4;
+    constexpr int kMaskWords = H == 16 && W < 8 ? 4 : (31 + W) / W;
     const int nblk = (len + 63) / 64, nwords = (nblk + 31) / 32;
     const bool one_round = a.nb <= 32 * kMaskWords * W;
     int page[kMaskWords];
@@ -1330,56 +1331,72 @@ __global__ void __launch_bounds__(Q * D) decode_quant_merge_kernel(const DecodeA
         a.lse[bh] = log_sum(M, l);
 }
 
-// Estimated time, in us, of `ctas` CTAs of H heads with `blocks` blocks each:
-//                            eight heads  sixteen
-//   a CTA's start and end          6         8     alone on its SM
-//                                  7.5       9.5   for two at once, per wave
-//   a block                        0.4       0.65  for a CTA alone
-//                                  0.31      0.46  of the SM for two
-//   the second kernel         2 and 0.04 a split
+// How a call is cut up: heads and CTAs of an SM, and the estimated time.
+struct Plan {
+    int H, P;
+    double us;
+};
+
+// Estimated time, in us, of `ctas` CTAs with `blocks` blocks each:
+//                                     eight heads  sixteen
+//   one CTA per SM (P = 1)            7.2          9.2     start and end
+//                                     0.3          0.46    a block
+//   two (P = 2)                       7.5          9.5     start and end, per wave
+//                                     0.31         0.46    a block, of the SM
+//   two, but no more CTAs than SMs    6            8
+//                                     0.4          0.65
+//   the second kernel                 2 and 0.04 a split
 // Measured (4 bits, D = 128): 8 units (a sequence's head tile) of 512 blocks, all
-// active: 18 splits 20.7 us, 24: 23.8, 37: 19.8; a tenth active: 9: 15.2, 18: 11.8,
-// 37: 12.4; 128 units of 256: 1 split 97 us, 2: 86, 4: 91.  Sixteen heads, 64 units
-// of 256 blocks: 1 split 172 us, 2: 93, 4: 70; of 64 blocks: 50, 32, 27.
-double decode_quant_us(int H, long long ctas, double blocks, double splits, int sms)
+// active: P = 1, 9 splits 26.0 us, 12: 22.3, 18: 19.4; P = 2, 18: 20.7, 37: 19.8; a
+// tenth active: P = 1, 9: 14.3, 18: 12.0; P = 2, 18: 11.6, 37: 12.4; 128 units of 256,
+// P = 2: 1 split 97 us, 2: 86, 4: 91.  Sixteen heads, 64 units of 256 blocks, P = 2:
+// 1 split 172 us, 2: 93, 4: 70; of 64 blocks: 50, 32, 27.
+double decode_quant_us(const Plan &p, long long ctas, double blocks, double splits, int sms)
 {
-    const bool two = H == 16;
+    const bool two = p.H == 16;
     const long long load = (ctas + sms - 1) / sms, waves = (load + 1) / 2;
-    return (load == 1 ? (two ? 8.0 : 6.0) + (two ? 0.65 : 0.4) * blocks
-                      : (two ? 9.5 : 7.5) * (double)waves + (two ? 0.46 : 0.31) * (double)load * blocks) +
-           (splits > 1.0 ? 2.0 + 0.04 * splits : 0.0);
+    const double merge = splits > 1.0 ? 2.0 + 0.04 * splits : 0.0;
+    if (p.P == 1)
+        return load > 1 ? 1e30 : (two ? 9.2 : 7.2) + (two ? 0.46 : 0.3) * blocks + merge;
+    if (load == 1)
+        return (two ? 8.0 : 6.0) + (two ? 0.65 : 0.4) * blocks + merge;
+    return (two ? 9.5 : 7.5) * (double)waves + (two ? 0.46 : 0.31) * (double)load * blocks + merge;
 }
 
-// How a call is split for H heads a CTA (nsplit, slots), and its time: the least estimated time with half of the
+// The splits (nsplit, slots) of a plan: the least estimated time with half of the
 // blocks active (the mask is on the device) and at least a block for every
-// second warp.  Lengths given: one or two CTAs per SM in all, where there are
+// second warp.  Lengths given: a CTA for each place on the SMs, where there are
 // enough for every sequence's tiles, shared out by length: a batch of 8 from 32k
 // tokens down takes 45 us with 4 splits each, 39 so.  Not for two or three
-// sequences, whose CTAs pair up on the SMs (64k and 37k tokens at 8 bits: 42 us with
-// 18 splits each, 45 shared out), and in whole splits where a sequence has few
-// (16 of 16k tokens: 88 us with two each, 90 with 37 slots).
-double decode_quant_split(DecodeArgs &a, int H, int sms)
+// sequences, whose CTAs pair up on the SMs (64k and 37k tokens at 8 bits: 40.6 us with
+// 18 splits each, 45 shared out, 41.5 with one CTA per SM), and in whole splits where
+// a sequence has few (16 of 16k tokens: 88 us with two each, 90 with 37 slots).
+void decode_quant_split(DecodeArgs &a, Plan &p, int sms)
 {
     const int g = a.Hq / a.Hkv;
-    a.tiles = (g + H - 1) / H;
+    a.tiles = (g + p.H - 1) / p.H;
     a.per_tile = (g + a.tiles - 1) / a.tiles;
     const int tiles = a.Hkv * a.tiles;
     const int lo = (a.nb + kListMax - 2) / (kListMax - 1);            // a split's block list has to fit
     const int cap = a.nb / 4 < kMaxDecodeSplits ? a.nb / 4 : kMaxDecodeSplits;
-    double best_us = 1e30;
     a.nsplit = lo;
     a.slots = 0;
-    for (int ns = lo; ns <= cap; ++ns) {
-        const double us = decode_quant_us(H, (long long)a.B * tiles * ns, 0.5 * a.nb / ns, ns, sms);
-        if (us < best_us) {
-            best_us = us;
+    p.us = decode_quant_us(p, (long long)a.B * tiles * lo, 0.5 * a.nb / lo, lo, sms);
+    for (int ns = lo + 1; ns <= cap; ++ns) {
+        const double us = decode_quant_us(p, (long long)a.B * tiles * ns, 0.5 * a.nb / ns, ns, sms);
+        if (us < p.us) {
+            p.us = us;
             a.nsplit = ns;
         }
     }
-    if (a.lens == nullptr || a.B < 4 || a.B > kBalanced)
-        return best_us;
-    double shared_us = 1e30;
-    for (int load = 1; load <= 2; ++load) {
+    if (a.lens == nullptr || a.B == 1 || a.B > kBalanced)
+        return;
+    if (a.B < 4) {
+        if (p.P == 1)
+            p.us = 1e30;
+        return;
+    }
+    for (int load = 1; load <= p.P; ++load) {
         int slots = load * sms / tiles;
         if (slots < 4 * a.B)
             slots -= slots % a.B;
@@ -1387,25 +1404,24 @@ double decode_quant_split(DecodeArgs &a, int H, int sms)
         if (slots < a.B * (1 + lo) || slots > a.B * (1 + cap))
             continue;
         const double each = (double)slots / a.B;
-        const double us = decode_quant_us(H, (long long)slots * tiles, 0.5 * a.nb / each, each, sms);
-        if (us < shared_us) {
-            shared_us = us;
+        const double us = decode_quant_us(p, (long long)slots * tiles, 0.5 * a.nb / each, each, sms);
+        if (a.slots == 0 || us < p.us) {
+            p.us = us;
             a.slots = slots;
         }
     }
-    return a.slots > 0 ? shared_us : best_us;
 }
 
-template <int BITS, int D, int H>
+template <int BITS, int D, int H, int P>
 cudaError_t launch(const DecodeArgs &a, cudaStream_t stream)
 {
-    using C = DecodeCfg<BITS, D, H>;
-    cudaError_t e = cudaFuncSetAttribute(decode_quant_kernel<BITS, D, H>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+    using C = DecodeCfg<BITS, D, H, P>;
+    cudaError_t e = cudaFuncSetAttribute(decode_quant_kernel<BITS, D, H, P>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                          C::ring);
     if (e != cudaSuccess)
         return e;
     const dim3 grid(a.slots > 0 ? a.slots : a.nsplit, a.Hkv * a.tiles, a.slots > 0 ? 1 : a.B);
-    decode_quant_kernel<BITS, D, H><<<grid, C::W * 32, C::ring, stream>>>(a);
+    decode_quant_kernel<BITS, D, H, P><<<grid, C::W * 32, C::ring, stream>>>(a);
     e = cudaGetLastError();
     if (e != cudaSuccess || (a.slots == 0 && a.nsplit == 1))
         return e;
@@ -1414,6 +1430,16 @@ cudaError_t launch(const DecodeArgs &a, cudaStream_t stream)
     else
         decode_quant_merge_kernel<D, 1><<<a.B * a.Hq, D, 0, stream>>>(a);
     return cudaGetLastError();
+}
+
+using Launch = cudaError_t (*)(const DecodeArgs &, cudaStream_t);
+
+template <int BITS, int D>
+Launch kernel_of(const Plan &p)
+{
+    if (p.H == 16)
+        return p.P == 1 ? launch<BITS, D, 16, 1> : launch<BITS, D, 16, 2>;
+    return p.P == 1 ? launch<BITS, D, 8, 1> : launch<BITS, D, 8, 2>;
 }
 
 } // namespace
@@ -1444,16 +1470,24 @@ cudaError_t launch_decode_quant(int bits, int B, int Hq, int Hkv, int L, int d, 
         e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
     if (e != cudaSuccess)
         return e;
-    // More than eight heads of a KV head: tiles of sixteen where they are estimated
-    // faster, as they are for enough blocks (groups of 16, 64 units of 256 blocks, all
-    // active: 71 us, 88 by eights; 8 of 512, a tenth active: 24 and 21).
-    const double us = decode_quant_split(a, 8, sms);
-    DecodeArgs wide = a;
-    if (Hq / Hkv > 8 && decode_quant_split(wide, 16, sms) < us)
-        return bits == 4 ? (d == 128 ? launch<4, 128, 16>(wide, stream) : launch<4, 64, 16>(wide, stream))
-                         : (d == 128 ? launch<8, 128, 16>(wide, stream) : launch<8, 64, 16>(wide, stream));
-    return bits == 4 ? (d == 128 ? launch<4, 128, 8>(a, stream) : launch<4, 64, 8>(a, stream))
-                     : (d == 128 ? launch<8, 128, 8>(a, stream) : launch<8, 64, 8>(a, stream));
+    // Eight heads a CTA or, for more of a KV head, sixteen, and one CTA per SM or two of
+    // half the warps: what is estimated fastest.  Sixteen for enough blocks (groups of
+    // 16, 64 units of 256 blocks, all active: 71 us, 88 by eights; 8 of 512, a tenth
+    // active: 24 and 21), one CTA for one round of long ones (decode_quant_us).
+    Plan best{};
+    DecodeArgs args = a;
+    for (int H = 8; H <= (Hq / Hkv > 8 ? 16 : 8); H += 8)
+        for (int P = 1; P <= 2; ++P) {
+            Plan p{H, P, 0.0};
+            decode_quant_split(a, p, sms);
+            if (best.H == 0 || p.us < best.us) {
+                best = p;
+                args = a;
+            }
+        }
+    const Launch f = bits == 4 ? (d == 128 ? kernel_of<4, 128>(best) : kernel_of<4, 64>(best))
+                               : (d == 128 ? kernel_of<8, 128>(best) : kernel_of<8, 64>(best));
+    return f(args, stream);
 }
 
 } // namespace seer

@@ -474,9 +474,13 @@ def test_decode_wide_groups_shared_out_by_length(bits, d):
 
 
 @pytest.mark.parametrize("bits,d", FORMATS)
-@pytest.mark.parametrize("nb", [800, 803])
-def test_decode_wide_groups_long_rows_and_bad_pages(bits, d, nb):
-    B, Hq, Hkv, L = 16, 16, 1, 64 * nb
+@pytest.mark.parametrize("B,Hq,nb", [
+    (16, 16, 800), (16, 16, 803),
+    (150, 16, 800), (150, 16, 803), (4, 16, 1600), (4, 16, 1603),   # rows of more blocks than one round, one CTA per SM or two
+    (1, 4, 1200), (1, 4, 1203),
+])
+def test_decode_long_rows_and_bad_pages_of_shared_caches(bits, d, B, Hq, nb):
+    Hkv, L = 1, 64 * nb
     one, table = make_cache(1, Hkv, nb, d, bits, True, 3)
     k, v = bf16((1, Hkv, L, d), 1), bf16((1, Hkv, L, d), 2)
     seer.seer_kv_write(one, k.cuda(), v.cuda())
@@ -486,13 +490,13 @@ def test_decode_wide_groups_long_rows_and_bad_pages(bits, d, nb):
     mask[:, :, [1, 700, nb - 1]] = 1
     o, lse = seer.seer_block_sparse_decode_quant(q.cuda(), cache, mask.cuda(), L, return_lse=True)
     seer.seer_check_status()
-    check_shared(o, lse, q, held, mask, [L] * B, (0, 15))
-    cache.block_table[15, 1], cache.block_table[15, 700], cache.block_table[15, nb - 1] = -1, one.pages.shape[0], 2 ** 30
+    check_shared(o, lse, q, held, mask, [L] * B, {0, B - 1})
+    cache.block_table[-1, 1], cache.block_table[-1, 700], cache.block_table[-1, nb - 1] = -1, one.pages.shape[0], 2 ** 30
     o, lse = seer.seer_block_sparse_decode_quant(q.cuda(), cache, mask.cuda(), L, return_lse=True)
     with pytest.raises(seer.SeerError):
         seer.seer_check_status()
-    mask[15, :, [1, 700, nb - 1]] = 0
-    check_shared(o, lse, q, held, mask, [L] * B, (0, 15))
+    mask[-1, :, [1, 700, nb - 1]] = 0
+    check_shared(o, lse, q, held, mask, [L] * B, {0, B - 1})
 
 
 @pytest.mark.parametrize("bits,d", FORMATS)

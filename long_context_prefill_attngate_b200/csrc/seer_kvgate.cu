@@ -19,7 +19,7 @@
 //  * Rotation as in the bf16 cache's key rows: frequency and angle in double,
 //    reduced modulo 2 pi, then fp32.
 //
-// 512 blocks of 8 heads at 4 bits (D = d_gate = 128): 11.1 us for 23 MB, of which the
+// 512 blocks of 8 heads at 4 bits (D = d_gate = 128): 10.8 us for 23 MB, of which the
 // pooling of a warp's two blocks, one after the other, is 60 % (latency and
 // instructions; HBM alone would be 3.6 us), the projection and the rotation 8 % each;
 // the last block of 4 sequences (max+min, 8 bits): 5.1 us, all latency.
@@ -150,22 +150,23 @@ __device__ __forceinline__ void ldg_words(uint32_t (&w)[N], const uint8_t *p)
     }
 }
 
-// One pooled value as three bf16 parts.
-__device__ __forceinline__ void put_parts(__nv_bfloat16 *at, int part_stride, float x)
+// Two pooled values as three bf16 parts each.
+__device__ __forceinline__ void put_parts(__nv_bfloat16 *at, int part_stride, float x, float y)
 {
-    const __nv_bfloat16 hi = __float2bfloat16_rn(x);
-    const float r = x - __bfloat162float(hi);
-    const __nv_bfloat16 mid = __float2bfloat16_rn(r);
-    at[0] = hi;
-    at[part_stride] = mid;
-    at[2 * part_stride] = __float2bfloat16_rn(r - __bfloat162float(mid));
+#pragma unroll
+    for (int i = 0; i < 3; ++i) {
+        const __nv_bfloat162 part = __floats2bfloat162_rn(x, y);
+        *reinterpret_cast<__nv_bfloat162 *>(at + i * part_stride) = part;
+        x -= __low2float(part);
+        y -= __high2float(part);
+    }
 }
 
-// The mean of block (page, kvh), `rows` tokens of it, by one warp into row[D]
-// (three parts).  A lane has rows k, k + 1, k + 8, k + 9 (k = 2 tig) of each
-// 16-token tile and the words of its eighth of a row: gid.
+// The mean of block (page, kvh), `rows` tokens of it, by one warp into row[D].
+// A lane has rows k, k + 1, k + 8, k + 9 (k = 2 tig) of each 16-token tile and the
+// words of its eighth of a row: gid.
 template <int BITS, int D>
-__device__ __forceinline__ void pool_mean(const uint8_t *rec, int rows, __nv_bfloat16 *row, int part_stride, int lane)
+__device__ __forceinline__ void pool_mean(const uint8_t *rec, int rows, float *row, int lane)
 {
     using F = KvFmt<BITS, D>;
     constexpr int VW = F::R / 32, EPW = 32 / BITS;       // a lane's words of a row, elements of a word
@@ -254,12 +255,11 @@ __device__ __forceinline__ void pool_mean(const uint8_t *rec, int rows, __nv_bfl
         if (tig != gr >> 1)
             continue;
 #pragma unroll
-        for (int m = 0; m < EPW / 2; ++m)
-#pragma unroll
-            for (int r = 0; r < 2; ++r) {                // element 2m + r in the rows' lower or upper eight
-                const float sum = (gr & 1 ? c[k][m][2 * r + 1] : c[k][m][2 * r]) * down * (BITS == 4 && r ? 1048576.f : 16777216.f);
-                put_parts(row + e0 + 2 * m + r, part_stride, (sum + z) * inv);
-            }
+        for (int m = 0; m < EPW / 2; ++m) {              // elements 2m, 2m + 1: the rows' lower and upper eight
+            const float lo = (gr & 1 ? c[k][m][1] : c[k][m][0]) * down * 16777216.f;
+            const float hi = (gr & 1 ? c[k][m][3] : c[k][m][2]) * down * (BITS == 4 ? 1048576.f : 16777216.f);
+            *reinterpret_cast<float2 *>(row + e0 + 2 * m) = make_float2((lo + z) * inv, (hi + z) * inv);
+        }
     }
 }
 
@@ -342,7 +342,8 @@ __global__ void __launch_bounds__(kGateThreads, 2)
     __nv_bfloat16 *sw = reinterpret_cast<__nv_bfloat16 *>(gsm);          // [DK][ws]
     __nv_bfloat16 *sx = sw + DK * ws;                                    // [3][kGateRows][XS]
     double *sfreq = reinterpret_cast<double *>(sx + 3 * kGateRows * XS); // [dg / 2]
-    float *sy = reinterpret_cast<float *>(sfreq + dg / 2);               // [kGateRows][ys]
+    float *sp = reinterpret_cast<float *>(sfreq + dg / 2);               // [kGateRows][DK] (even)
+    float *sy = sp + kGateRows * DK;                                     // [kGateRows][ys]
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, gid = lane >> 2, tig = lane & 3;
     const int b = blockIdx.y / Hkv, kvh = blockIdx.y % Hkv;
     const int j0 = first + (int)blockIdx.x * kGateRows;
@@ -376,7 +377,7 @@ __global__ void __launch_bounds__(kGateThreads, 2)
         return page < 0 ? nullptr : kv_half<F>(kv, Hkv, page, kvh, 0);
     };
     if constexpr (MAXMIN) {
-        uint32_t *kx = reinterpret_cast<uint32_t *>(sy + kGateRows * ys);          // [kGateRows][DK]
+        uint32_t *kx = reinterpret_cast<uint32_t *>(sp);
         for (int i = threadIdx.x; i < valid * DK; i += kGateThreads)
             kx[i] = 0u;
         __syncthreads();
@@ -387,22 +388,29 @@ __global__ void __launch_bounds__(kGateThreads, 2)
             if (rec != nullptr)
                 pool_extrema<BITS, D>(rec, tokens(i), p * (8 / parts), (p + 1) * (8 / parts), kx + i * DK, lane);
         }
-        __syncthreads();
-        for (int i = threadIdx.x; i < valid * DK; i += kGateThreads) {
-            const float x = kx[i] == 0u ? 0.f : from_max_key(kx[i]);     // no token: 0
-            put_parts(sx + i / DK * XS + i % DK, kGateRows * XS, i % DK < D ? x : -x);
-        }
     } else {
         const uint8_t *next = record(warp);
         for (int i = warp; i < valid; i += kWarps) {
             const uint8_t *rec = next;
             next = record(i + kWarps);                   // a table entry ahead
             if (rec != nullptr)
-                pool_mean<BITS, D>(rec, tokens(i), sx + i * XS, kGateRows * XS, lane);
+                pool_mean<BITS, D>(rec, tokens(i), sp + i * DK, lane);
             else
                 for (int e = lane; e < D; e += 32)
-                    put_parts(sx + i * XS + e, kGateRows * XS, 0.f);
+                    sp[i * DK + e] = 0.f;
         }
+    }
+    __syncthreads();
+    for (int i = 2 * threadIdx.x; i < valid * DK; i += 2 * kGateThreads) {
+        float2 x = *reinterpret_cast<const float2 *>(sp + i);
+        if constexpr (MAXMIN) {
+            auto value = [&](float key) {                // no token: 0
+                const uint32_t k = __float_as_uint(key);
+                return k == 0u ? 0.f : i % DK < D ? from_max_key(k) : -from_max_key(k);
+            };
+            x = make_float2(value(x.x), value(x.y));
+        }
+        put_parts(sx + i / DK * XS + i % DK, kGateRows * XS, x.x, x.y);
     }
     asm volatile("cp.async.wait_group 0;" ::: "memory");
     __syncthreads();
@@ -464,7 +472,7 @@ cudaError_t launch(int B, int Hkv, int L, const KvView &kv, const int32_t *lens,
     constexpr int DK = MAXMIN ? 2 * D : D;
     const int nb = num_blocks(L), dgp = (dg + 7) & ~7;
     const size_t smem = sizeof(__nv_bfloat16) * ((size_t)DK * (dgp + kPad) + 3 * kGateRows * (DK + kPad)) +
-                        sizeof(double) * (dg / 2) + sizeof(float) * kGateRows * (dg + 1 + (MAXMIN ? DK : 0));
+                        sizeof(double) * (dg / 2) + sizeof(float) * kGateRows * (DK + dg + 1);
     const cudaError_t e = cudaFuncSetAttribute(kv_gate_kernel<BITS, D, MAXMIN>,
                                                cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess)

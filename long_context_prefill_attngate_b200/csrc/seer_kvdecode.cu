@@ -166,11 +166,11 @@ __device__ __forceinline__ int tile_token(int r) { return r ^ ((r >> 1) & 1); }
 // 16 banks apart, so eight lanes read 16 bytes each without a conflict.
 template <int BITS, int D, int H>
 struct QShared {
-    static constexpr int NG = KvFmt<BITS, D>::NG, P = H / 8;
+    static constexpr int NG = KvFmt<BITS, D>::NG, P = H == 16 ? 2 : 1;
     static constexpr int STEPS = NG == 4 ? 2 : 1;   // MMA steps of z sum(q)
     static constexpr int kSum = P * D / 2;
     static constexpr int LEN = kSum + P * 8 * STEPS;
-    uint32_t w[8][LEN + (48 - LEN % 32) % 32];
+    uint32_t w[H / P][LEN + (48 - LEN % 32) % 32];
     float inv[H];                                   // 2^-qe
 
     // Element e's half word.
@@ -357,22 +357,24 @@ __device__ __forceinline__ int splits_of(const DecodeArgs &a, int b, int lane)
 }
 
 // What a warp sums up for the heads of its CTA, half record by half record.
+// Up to eight heads: on N, keys or output elements on M.  Up to four stand in N
+// twice (up to two four times), and the places share the groups of a row: each has
+// p s and p z of its own, and one B operand serves a group of every place (32k tokens
+// of a layer, groups of four, all active: 17.9 us, 19.5 with eight columns).
 template <int BITS, int D, int H>
-struct Sums;
-
-// Up to eight heads: on N, keys or output elements on M.
-template <int BITS, int D>
-struct Sums<BITS, D, 8> {
+struct Sums {
     using F = KvFmt<BITS, D>;
     static constexpr int NG = F::NG, R = F::R;
     static constexpr int KS = D / 16;               // MMA steps of a score; also MMA rows of an output / 16
     static constexpr int KW = R / 16, VW = R / 32;  // 32-bit words of a lane's K row, V row
     static constexpr int UPG = KS / NG;             // MMAs of a group
-    using Q = QShared<BITS, D, 8>;
+    static constexpr int REP = 8 / H, NS = NG / REP;   // places of a head, groups of a place
+    static_assert(NS > 0);
+    using Q = QShared<BITS, D, H>;
 
-    float m[2], l[2], zacc[NG][2], acc[KS][4], fac[2];
+    float m[2], l[2], zacc[NS][2], acc[KS][4], fac[2];
     int ve;                                         // exponent field of V's largest scale so far
-    int gid, tig, tr, at_k, at_p, at_z, at_v0, at_v1;
+    int gid, tig, tr, at_k, at_p, at_z, at_pv, at_v0, at_v1;
 
     __device__ __forceinline__ void clear()
     {
@@ -388,14 +390,14 @@ struct Sums<BITS, D, 8> {
         // that a masked score's -infinity stays one)
 #pragma unroll
         for (int e = 0; e < 2; ++e)
-            fac[e] = fminf(fmaxf(sq.inv[2 * tig + e] * scale, 1.2e-38f), 3e38f);
+            fac[e] = fminf(fmaxf(sq.inv[(2 * tig + e) & (H - 1)] * scale, 1.2e-38f), 3e38f);
         clear();
         ve = 27;
 #pragma unroll
         for (int i = 0; i < KS; ++i)
             acc[i][0] = acc[i][1] = acc[i][2] = acc[i][3] = 0.f;
 #pragma unroll
-        for (int gr = 0; gr < NG; ++gr)
+        for (int gr = 0; gr < NS; ++gr)
             zacc[gr][0] = zacc[gr][1] = 0.f;
         // this lane's places in a half record: K row and params of tile row gid (row
         // gid + 8 and the second tile a whole number of rows further, with the same
@@ -405,6 +407,7 @@ struct Sums<BITS, D, 8> {
         at_k = tr * R + (BITS == 8 && D == 128 ? (tr & 1) * 64 + tig * 16 : tig * (R / 4));
         at_p = tr * F::PAR;
         at_z = F::kParK + at_p + Q::par_at(tig, 0);
+        at_pv = F::kParV + at_p + 2 * tig / H * 4 * NS;
         at_v0 = F::kCodeV + t0 * R + (gid ^ F::v_swizzle(t0)) * (R / 8);
         at_v1 = F::kCodeV + t1 * R + (gid ^ F::v_swizzle(t1)) * (R / 8);
     }
@@ -417,13 +420,13 @@ struct Sums<BITS, D, 8> {
         uint32_t qf[KS][2], qz[2 * Q::STEPS];
 #pragma unroll
         for (int i = 0; i < KS; i += 2) {
-            const uint4 x = *reinterpret_cast<const uint4 *>(&sq.w[gid][8 * i + 4 * tig]);
+            const uint4 x = *reinterpret_cast<const uint4 *>(&sq.w[gid & (H - 1)][8 * i + 4 * tig]);
             qf[i][0] = x.x;
             qf[i][1] = x.y;
             qf[i + 1][0] = x.z;
             qf[i + 1][1] = x.w;
         }
-        load_words(qz, reinterpret_cast<const uint8_t *>(&sq.w[gid][Q::kSum + 2 * Q::STEPS * tig]));
+        load_words(qz, reinterpret_cast<const uint8_t *>(&sq.w[gid & (H - 1)][Q::kSum + 2 * Q::STEPS * tig]));
 
         // ---- raw scores of two 16-token tiles
         float s[2][4];
@@ -488,7 +491,7 @@ struct Sums<BITS, D, 8> {
             }
         }
         const bool all_heads = hbits == 0xffffffffu;
-        const bool act0 = hbits >> (2 * tig) & 1u, act1 = hbits >> (2 * tig + 1) & 1u;
+        const bool act0 = hbits >> (2 * tig & (H - 1)) & 1u, act1 = hbits >> ((2 * tig & (H - 1)) + 1) & 1u;
         if (keys < 32) {                            // the sequence's last tokens
             __syncwarp();                           // (keeps this a branch)
 #pragma unroll
@@ -500,13 +503,13 @@ struct Sums<BITS, D, 8> {
         }
 
         // ---- V's params (zero behind the length) and the power of two for p s
-        uint32_t vp[2][2][NG];                      // [tile][row, row + 8]
+        uint32_t vp[2][2][NS];                      // [tile][row, row + 8]
         uint32_t vmax = 0;
 #pragma unroll
         for (int mt = 0; mt < 2; ++mt)
 #pragma unroll
             for (int hf = 0; hf < 2; ++hf)
-                load_words(vp[mt][hf], h + F::kParV + at_p + (16 * mt + 8 * hf) * F::PAR);
+                load_words(vp[mt][hf], h + at_pv + (16 * mt + 8 * hf) * F::PAR);
         if (keys < 32) {
             __syncwarp();
 #pragma unroll
@@ -514,18 +517,21 @@ struct Sums<BITS, D, 8> {
 #pragma unroll
                 for (int hf = 0; hf < 2; ++hf)
 #pragma unroll
-                    for (int gr = 0; gr < NG; ++gr)
+                    for (int gr = 0; gr < NS; ++gr)
                         if (16 * mt + tr + 8 * hf >= keys)
                             vp[mt][hf][gr] = 0u;
         }
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            if constexpr (NG == 1)
+            if constexpr (NS == 1)
                 vmax = __vmaxu2(vmax, vp[i / 2][i % 2][0]);
 #pragma unroll
-            for (int gr = 0; gr + 1 < NG; gr += 2)
+            for (int gr = 0; gr + 1 < NS; gr += 2)
                 vmax = __vimax3_u16x2(vmax, vp[i / 2][i % 2][gr], vp[i / 2][i % 2][gr + 1]);
         }
+#pragma unroll
+        for (int off = H / 2; off < 4; off <<= 1)
+            vmax = __vmaxu2(vmax, __shfl_xor_sync(0xffffffffu, vmax, off));
         float mx[2];
 #pragma unroll
         for (int e = 0; e < 2; ++e)
@@ -554,7 +560,7 @@ struct Sums<BITS, D, 8> {
                 for (int e = 0; e < 4; ++e)
                     acc[i][e] *= alpha[e & 1] * down;
 #pragma unroll
-            for (int gr = 0; gr < NG; ++gr) {
+            for (int gr = 0; gr < NS; ++gr) {
                 zacc[gr][0] *= alpha[0];
                 zacc[gr][1] *= alpha[1];
             }
@@ -590,71 +596,81 @@ struct Sums<BITS, D, 8> {
             for (int e = 0; e < 4; ++e)
                 pu[e] = p[e] * up;
 #pragma unroll
-            for (int gr = 0; gr < NG; ++gr) {
-                const float sa = kv_scale(vp[mt][0][gr]), sb = kv_scale(vp[mt][1][gr]);
-                const float za = kv_zero(vp[mt][0][gr]), zb = kv_zero(vp[mt][1][gr]);
+            for (int j = 0; j < NS; ++j) {
+                const float sa = kv_scale(vp[mt][0][j]), sb = kv_scale(vp[mt][1][j]);
+                const float za = kv_zero(vp[mt][0][j]), zb = kv_zero(vp[mt][1][j]);
                 const uint32_t b0 = movmatrix(pack_half2(pu[0] * sa, pu[1] * sa));
                 const uint32_t b1 = movmatrix(pack_half2(pu[2] * sb, pu[3] * sb));
                 if (act0)                           // a NaN of V stays out of heads that left the block out
-                    zacc[gr][0] = fmaf(p[0], za, fmaf(p[2], zb, zacc[gr][0]));
+                    zacc[j][0] = fmaf(p[0], za, fmaf(p[2], zb, zacc[j][0]));
                 if (act1)
-                    zacc[gr][1] = fmaf(p[1], za, fmaf(p[3], zb, zacc[gr][1]));
-                if constexpr (BITS == 4) {
-                    const unsigned sel = gr & 1 ? 0x7632u : 0x5410u;
-                    // lower rows: an element; upper rows: the byte, that element plus 16 times the next
-                    const uint32_t x01 = __byte_perm(v0[gr / 2], v1[gr / 2], sel), x23 = __byte_perm(v2[gr / 2], v3[gr / 2], sel);
+                    zacc[j][1] = fmaf(p[1], za, fmaf(p[3], zb, zacc[j][1]));
 #pragma unroll
-                    for (int i = 0; i < UPG; ++i) {
-                        const uint32_t y01 = i ? __byte_perm(x01, 0u, 0x4341) : x01 & 0x00FF00FFu;
-                        const uint32_t y23 = i ? __byte_perm(x23, 0u, 0x4341) : x23 & 0x00FF00FFu;
-                        mma16816(acc[gr * UPG + i], y01 & 0x000F000Fu, y01, y23 & 0x000F000Fu, y23, b0, b1);
-                    }
-                } else {
+                for (int gr = j; gr < NG; gr += NS) {
+                    if constexpr (BITS == 4) {
+                        const unsigned sel = gr & 1 ? 0x7632u : 0x5410u;
+                        // lower rows: an element; upper rows: the byte, that element plus 16 times the next
+                        const uint32_t x01 = __byte_perm(v0[gr / 2], v1[gr / 2], sel);
+                        const uint32_t x23 = __byte_perm(v2[gr / 2], v3[gr / 2], sel);
 #pragma unroll
-                    for (int i = 0; i < UPG; ++i) {
-                        const int w = 2 * gr + i / 2;
-                        const unsigned sel = i & 1 ? 0x7632u : 0x5410u;
-                        const uint32_t x01 = __byte_perm(v0[w], v1[w], sel), x23 = __byte_perm(v2[w], v3[w], sel);
-                        mma16816(acc[gr * UPG + i], __byte_perm(x01, 0u, 0x4240), __byte_perm(x01, 0u, 0x4341),
-                                 __byte_perm(x23, 0u, 0x4240), __byte_perm(x23, 0u, 0x4341), b0, b1);
+                        for (int i = 0; i < UPG; ++i) {
+                            const uint32_t y01 = i ? __byte_perm(x01, 0u, 0x4341) : x01 & 0x00FF00FFu;
+                            const uint32_t y23 = i ? __byte_perm(x23, 0u, 0x4341) : x23 & 0x00FF00FFu;
+                            mma16816(acc[gr * UPG + i], y01 & 0x000F000Fu, y01, y23 & 0x000F000Fu, y23, b0, b1);
+                        }
+                    } else {
+#pragma unroll
+                        for (int i = 0; i < UPG; ++i) {
+                            const int w = 2 * gr + i / 2;
+                            const unsigned sel = i & 1 ? 0x7632u : 0x5410u;
+                            const uint32_t x01 = __byte_perm(v0[w], v1[w], sel), x23 = __byte_perm(v2[w], v3[w], sel);
+                            mma16816(acc[gr * UPG + i], __byte_perm(x01, 0u, 0x4240), __byte_perm(x01, 0u, 0x4341),
+                                     __byte_perm(x23, 0u, 0x4240), __byte_perm(x23, 0u, 0x4341), b0, b1);
+                        }
                     }
                 }
             }
         }
     }
 
-    // over the lanes that share a head: maxima and sums to ml[8], outputs to so[8][D]
+    // over the lanes that share a head: maxima and sums to ml[H], outputs to so[H][D]
     __device__ __forceinline__ void finish(float *so, float2 *ml)
     {
+        const int h = 2 * tig & (H - 1), place = 2 * tig / H;                 // first head, which of its places
 #pragma unroll
         for (int off = 4; off < 32; off <<= 1)
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
                 l[e] += __shfl_xor_sync(0xffffffffu, l[e], off);
 #pragma unroll
-                for (int gr = 0; gr < NG; ++gr)
-                    zacc[gr][e] += __shfl_xor_sync(0xffffffffu, zacc[gr][e], off);
+                for (int j = 0; j < NS; ++j)
+                    zacc[j][e] += __shfl_xor_sync(0xffffffffu, zacc[j][e], off);
             }
-        if (gid == 0) {
-            ml[2 * tig] = make_float2(m[0] == -INFINITY ? m[0] : m[0] * fac[0], l[0]);
-            ml[2 * tig + 1] = make_float2(m[1] == -INFINITY ? m[1] : m[1] * fac[1], l[1]);
+        if (gid == 0 && place == 0) {
+            ml[h] = make_float2(m[0] == -INFINITY ? m[0] : m[0] * fac[0], l[0]);
+            ml[h + 1] = make_float2(m[1] == -INFINITY ? m[1] : m[1] * fac[1], l[1]);
         }
         const float un = pow2_field(ve - 14 + kSlack);       // with 2^24 the inverse of `up` and the codes' unit
 #pragma unroll
         for (int e = 0; e < 2; ++e)
 #pragma unroll
-            for (int gr = 0; gr < NG; ++gr)
+            for (int j = 0; j < NS; ++j)
 #pragma unroll
                 for (int i = 0; i < UPG; i += 2) {
                     float v[4];
 #pragma unroll
                     for (int k = 0; k < 2; ++k) {
-                        const float lo = acc[gr * UPG + i + k][e], hi = acc[gr * UPG + i + k][e + 2];
-                        v[2 * k] = lo * un * 16777216.f + zacc[gr][e];
-                        v[2 * k + 1] = (BITS == 4 ? (hi - lo) * un * 1048576.f : hi * un * 16777216.f) + zacc[gr][e];
+                        float lo = acc[j * UPG + i + k][e], hi = acc[j * UPG + i + k][e + 2];
+#pragma unroll
+                        for (int r = 1; r < REP; ++r) {
+                            lo = place == r ? acc[(r * NS + j) * UPG + i + k][e] : lo;
+                            hi = place == r ? acc[(r * NS + j) * UPG + i + k][e + 2] : hi;
+                        }
+                        v[2 * k] = lo * un * 16777216.f + zacc[j][e];
+                        v[2 * k + 1] = (BITS == 4 ? (hi - lo) * un * 1048576.f : hi * un * 16777216.f) + zacc[j][e];
                     }
                     const float4 r = make_float4(v[0], v[1], v[2], v[3]);
-                    *reinterpret_cast<float4 *>(so + (2 * tig + e) * D + F::G * gr + gid * (F::G / 8) + 2 * i) = r;
+                    *reinterpret_cast<float4 *>(so + (h + e) * D + F::G * (place * NS + j) + gid * (F::G / 8) + 2 * i) = r;
                 }
     }
 };
@@ -1437,6 +1453,12 @@ using Launch = cudaError_t (*)(const DecodeArgs &, cudaStream_t);
 template <int BITS, int D>
 Launch kernel_of(const Plan &p)
 {
+    if constexpr (KvFmt<BITS, D>::NG == 4)
+        if (p.H == 2)
+            return p.P == 1 ? launch<BITS, D, 2, 1> : launch<BITS, D, 2, 2>;
+    if constexpr (KvFmt<BITS, D>::NG > 1)
+        if (p.H == 4)
+            return p.P == 1 ? launch<BITS, D, 4, 1> : launch<BITS, D, 4, 2>;
     if (p.H == 16)
         return p.P == 1 ? launch<BITS, D, 16, 1> : launch<BITS, D, 16, 2>;
     return p.P == 1 ? launch<BITS, D, 8, 1> : launch<BITS, D, 8, 2>;
@@ -1470,13 +1492,15 @@ cudaError_t launch_decode_quant(int bits, int B, int Hq, int Hkv, int L, int d, 
         e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
     if (e != cudaSuccess)
         return e;
-    // Eight heads a CTA or, for more of a KV head, sixteen, and one CTA per SM or two of
+    // Two, four or eight heads a CTA by the heads of a KV head or, for more, sixteen, and one CTA per SM or two of
     // half the warps: what is estimated fastest.  Sixteen for enough blocks (groups of
     // 16, 64 units of 256 blocks, all active: 71 us, 88 by eights; 8 of 512, a tenth
     // active: 24 and 21), one CTA for one round of long ones (decode_quant_us).
     Plan best{};
     DecodeArgs args = a;
-    for (int H = 8; H <= (Hq / Hkv > 8 ? 16 : 8); H += 8)
+    const int g = Hq / Hkv, groups = d / (bits == 4 ? 32 : 64);
+    const int least = g <= 2 && groups == 4 ? 2 : g <= 4 && groups > 1 ? 4 : 8;
+    for (int H = least; H <= (g > 8 ? 16 : least); H += H)
         for (int P = 1; P <= 2; ++P) {
             Plan p{H, P, 0.0};
             decode_quant_split(a, p, sms);

@@ -33,12 +33,12 @@
 //    most; a second kernel joins them.
 //
 // What bounds it: with 8 bits and long caches HBM (128k tokens at density 0.17: the loop
-// itself reads 7 TB/s; 35.5 us a call with start, end and join, 22.8 at the copy
-// rate).  With 4 bits the instructions of the loop: some 350 a tile of 16 tokens
-// and warp, 160 of them on the integer pipe at two cycles each, against 6 cycles
-// a token that HBM allows (32k tokens of a layer, all active: 19.5 us, 6.4 at the
-// copy rate).  Short ones: a CTA's start and end, some 8,000 cycles of latencies,
-// and the join (32k at density 0.1: 11.8 us; 200 tokens: 5).
+// itself reads 7 TB/s; 35.2 us a call with start, end and join, 22.8 at the copy
+// rate).  With 4 bits the instructions of the loop, about half of them on the integer
+// pipe at two cycles each, against 6 cycles a token that HBM allows (32k tokens of a
+// layer, all active: 17.9 us, 6.4 at the copy rate).  Short ones: a CTA's start and
+// end, some 8,000 cycles of latencies, and the join (32k at density 0.1: 10.8 us; 200
+// tokens: 4.6).
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -1354,19 +1354,19 @@ struct Plan {
 };
 
 // Estimated time, in us, of `ctas` CTAs with `blocks` blocks each:
-//                                     eight heads  sixteen
-//   one CTA per SM (P = 1)            7.2          9.2     start and end
-//                                     0.3          0.46    a block
-//   two (P = 2)                       7.5          9.5     start and end, per wave
-//                                     0.31         0.46    a block, of the SM
-//   two, but no more CTAs than SMs    6            8
-//                                     0.4          0.65
+//                                     to eight heads   sixteen
+//   one CTA per SM (P = 1)            7.2              9.2     start and end
+//                                     0.3              0.46    a block
+//   two (P = 2)                       7.5              9.5     start and end, per wave
+//                                     0.31             0.46    a block, of the SM
+//   two, but no more CTAs than SMs    6                8
+//                                     0.4              0.65
 //   the second kernel                 2 and 0.04 a split
-// Measured (4 bits, D = 128): 8 units (a sequence's head tile) of 512 blocks, all
-// active: P = 1, 9 splits 26.0 us, 12: 22.3, 18: 19.4; P = 2, 18: 20.7, 37: 19.8; a
-// tenth active: P = 1, 9: 14.3, 18: 12.0; P = 2, 18: 11.6, 37: 12.4; 128 units of 256,
-// P = 2: 1 split 97 us, 2: 86, 4: 91.  Sixteen heads, 64 units of 256 blocks, P = 2:
-// 1 split 172 us, 2: 93, 4: 70; of 64 blocks: 50, 32, 27.
+// Measured (4 bits, D = 128, eight columns of heads): 8 units (a sequence's head
+// tile) of 512 blocks, all active: P = 1, 9 splits 26.0 us, 12: 22.3, 18: 19.4;
+// P = 2, 18: 20.7, 37: 19.8; a tenth active: P = 1, 9: 14.3, 18: 12.0; P = 2, 18: 11.6,
+// 37: 12.4; 128 units of 256, P = 2: 1 split 97 us, 2: 86, 4: 91.  Sixteen heads, 64
+// units of 256 blocks, P = 2: 1 split 172 us, 2: 93, 4: 70; of 64 blocks: 50, 32, 27.
 double decode_quant_us(const Plan &p, long long ctas, double blocks, double splits, int sms)
 {
     const bool two = p.H == 16;
@@ -1383,8 +1383,8 @@ double decode_quant_us(const Plan &p, long long ctas, double blocks, double spli
 // blocks active (the mask is on the device) and at least a block for every
 // second warp.  Lengths given: a CTA for each place on the SMs, where there are
 // enough for every sequence's tiles, shared out by length: a batch of 8 from 32k
-// tokens down takes 45 us with 4 splits each, 39 so.  Not for two or three
-// sequences, whose CTAs pair up on the SMs (64k and 37k tokens at 8 bits: 40.6 us with
+// tokens down took 45 us with 4 splits each, 39 so.  Not for two or three
+// sequences, whose CTAs pair up on the SMs (64k and 37k tokens at 8 bits: 40.7 us with
 // 18 splits each, 45 shared out, 41.5 with one CTA per SM), and in whole splits where
 // a sequence has few (16 of 16k tokens: 88 us with two each, 90 with 37 slots).
 void decode_quant_split(DecodeArgs &a, Plan &p, int sms)

@@ -376,6 +376,13 @@ def test_decode_ranges(bits, d, kscale, vscale, scale):
 
 
 @pytest.mark.parametrize("bits,d", FORMATS)
+@pytest.mark.parametrize("B,Hq", [(1, 4), (1, 8), (150, 12)])
+@pytest.mark.parametrize("kscale,vscale,scale", [(30.0, 1.0, None), (1.0, 1e12, None), (1e-3, 1e-12, 5.0)])
+def test_decode_ranges_of_groups_of_any_size(bits, d, B, Hq, kscale, vscale, scale):
+    attend(bits, d, B, Hq, 1, 400, 0.7, seed=14, kscale=kscale, vscale=vscale, scale=scale)
+
+
+@pytest.mark.parametrize("bits,d", FORMATS)
 def test_decode_token_scales_far_apart(bits, d):
     """V of neighbouring tokens 2^40 apart in magnitude, growing and shrinking along the cache; q far from 1."""
     B, Hq, Hkv, L = 1, 8, 2, 400
@@ -500,8 +507,9 @@ def test_decode_long_rows_and_bad_pages_of_shared_caches(bits, d, B, Hq, nb):
 
 
 @pytest.mark.parametrize("bits,d", FORMATS)
-def test_decode_wide_groups_nan_stays_where_it_is(bits, d):
-    B, Hq, L, G = 150, 16, 450, ref.group(bits)
+@pytest.mark.parametrize("B,Hq", [(150, 16), (1, 16), (1, 8), (1, 4), (1, 2)])
+def test_decode_nan_stays_where_it_is_in_groups_of_any_size(bits, d, B, Hq):
+    L, G = 450, ref.group(bits)
     one, table = make_cache(1, 1, 8, d, bits, True, 0)
     k, v = bf16((1, 1, L, d), 1), bf16((1, 1, L, d), 2)
     k[0, 0, 70, 3] = float("nan")                           # block 1
@@ -512,18 +520,23 @@ def test_decode_wide_groups_nan_stays_where_it_is(bits, d):
     mask[:, 2::4, 2] = 0
     mask[:, 3::4, 1:3] = 0
     q = bf16((B, Hq, d), 3)
-    q[:, 7, 5] = float("nan")
+    q[:, 7:8, 5] = float("nan")
     o, lse = seer.seer_block_sparse_decode_quant(q.cuda(), shared(one, B), mask.cuda(), L, return_lse=True)
     seer.seer_check_status()
     held = parts(one, table)
-    assert torch.isnan(o[:, 0::4]).all() and torch.isnan(o[:, 2::4]).all() and torch.isnan(o[:, 7]).all()
+    assert torch.isnan(o[:, 0::4]).all() and torch.isnan(o[:, 2::4]).all() and torch.isnan(o[:, 7:8]).all()
     assert torch.isnan(o[:, 1::4, d - G:]).all() and torch.isfinite(o[:, 1::4, :d - G]).all()
-    h = [3, 11, 15]
-    check_shared(o[:, h], lse[:, h], q[:, h], held, mask[:, h], [L] * B, (0, 77, 149))
+    h = [x for x in (3, 11, 15) if x < Hq]
+    if h:
+        check_shared(o[:, h], lse[:, h], q[:, h], held, mask[:, h], [L] * B, {0, B // 2, B - 1})
+    kq, vq = held                                           # the groups before the NaN, of a head that takes its block
+    vq = (vq[0], vq[1], np.where(np.isnan(vq[2]), 0.0, vq[2]))
+    want = ref.decode(f64(q[:1, 1:2]), kq, vq, mask[:1, 1:2].numpy(), [L])[0][0, 0, :d - G]
+    assert np.all(np.abs(f64(o[0, 1, :d - G]) - want) <= 2.0 ** -6 * (np.abs(want) + 0.1))
 
 
 @pytest.mark.parametrize("bits,d", FORMATS)
-@pytest.mark.parametrize("Hq,B", [(4, 1), (16, 150)])
+@pytest.mark.parametrize("Hq,B", [(4, 1), (16, 150), (2, 1), (8, 1)])
 @pytest.mark.parametrize("step", [0.001, 0.01, 0.1, 3.0, -0.1])
 def test_decode_scores_rising_along_the_cache(bits, d, Hq, B, step):
     """Maxima that move by less and by more than a step of the running maximum, token after token."""

@@ -24,9 +24,11 @@ import torch
 from . import _binding as B
 from ._binding import _check, _need, lib
 
-try:                                                # the current stream's pointer without a Stream object around it
-    from torch._C import _cuda_getCurrentRawStream as _current_stream
+try:                                                # without a Stream object, and for devices that tensors live on
+    from torch._C import _cuda_getCurrentRawStream as _current_stream, _cuda_getDevice as _current_device
 except ImportError:
+    _current_device = torch.cuda.current_device
+
     def _current_stream(dev):
         return torch.cuda.current_stream(dev).cuda_stream
 
@@ -37,17 +39,23 @@ _bf16, _f32, _i32, _u8 = torch.bfloat16, torch.float32, torch.int32, torch.uint8
 @functools.lru_cache(maxsize=None)
 def seer_kv_record_bytes(bits: int, d: int) -> int:
     """Bytes of a cache record: one head's 64 tokens of K and V."""
-    n = int(lib().seer_kv_record_bytes(int(bits), int(d)))
+    n = int((B._lib or lib()).seer_kv_record_bytes(int(bits), int(d)))
     if n == 0:
         raise B.SeerError(B.SEER_ERR_UNSUPPORTED, B.seer_last_error())
     return n
+
+
+@functools.lru_cache(maxsize=1024)
+def _attention_workspace(Bsz: int, Hq: int, Hkv: int, d: int) -> int:
+    """Bytes of the attention's workspace: the same for every L."""
+    return B.seer_workspace_bytes(B.SEER_CALL_BLOCK_SPARSE_DECODE_QUANT, B.seer_shape(Bsz, Hq, Hkv, 1, d))
 
 
 class SeerKVCache:
     """Pages u8 [n_pages, Hkv, record] and, for sequences that share them, a block table int32 [B, max_blocks]
     (without one, page b * max_blocks + j is block j of sequence b)."""
 
-    __slots__ = ("pages", "block_table", "d", "bits", "Hkv", "B", "max_blocks", "_dev", "_c", "_ws")
+    __slots__ = ("pages", "block_table", "d", "bits", "Hkv", "B", "max_blocks", "_dev", "_c")
 
     def __init__(self, pages, d: int, bits: int, block_table=None, batch: int = 1):
         _need((bits == 4 or bits == 8) and (d == 128 or d == 64), "a cache has 4 or 8 bits and a head dim of 64 or 128")
@@ -65,7 +73,6 @@ class SeerKVCache:
             _need(batch >= 1 and n_pages % batch == 0, "pages must be batch * max_blocks without a block table")
             self.B, self.max_blocks = batch, n_pages // batch
         self.pages, self.block_table, self.d, self.bits = pages, block_table, d, bits
-        self._ws = {}                               # bytes of the attention's workspace by Hq
         self._c = B.seer_kv_cache(bits, n_pages, self.max_blocks, pages.data_ptr(),
                                   None if block_table is None else block_table.data_ptr())
 
@@ -85,7 +92,7 @@ def _on(dev: int, stream, call):
     """call(stream pointer) with device `dev` current and, if a stream is given, that stream current too: what torch
     allocates in it then belongs to the stream that uses it."""
     _need(dev >= 0, "the cache must be on a CUDA device")
-    if stream is None and dev == torch.cuda.current_device():
+    if stream is None and dev == _current_device():
         return call(_current_stream(dev))
     with torch.cuda.device(dev):
         if stream is None:
@@ -136,7 +143,7 @@ def seer_kv_write(cache, k, v, start=None, count=None, start_pos: int = 0, strea
     sp, cp = _per_sequence(cache, _START, start), _per_sequence(cache, _COUNT, count)
     rows = B.seer_kv_rows(k.data_ptr(), v.data_ptr(), *_strides(k, shape, _LAYOUT), *_strides(v, shape, _LAYOUT))
     sh = B.seer_shape(cache.B, cache.Hkv, cache.Hkv, shape[2], cache.d)
-    _on(cache._dev, stream, lambda st: _check(lib().seer_kv_write(
+    _on(cache._dev, stream, lambda st: _check((B._lib or lib()).seer_kv_write(
         _byref(sh), _byref(cache._c), _byref(rows), sp, cp, int(start_pos), st)))
 
 
@@ -154,7 +161,7 @@ def seer_kv_read(cache, n: int, start=None, count=None, start_pos: int = 0, k=No
         make = torch.empty if count is None else torch.zeros
         ko = make(*shape, dtype=_bf16, device=cache.pages.device) if k is None else k
         vo = make(*shape, dtype=_bf16, device=cache.pages.device) if v is None else v
-        _check(lib().seer_kv_read(_byref(sh), _byref(cache._c), sp, cp, int(start_pos), ko.data_ptr(), vo.data_ptr(), st))
+        _check((B._lib or lib()).seer_kv_read(_byref(sh), _byref(cache._c), sp, cp, int(start_pos), ko.data_ptr(), vo.data_ptr(), st))
         return ko, vo
 
     return _on(cache._dev, stream, call)
@@ -180,7 +187,7 @@ def seer_gate_key_cache_quant(cache, wk, L: int, kt=None, first_block: int = 0, 
 
     def call(st):
         out = torch.empty(*shape, dtype=_f32, device=cache.pages.device) if kt is None else kt
-        _check(lib().seer_gate_key_cache_quant(_byref(sh), _byref(cache._c), lp, wk.data_ptr(), _byref(gp),
+        _check((B._lib or lib()).seer_gate_key_cache_quant(_byref(sh), _byref(cache._c), lp, wk.data_ptr(), _byref(gp),
                                                int(first_block), out.data_ptr(), st))
         return out
 
@@ -206,16 +213,14 @@ def seer_block_sparse_decode_quant(q_tok, cache, mask, L: int, lens=None, softma
     lp = _per_sequence(cache, _LENS, lens)
     sh = B.seer_shape(cache.B, Hq, cache.Hkv, int(L), cache.d)
 
-    need = cache._ws.get(Hq)
-    if need is None:                                # (the same for every L)
-        need = cache._ws[Hq] = B.seer_workspace_bytes(B.SEER_CALL_BLOCK_SPARSE_DECODE_QUANT, sh)
+    need = _attention_workspace(cache.B, Hq, cache.Hkv, cache.d)
 
     def call(st):
         out = torch.empty_like(q_tok) if o is None else o
         ls = torch.empty(cache.B, Hq, dtype=_f32, device=cache.pages.device) if return_lse and lse is None else lse
         ws = cache.pages.new_empty(need) if workspace is None else workspace
         wsb = need if workspace is None else workspace.numel() * workspace.element_size()
-        _check(lib().seer_block_sparse_decode_quant(
+        _check((B._lib or lib()).seer_block_sparse_decode_quant(
             _byref(sh), q_tok.data_ptr(), _byref(cache._c), lp, mask.data_ptr(), float(softmax_scale),
             out.data_ptr(), None if ls is None else ls.data_ptr(), ws.data_ptr(), wsb, st))
         return (out, ls) if ls is not None else out

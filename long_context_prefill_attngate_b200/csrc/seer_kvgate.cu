@@ -4,11 +4,11 @@
 //
 // One kernel: a CTA pools sixteen blocks of a head and projects them.
 //  * Pooling reads the K half of each record once (HBM-bound for a whole
-//    cache).  The mean is an MMA too: the codes, transposed by pairing two
-//    tokens' words, are the fp16 subnormals n 2^-24 on M (as in the decode
-//    kernel), a group's scales are a column of N, normalised by the block's
-//    largest scale (exact in fp16 down to 2^-29 of it), and z is summed in fp32.
-//    0.75 integer operations an element instead of two and two fp32 ones.
+//    cache).  The mean is an MMA too: the codes are the fp16 subnormals n 2^-24 on
+//    M (as in the decode kernel), a group's scales are two columns of N, normalised
+//    by the block's largest scale (exact in fp16 down to 2^-29 of it), and z is
+//    summed in fp32.  Half an integer operation an element instead of two and two
+//    fp32 ones.
 //    Max and min (the other pooling) take z + s n element by element; their
 //    warps share a block's rows when the CTA has few blocks.
 //  * Projection: sixteen pooled rows are the M of an mma.sync m16n8k16 (the
@@ -19,10 +19,10 @@
 //  * Rotation as in the bf16 cache's key rows: frequency and angle in double,
 //    reduced modulo 2 pi, then fp32.
 //
-// 512 blocks of 8 heads at 4 bits (D = d_gate = 128): 10.8 us for 23 MB, of which the
-// pooling of a warp's two blocks, one after the other, is 60 % (latency and
+// 512 blocks of 8 heads at 4 bits (D = d_gate = 128): 10.1 us for 23 MB, of which the
+// pooling of a warp's two blocks, one after the other, is half (latency and
 // instructions; HBM alone would be 3.6 us), the projection and the rotation 8 % each;
-// the last block of 4 sequences (max+min, 8 bits): 5.1 us, all latency.
+// the last block of 4 sequences (max+min, 8 bits): 5.5 us, all latency.
 #include <cmath>
 
 #include <cuda_bf16.h>
@@ -163,13 +163,15 @@ __device__ __forceinline__ void put_parts(__nv_bfloat16 *at, int part_stride, fl
 }
 
 // The mean of block (page, kvh), `rows` tokens of it, by one warp into row[D].
-// A lane has rows k, k + 1, k + 8, k + 9 (k = 2 tig) of each 16-token tile and the
-// words of its eighth of a row: gid.
+// A lane has the words of its eighth of a row, gid, of four tokens of every 16.
+// An A operand's pair is two elements of one word, so its even and odd places sum
+// up for different elements: a group's scales stand in two columns of N, once in
+// the even places (zero in the odd ones) and once in the odd.
 template <int BITS, int D>
 __device__ __forceinline__ void pool_mean(const uint8_t *rec, int rows, float *row, int lane)
 {
     using F = KvFmt<BITS, D>;
-    constexpr int VW = F::R / 32, EPW = 32 / BITS;       // a lane's words of a row, elements of a word
+    constexpr int VW = F::R / 32, U = BITS == 4 ? 2 : 1;  // a lane's words of a row, MMAs of a word
     const int gid = lane >> 2, tig = lane & 3;
     // every load of the block first (rows behind its tokens too: their scales count as 0)
     uint32_t w[4][4][VW], par[4][4];                     // [tile][row of the lane]
@@ -181,7 +183,8 @@ __device__ __forceinline__ void pool_mean(const uint8_t *rec, int rows, float *r
             const int at = BITS == 8 && D == 128 ? ((gid >> 2) ^ (t & 1)) * 64 + (gid & 3) * 16 : gid * (F::R / 8);
             ldg_words(w[mt][i], rec + mt / 2 * F::HALF + t * F::R + at);
         }
-    // scales of group gid and the sum of its zeros
+    // scales of group gid / 2 and the sum of its zeros
+    const int gr = gid >> 1;
     uint32_t smax = 0;
     float zs = 0.f;
 #pragma unroll
@@ -189,76 +192,83 @@ __device__ __forceinline__ void pool_mean(const uint8_t *rec, int rows, float *r
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             const int t = 16 * mt + 2 * tig + (i & 1) + (i >> 1) * 8;
-            par[mt][i] = gid < F::NG && t < rows ? __ldg(reinterpret_cast<const uint32_t *>(
-                                                             rec + t / 32 * F::HALF + F::kParK + t % 32 * F::PAR) + gid)
-                                                 : 0u;
+            par[mt][i] = gr < F::NG && t < rows ? __ldg(reinterpret_cast<const uint32_t *>(
+                                                            rec + t / 32 * F::HALF + F::kParK + t % 32 * F::PAR) + gr)
+                                                : 0u;
         }
 #pragma unroll
     for (int mt = 0; mt < 4; ++mt)
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            smax = max(smax, par[mt][i] & 0xFFFFu);
+            smax = __vmaxu2(smax, par[mt][i]);
             zs += kv_zero(par[mt][i]);
         }
     zs += __shfl_xor_sync(0xffffffffu, zs, 1);
     zs += __shfl_xor_sync(0xffffffffu, zs, 2);
-    smax = __reduce_max_sync(0xffffffffu, smax);
+    smax = __reduce_max_sync(0xffffffffu, smax & 0xFFFFu);
     const int se = max((int)(smax >> 7), 27);            // exponent field of the largest scale, at least 2^-100's
     const float up = __uint_as_float((uint32_t)(268 - se) << 23);      // scales to at most 2^15
-    float c[VW][EPW / 2][4];
+    const unsigned first = gid & 1 ? 0x1044u : 0x4410u, second = gid & 1 ? 0x3244u : 0x4432u;
+    float c[VW][U][4];
 #pragma unroll
     for (int k = 0; k < VW; ++k)
 #pragma unroll
-        for (int m = 0; m < EPW / 2; ++m)
-            c[k][m][0] = c[k][m][1] = c[k][m][2] = c[k][m][3] = 0.f;
+        for (int u = 0; u < U; ++u)
+            c[k][u][0] = c[k][u][1] = c[k][u][2] = c[k][u][3] = 0.f;
 #pragma unroll
-    for (int mt = 0; mt < 4; ++mt) {
-        const uint32_t b0 = pack_half2(kv_scale(par[mt][0]) * up, kv_scale(par[mt][1]) * up);
-        const uint32_t b1 = pack_half2(kv_scale(par[mt][2]) * up, kv_scale(par[mt][3]) * up);
+    for (int mt = 0; mt < 4; ++mt)
 #pragma unroll
-        for (int k = 0; k < VW; ++k)
+        for (int i = 0; i < 4; i += 2) {
+            const uint32_t s2 = pack_half2(kv_scale(par[mt][i]) * up, kv_scale(par[mt][i + 1]) * up);
+            const uint32_t b0 = __byte_perm(s2, 0u, first), b1 = __byte_perm(s2, 0u, second);
 #pragma unroll
-            for (int hw = 0; hw < 2; ++hw) {             // halves of a word of two tokens
-                uint32_t x01 = __byte_perm(w[mt][0][k], w[mt][1][k], hw ? 0x7632 : 0x5410);
-                uint32_t x23 = __byte_perm(w[mt][2][k], w[mt][3][k], hw ? 0x7632 : 0x5410);
+            for (int k = 0; k < VW; ++k) {
+                uint32_t x = w[mt][i][k], y = w[mt][i + 1][k];
                 if constexpr (BITS == 4) {
 #pragma unroll
                     for (int u = 0; u < 2; ++u) {
-                        mma_f16(c[k][2 * hw + u], x01 & 0x000F000Fu, x01 & 0x00F000F0u, x23 & 0x000F000Fu,
-                                x23 & 0x00F000F0u, b0, b1);
-                        x01 >>= 8;
-                        x23 >>= 8;
+                        mma_f16(c[k][u], x & 0x000F000Fu, x & 0x00F000F0u, y & 0x000F000Fu, y & 0x00F000F0u, b0, b1);
+                        x >>= 8;
+                        y >>= 8;
                     }
                 } else {
-                    mma_f16(c[k][hw], __byte_perm(x01, 0u, 0x4240), __byte_perm(x01, 0u, 0x4341),
-                            __byte_perm(x23, 0u, 0x4240), __byte_perm(x23, 0u, 0x4341), b0, b1);
+                    mma_f16(c[k][0], __byte_perm(x, 0u, 0x4140), __byte_perm(x, 0u, 0x4342), __byte_perm(y, 0u, 0x4140),
+                            __byte_perm(y, 0u, 0x4342), b0, b1);
                 }
             }
-    }
-    // a lane's elements: of word k, (hw, u) -> e; the group of its words is a column of c
+        }
+    // a lane holds the sums of the words whose group is tig
     const float down = __uint_as_float((uint32_t)(se - 14) << 23), inv = 1.f / (float)rows;
+    const float z = __shfl_sync(0xffffffffu, zs, 8 * tig);
 #pragma unroll
     for (int k = 0; k < VW; ++k) {
-        int gr, e0;                                      // group and first element of the word
+        int g, e0;                                       // group and first element of the word
         if (BITS == 4) {
             const int wd = gid * VW + k;
-            gr = wd % F::NG;
-            e0 = 32 * gr + wd / F::NG * 8;
+            g = wd % F::NG;
+            e0 = 32 * g + wd / F::NG * 8;
         } else if (D == 128) {
-            gr = gid >> 2;
-            e0 = 64 * gr + 16 * k + 4 * (gid & 3);
+            g = gid >> 2;
+            e0 = 64 * g + 16 * k + 4 * (gid & 3);
         } else {
-            gr = 0;
+            g = 0;
             e0 = 16 * (gid * 2 % 4 + k) + 4 * (gid / 2);
         }
-        const float z = __shfl_sync(0xffffffffu, zs, gr * 4);
-        if (tig != gr >> 1)
+        if (tig != g)
             continue;
 #pragma unroll
-        for (int m = 0; m < EPW / 2; ++m) {              // elements 2m, 2m + 1: the rows' lower and upper eight
-            const float lo = (gr & 1 ? c[k][m][1] : c[k][m][0]) * down * 16777216.f;
-            const float hi = (gr & 1 ? c[k][m][3] : c[k][m][2]) * down * (BITS == 4 ? 1048576.f : 16777216.f);
-            *reinterpret_cast<float2 *>(row + e0 + 2 * m) = make_float2((lo + z) * inv, (hi + z) * inv);
+        for (int u = 0; u < U; ++u) {
+            const float v0 = c[k][u][0] * down * 16777216.f, v1 = c[k][u][1] * down * 16777216.f;
+            const float v2 = c[k][u][2] * down * (BITS == 4 ? 1048576.f : 16777216.f);
+            const float v3 = c[k][u][3] * down * (BITS == 4 ? 1048576.f : 16777216.f);
+            float2 *at = reinterpret_cast<float2 *>(row + e0 + 2 * u);
+            if (BITS == 4) {                             // elements 2u, 2u + 1 and four further
+                at[0] = make_float2((v0 + z) * inv, (v2 + z) * inv);
+                at[2] = make_float2((v1 + z) * inv, (v3 + z) * inv);
+            } else {
+                at[0] = make_float2((v0 + z) * inv, (v1 + z) * inv);
+                at[1] = make_float2((v2 + z) * inv, (v3 + z) * inv);
+            }
         }
     }
 }
@@ -347,7 +357,13 @@ __global__ void __launch_bounds__(kGateThreads, 2)
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, gid = lane >> 2, tig = lane & 3;
     const int b = blockIdx.y / Hkv, kvh = blockIdx.y % Hkv;
     const int j0 = first + (int)blockIdx.x * kGateRows;
+    const int valid = min(kGateRows, nb - j0);
+    __shared__ int s_page[kGateRows];
+    // length and pages on their way while Wk is fetched
     const int len = lens != nullptr ? max(0, min(__ldg(lens + b), L)) : L;
+    int page = b * kv.max_blocks + j0 + (int)threadIdx.x;
+    if (threadIdx.x < valid && kv.table != nullptr)
+        page = __ldg(kv.table + (long long)b * kv.max_blocks + j0 + threadIdx.x);
 
     // ---- Wk of the head on its way to shared memory
     const __nv_bfloat16 *w = wk + (long long)kvh * wk_stride;
@@ -366,21 +382,26 @@ __global__ void __launch_bounds__(kGateThreads, 2)
     asm volatile("cp.async.commit_group;" ::: "memory");
     if (threadIdx.x < dg / 2)
         sfreq[threadIdx.x] = exp(log_freq * (double)threadIdx.x);
+    auto tokens = [&](int i) { return i < valid ? min(64, len - 64 * (j0 + i)) : 0; };
+    if (threadIdx.x < valid) {                           // -1: a block without a token, or an entry that names no page
+        const bool used = tokens(threadIdx.x) > 0, bad = page < 0 || page >= kv.n_pages;
+        if (used && bad)
+            set_status(status, kStatusPage);
+        s_page[threadIdx.x] = used && !bad ? page : -1;
+    }
+    uint32_t *kx = reinterpret_cast<uint32_t *>(sp);     // max+min: the keys, no token yet
+    if constexpr (MAXMIN)
+        for (int i = threadIdx.x; i < valid * DK; i += kGateThreads)
+            kx[i] = 0u;
+    __syncthreads();
 
     // ---- pooling (rows of sx behind the last block stay unwritten: their
     // products are rows of their own, which nothing reads)
     constexpr int kWarps = kGateThreads / 32;
-    const int valid = min(kGateRows, nb - j0);
-    auto tokens = [&](int i) { return i < valid ? min(64, len - 64 * (j0 + i)) : 0; };
-    auto record = [&](int i) -> const uint8_t * {        // null where block j0 + i has no token or no page
-        const int page = tokens(i) > 0 ? kv_page(kv, b, j0 + i, status) : -1;
-        return page < 0 ? nullptr : kv_half<F>(kv, Hkv, page, kvh, 0);
+    auto record = [&](int i) -> const uint8_t * {        // null where block j0 + i has none
+        return s_page[i] < 0 ? nullptr : kv_half<F>(kv, Hkv, s_page[i], kvh, 0);
     };
     if constexpr (MAXMIN) {
-        uint32_t *kx = reinterpret_cast<uint32_t *>(sp);
-        for (int i = threadIdx.x; i < valid * DK; i += kGateThreads)
-            kx[i] = 0u;
-        __syncthreads();
         const int parts = valid <= 4 ? kWarps : 1;       // warps that share a block: an eighth costs a fifth of the whole
         for (int u = warp; u < valid * parts; u += kWarps) {
             const int i = u / parts, p = u % parts;
@@ -389,10 +410,8 @@ __global__ void __launch_bounds__(kGateThreads, 2)
                 pool_extrema<BITS, D>(rec, tokens(i), p * (8 / parts), (p + 1) * (8 / parts), kx + i * DK, lane);
         }
     } else {
-        const uint8_t *next = record(warp);
         for (int i = warp; i < valid; i += kWarps) {
-            const uint8_t *rec = next;
-            next = record(i + kWarps);                   // a table entry ahead
+            const uint8_t *rec = record(i);
             if (rec != nullptr)
                 pool_mean<BITS, D>(rec, tokens(i), sp + i * DK, lane);
             else

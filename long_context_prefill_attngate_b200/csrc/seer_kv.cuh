@@ -18,6 +18,39 @@
 
 namespace seer {
 
+// The cache's kernels start while the kernel before them in their stream ends (a
+// programmatic launch: between two of them the launch latency, some 2 us of a call
+// outside a graph, passes under the first) and wait for it, and for what it wrote,
+// before they touch memory.  All threads, first of all.  Loads are plain ones: a
+// read-only load (ld.global.nc) would be free to pass the wait.
+__device__ __forceinline__ void wait_for_previous_kernel()
+{
+    asm volatile("griddepcontrol.wait;\n\tgriddepcontrol.launch_dependents;" ::: "memory");
+}
+
+template <class T>
+__device__ __forceinline__ T load(const T *p)
+{
+    return *p;
+}
+
+template <class... P, class... A>
+cudaError_t launch_programmatic(void (*kernel)(P...), dim3 grid, int threads, size_t smem, cudaStream_t stream, A... args)
+{
+    cudaLaunchAttribute attr{};
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, P(args)...);
+    return e == cudaSuccess ? e : cudaGetLastError();    // (and cleared)
+}
+
 // What the kernels need of a seer_kv_cache.
 struct KvView {
     uint8_t *pages;              // [n_pages, Hkv, record]
@@ -68,7 +101,7 @@ struct KvFmt {
 // the table names none of the cache's pages.  j is within max_blocks.
 __device__ __forceinline__ int kv_page(const KvView &kv, int b, int j, int *status)
 {
-    const int p = kv.table != nullptr ? __ldg(kv.table + (long long)b * kv.max_blocks + j) : b * kv.max_blocks + j;
+    const int p = kv.table != nullptr ? load(kv.table + (long long)b * kv.max_blocks + j) : b * kv.max_blocks + j;
     if (p < 0 || p >= kv.n_pages) {
         set_status(status, kStatusPage);
         return -1;

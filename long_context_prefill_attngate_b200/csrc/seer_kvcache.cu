@@ -51,8 +51,8 @@ __device__ __forceinline__ PageRows page_rows(const KvView &kv, int Hkv, int b, 
                                               const int32_t *count, int start_pos, int *status)
 {
     PageRows r{nullptr, 0, 0, 0};
-    const int rows = count != nullptr ? min(__ldg(count + b), n) : n;
-    const long long first = (long long)(start != nullptr ? __ldg(start + b) : 0) + start_pos;
+    const int rows = count != nullptr ? min(load(count + b), n) : n;
+    const long long first = (long long)(start != nullptr ? load(start + b) : 0) + start_pos;
     if (rows <= 0)
         return r;
     // beyond +- 2^22 no row of at most 2^20 meets a cache of at most 2^20 tokens
@@ -223,6 +223,7 @@ __global__ void __launch_bounds__(kRowThreads) kv_write_kernel(KvView kv, KvRows
     using F = KvFmt<BITS, D>;
     using M = RowMap<BITS, D, 16>;
     constexpr int NI = 64 / (kRowThreads / 32 * M::RPW);  // rows of a lane for each of K and V
+    wait_for_previous_kernel();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, c = lane % M::CH;
     const int b = blockIdx.y / Hkv, kvh = blockIdx.y % Hkv;
     const PageRows r = page_rows<F>(kv, Hkv, b, kvh, n, start, count, start_pos, status);
@@ -240,8 +241,8 @@ __global__ void __launch_bounds__(kRowThreads) kv_write_kernel(KvView kv, KvRows
             in[is_v][i][0] = in[is_v][i][1] = make_uint4(0u, 0u, 0u, 0u);
             if (t >= r.lo && t < r.hi) {
                 const uint4 *at = reinterpret_cast<const uint4 *>(src[is_v] + t * (is_v ? x.v_stride_t : x.k_stride_t));
-                in[is_v][i][0] = __ldg(at);
-                in[is_v][i][1] = __ldg(at + 1);
+                in[is_v][i][0] = load(at);
+                in[is_v][i][1] = load(at + 1);
             }
         }
 #pragma unroll
@@ -303,6 +304,7 @@ __global__ void __launch_bounds__(kRowThreads) kv_read_kernel(KvView kv, int Hkv
     using F = KvFmt<BITS, D>;
     using M = RowMap<BITS, D, 8>;
     constexpr int NI = 64 / (kRowThreads / 32 * M::RPW);
+    wait_for_previous_kernel();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, c = lane % M::CH;
     const int b = blockIdx.y / Hkv, kvh = blockIdx.y % Hkv;
     const PageRows r = page_rows<F>(kv, Hkv, b, kvh, n, start, count, start_pos, status);
@@ -385,8 +387,8 @@ cudaError_t launch_kv_write(int bits, int B, int Hkv, int n, int d, const KvView
 {
     const auto f = bits == 4 ? (d == 128 ? kv_write_kernel<4, 128> : kv_write_kernel<4, 64>)
                              : (d == 128 ? kv_write_kernel<8, 128> : kv_write_kernel<8, 64>);
-    f<<<dim3(pages_of(n), B * Hkv), kRowThreads, 0, stream>>>(kv, x, Hkv, n, start, count, start_pos, status);
-    return cudaGetLastError();
+    return launch_programmatic(f, dim3(pages_of(n), B * Hkv), kRowThreads, 0, stream, kv, x, Hkv, n, start, count, start_pos,
+                               status);
 }
 
 cudaError_t launch_kv_read(int bits, int B, int Hkv, int n, int d, const KvView &kv, const int32_t *start,
@@ -394,10 +396,8 @@ cudaError_t launch_kv_read(int bits, int B, int Hkv, int n, int d, const KvView 
 {
     const auto f = bits == 4 ? (d == 128 ? kv_read_kernel<4, 128> : kv_read_kernel<4, 64>)
                              : (d == 128 ? kv_read_kernel<8, 128> : kv_read_kernel<8, 64>);
-    f<<<dim3(pages_of(n), B * Hkv), kRowThreads, 0, stream>>>(kv, Hkv, n, start, count, start_pos,
-                                                              static_cast<__nv_bfloat16 *>(k),
-                                                              static_cast<__nv_bfloat16 *>(v), status);
-    return cudaGetLastError();
+    return launch_programmatic(f, dim3(pages_of(n), B * Hkv), kRowThreads, 0, stream, kv, Hkv, n, start, count, start_pos,
+                               static_cast<__nv_bfloat16 *>(k), static_cast<__nv_bfloat16 *>(v), status);
 }
 
 } // namespace seer

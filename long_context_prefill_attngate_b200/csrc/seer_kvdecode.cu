@@ -199,11 +199,11 @@ struct QShared {
     __device__ __forceinline__ static void fetch(Raw &u, const __nv_bfloat16 *qp, int lane)
     {
         if constexpr (N == 4) {
-            const uint2 x = qp != nullptr ? __ldg(reinterpret_cast<const uint2 *>(qp) + lane) : make_uint2(0u, 0u);
+            const uint2 x = qp != nullptr ? load(reinterpret_cast<const uint2 *>(qp) + lane) : make_uint2(0u, 0u);
             u[0] = x.x;
             u[1] = x.y;
         } else {
-            u[0] = qp != nullptr ? __ldg(reinterpret_cast<const uint32_t *>(qp) + lane) : 0u;
+            u[0] = qp != nullptr ? load(reinterpret_cast<const uint32_t *>(qp) + lane) : 0u;
         }
     }
     // ... and into its row.
@@ -288,7 +288,7 @@ constexpr int kBalanced = 64;             // sequences
 
 __device__ __forceinline__ int blocks_of(const DecodeArgs &a, int b)
 {
-    return b < a.B ? (max(0, min(__ldg(a.lens + b), a.L)) + 63) / 64 : 0;
+    return b < a.B ? (max(0, min(load(a.lens + b), a.L)) + 63) / 64 : 0;
 }
 
 struct Shares {
@@ -1002,6 +1002,7 @@ __global__ void __launch_bounds__(DecodeCfg<BITS, D, H, P>::W * 32, P) decode_qu
     __shared__ uint16_t s_block[kListMax];
     __shared__ __align__(16) QShared<BITS, D, H> s_q;
 
+    wait_for_previous_kernel();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     int b, split, ns;
     if (!slot_of(a, lane, b, split, ns))
@@ -1055,12 +1056,12 @@ __global__ void __launch_bounds__(DecodeCfg<BITS, D, H, P>::W * 32, P) decode_qu
                 for (int h = 0; h < H; ++h) {
                     raw[i][h] = 0;
                     if (h < gt)
-                        raw[i][h] = __ldg(mrow + (long long)h * a.nb + j);
+                        raw[i][h] = load(mrow + (long long)h * a.nb + j);
                 }
                 if (one_round) {
                     page[i] = b * a.kv.max_blocks + j;
                     if (a.kv.table != nullptr)
-                        page[i] = __ldg(a.kv.table + page[i]);
+                        page[i] = load(a.kv.table + page[i]);
                 }
             }
 #pragma unroll
@@ -1087,7 +1088,7 @@ __global__ void __launch_bounds__(DecodeCfg<BITS, D, H, P>::W * 32, P) decode_qu
                 for (int h = 0; h < H; ++h) {
                     raw[i][h] = 0;
                     if (h < gt)
-                        raw[i][h] = __ldg(reinterpret_cast<const uint32_t *>(mrow + (long long)h * a.nb + j));
+                        raw[i][h] = load(reinterpret_cast<const uint32_t *>(mrow + (long long)h * a.nb + j));
                 }
             }
 #pragma unroll
@@ -1165,7 +1166,7 @@ __global__ void __launch_bounds__(DecodeCfg<BITS, D, H, P>::W * 32, P) decode_qu
             __syncthreads();
             for (int i = threadIdx.x; i < r1 - r0; i += W * 32) {
                 const int j = s_block[i], at = b * a.kv.max_blocks + j;
-                entry(i, j, a.kv.table != nullptr ? __ldg(a.kv.table + at) : at);
+                entry(i, j, a.kv.table != nullptr ? load(a.kv.table + at) : at);
             }
         }
     }
@@ -1183,7 +1184,7 @@ __global__ void __launch_bounds__(DecodeCfg<BITS, D, H, P>::W * 32, P) decode_qu
                   F::HALF, my_bar + 8 * st);
     };
     auto head_byte = [&](int u) {
-        return u < n_units && lane < gt ? (int)__ldg(mrow + (long long)lane * a.nb + (s_block[u >> 1] & (kNoPage - 1))) : 0;
+        return u < n_units && lane < gt ? (int)load(mrow + (long long)lane * a.nb + (s_block[u >> 1] & (kNoPage - 1))) : 0;
     };
     if (lane == 0)
         for (int s = 0; s < ST; ++s)
@@ -1287,6 +1288,7 @@ __global__ void __launch_bounds__(Q * D) decode_quant_merge_kernel(const DecodeA
 {
     constexpr int N = Q == 4 ? kMaxDecodeSplits / 4 : 8;
     __shared__ float s_w[kMaxDecodeSplits], s_part[Q][D];
+    wait_for_previous_kernel();
     const long long bh = blockIdx.x;
     const int lane = threadIdx.x & 31, c = threadIdx.x % D, q = threadIdx.x / D;
     const int nsplit = splits_of(a, blockIdx.x / a.Hq, lane);
@@ -1437,15 +1439,12 @@ cudaError_t launch(const DecodeArgs &a, cudaStream_t stream)
     if (e != cudaSuccess)
         return e;
     const dim3 grid(a.slots > 0 ? a.slots : a.nsplit, a.Hkv * a.tiles, a.slots > 0 ? 1 : a.B);
-    decode_quant_kernel<BITS, D, H, P><<<grid, C::W * 32, C::ring, stream>>>(a);
-    e = cudaGetLastError();
+    e = launch_programmatic(decode_quant_kernel<BITS, D, H, P>, grid, C::W * 32, C::ring, stream, a);
     if (e != cudaSuccess || (a.slots == 0 && a.nsplit == 1))
         return e;
     if ((a.slots > 0 ? a.slots / a.B : a.nsplit) > 8)
-        decode_quant_merge_kernel<D, 4><<<a.B * a.Hq, 4 * D, 0, stream>>>(a);
-    else
-        decode_quant_merge_kernel<D, 1><<<a.B * a.Hq, D, 0, stream>>>(a);
-    return cudaGetLastError();
+        return launch_programmatic(decode_quant_merge_kernel<D, 4>, dim3(a.B * a.Hq), 4 * D, 0, stream, a);
+    return launch_programmatic(decode_quant_merge_kernel<D, 1>, dim3(a.B * a.Hq), D, 0, stream, a);
 }
 
 using Launch = cudaError_t (*)(const DecodeArgs &, cudaStream_t);

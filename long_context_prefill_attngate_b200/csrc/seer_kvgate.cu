@@ -136,17 +136,17 @@ template <int N>
 __device__ __forceinline__ void ldg_words(uint32_t (&w)[N], const uint8_t *p)
 {
     if constexpr (N == 8) {
-        const uint4 x = __ldg(reinterpret_cast<const uint4 *>(p)), y = __ldg(reinterpret_cast<const uint4 *>(p) + 1);
+        const uint4 x = load(reinterpret_cast<const uint4 *>(p)), y = load(reinterpret_cast<const uint4 *>(p) + 1);
         w[0] = x.x, w[1] = x.y, w[2] = x.z, w[3] = x.w, w[4] = y.x, w[5] = y.y, w[6] = y.z, w[7] = y.w;
     } else if constexpr (N == 4) {
-        const uint4 x = __ldg(reinterpret_cast<const uint4 *>(p));
+        const uint4 x = load(reinterpret_cast<const uint4 *>(p));
         w[0] = x.x, w[1] = x.y, w[2] = x.z, w[3] = x.w;
     } else if constexpr (N == 2) {
-        const uint2 x = __ldg(reinterpret_cast<const uint2 *>(p));
+        const uint2 x = load(reinterpret_cast<const uint2 *>(p));
         w[0] = x.x, w[1] = x.y;
     } else {
         static_assert(N == 1);
-        w[0] = __ldg(reinterpret_cast<const uint32_t *>(p));
+        w[0] = load(reinterpret_cast<const uint32_t *>(p));
     }
 }
 
@@ -192,7 +192,7 @@ __device__ __forceinline__ void pool_mean(const uint8_t *rec, int rows, float *r
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             const int t = 16 * mt + 2 * tig + (i & 1) + (i >> 1) * 8;
-            par[mt][i] = gr < F::NG && t < rows ? __ldg(reinterpret_cast<const uint32_t *>(
+            par[mt][i] = gr < F::NG && t < rows ? load(reinterpret_cast<const uint32_t *>(
                                                             rec + t / 32 * F::HALF + F::kParK + t % 32 * F::PAR) + gr)
                                                 : 0u;
         }
@@ -354,16 +354,17 @@ __global__ void __launch_bounds__(kGateThreads, 2)
     double *sfreq = reinterpret_cast<double *>(sx + 3 * kGateRows * XS); // [dg / 2]
     float *sp = reinterpret_cast<float *>(sfreq + dg / 2);               // [kGateRows][DK] (even)
     float *sy = sp + kGateRows * DK;                                     // [kGateRows][ys]
+    wait_for_previous_kernel();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, gid = lane >> 2, tig = lane & 3;
     const int b = blockIdx.y / Hkv, kvh = blockIdx.y % Hkv;
     const int j0 = first + (int)blockIdx.x * kGateRows;
     const int valid = min(kGateRows, nb - j0);
     __shared__ int s_page[kGateRows];
     // length and pages on their way while Wk is fetched
-    const int len = lens != nullptr ? max(0, min(__ldg(lens + b), L)) : L;
+    const int len = lens != nullptr ? max(0, min(load(lens + b), L)) : L;
     int page = b * kv.max_blocks + j0 + (int)threadIdx.x;
     if (threadIdx.x < valid && kv.table != nullptr)
-        page = __ldg(kv.table + (long long)b * kv.max_blocks + j0 + threadIdx.x);
+        page = load(kv.table + (long long)b * kv.max_blocks + j0 + threadIdx.x);
 
     // ---- Wk of the head on its way to shared memory
     const __nv_bfloat16 *w = wk + (long long)kvh * wk_stride;
@@ -496,10 +497,10 @@ cudaError_t launch(int B, int Hkv, int L, const KvView &kv, const int32_t *lens,
                                                cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess)
         return e;
-    kv_gate_kernel<BITS, D, MAXMIN><<<dim3((nb - first + kGateRows - 1) / kGateRows, B * Hkv), kGateThreads, smem, stream>>>(
-        kv, Hkv, L, lens, nb, first, static_cast<const __nv_bfloat16 *>(wk), wk_stride, dg,
-        -2.0 * log((double)theta) / dg, kt, status);
-    return cudaGetLastError();
+    return launch_programmatic(kv_gate_kernel<BITS, D, MAXMIN>, dim3((nb - first + kGateRows - 1) / kGateRows, B * Hkv),
+                               kGateThreads, smem, stream, kv, Hkv, L, lens, nb, first,
+                               static_cast<const __nv_bfloat16 *>(wk), wk_stride, dg, -2.0 * log((double)theta) / dg, kt,
+                               status);
 }
 
 } // namespace

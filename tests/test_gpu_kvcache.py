@@ -700,3 +700,72 @@ def test_decode_wait_timeout_is_reported_and_recoverable():
     o2, l2 = seer.seer_block_sparse_decode_quant(q.cuda(), cache, mask.cuda(), 60000, return_lse=True)
     seer.seer_check_status()
     assert torch.equal(o, o2) and torch.equal(lse, l2)
+
+
+# ------------------------------------------------------------------ kernels that start while the one before them ends
+
+def chain(cache, kv, q, wk, wq, mask, L, between, side=None):
+    """Rows over rows of the same places, each read, pooled and attended to by the call behind it."""
+    B, Hq, d = q.shape
+    n = kv[0][0].shape[2]
+    outs = []
+    for i, (k, v) in enumerate(kv):
+        at = (i % 2) * (L - n)
+        seer.seer_kv_write(cache, k, v, start_pos=at)
+        between()
+        rows = seer.seer_kv_read(cache, n, start_pos=at, k=torch.empty_like(k), v=torch.empty_like(v))
+        between()
+        kt = seer.seer_gate_key_cache_quant(cache, wk, L)
+        between()
+        scores = seer.seer_decode_gate_scores_cached(q, kt, wq, L, kt.shape[1])
+        lse = torch.zeros((B, Hq), device="cuda")
+        if side is not None:                                # a stream beside it reads the same cache
+            side.wait_stream(torch.cuda.current_stream())
+            with torch.cuda.stream(side):
+                other = seer.seer_block_sparse_decode_quant(q, cache, mask, L)
+        o = seer.seer_block_sparse_decode_quant(q, cache, mask, L, lse=lse)[0]
+        between()
+        if side is not None:
+            torch.cuda.current_stream().wait_stream(side)
+            outs.append(other)
+        q = o                                               # the next step's token from this one's output
+        outs += [*rows, kt, scores, o, lse]
+    return outs
+
+
+@pytest.mark.parametrize("bits,d", FORMATS)
+@pytest.mark.parametrize("B,Hkv,g,L", [(8, 4, 4, 4096), (1, 2, 16, 700), (40, 4, 10, 2000)])
+def test_calls_back_to_back(bits, d, B, Hkv, g, L):
+    """The same bits whether each call's kernels follow at once, after a wait on the host, or from a captured graph."""
+    nb, dg, steps = -(-L // 64), 64, 12
+    n = L // 2
+    kv = [(bf16((B, Hkv, n, d), 2 * i).cuda(), bf16((B, Hkv, n, d), 2 * i + 1).cuda()) for i in range(3)]
+    kv = [kv[i % 3] for i in range(steps)]
+    q, wk = bf16((B, Hkv * g, d), 7).cuda(), bf16((Hkv, d, dg), 8, 0.1).cuda()
+    wq = bf16((Hkv * g, d, dg), 9, 0.1).cuda()
+    mask = (torch.rand((B, Hkv * g, nb), generator=torch.Generator().manual_seed(1)) < 0.5).to(torch.uint8).cuda()
+
+    def run(between=lambda: None, side=None):
+        cache, _ = make_cache(B, Hkv, nb, d, bits, True, 4)
+        seer.seer_kv_write(cache, torch.zeros((B, Hkv, L, d), dtype=torch.bfloat16, device="cuda"),
+                           torch.zeros((B, Hkv, L, d), dtype=torch.bfloat16, device="cuda"))
+        return chain(cache, kv, q, wk, wq, mask, L, between, side)
+
+    want = run(torch.cuda.synchronize)
+    seer.seer_check_status()
+    for _ in range(3):
+        got = run()
+        assert all(torch.equal(a, b) for a, b in zip(got, want, strict=True))
+    cache, _ = make_cache(B, Hkv, nb, d, bits, True, 4)
+    zero = torch.zeros((B, Hkv, L, d), dtype=torch.bfloat16, device="cuda")
+    side, graph = torch.cuda.Stream(), torch.cuda.CUDAGraph()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(graph):
+        seer.seer_kv_write(cache, zero, zero)
+        got = chain(cache, kv, q, wk, wq, mask, L, lambda: None, side)
+    for _ in range(3):
+        graph.replay()
+        torch.cuda.synchronize()
+        seer.seer_check_status()
+        assert all(torch.equal(a, b) for a, b in zip([x for i, x in enumerate(got) if i % 7], want, strict=True))
+        assert all(torch.equal(got[7 * i], got[7 * i + 5]) for i in range(steps))

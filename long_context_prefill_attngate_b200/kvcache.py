@@ -88,28 +88,26 @@ class SeerKVCache:
         return self.max_blocks * B.BLOCK
 
 
-def _on(dev: int, stream, call):
-    """call(stream pointer) with device `dev` current and, if a stream is given, that stream current too: what torch
-    allocates in it then belongs to the stream that uses it."""
+def _elsewhere(fn, dev: int, stream, *args):
+    """fn(*args) with device `dev` current and, if a stream is given, that stream current too: what torch allocates
+    then belongs to the stream that uses it."""
     _need(dev >= 0, "the cache must be on a CUDA device")
-    if stream is None and dev == _current_device():
-        return call(_current_stream(dev))
     with torch.cuda.device(dev):
         if stream is None:
-            return call(_current_stream(dev))
+            return fn(*args)
         if not hasattr(stream, "cuda_stream"):
             stream = torch.cuda.ExternalStream(int(stream)) if int(stream) else torch.cuda.default_stream()
         with torch.cuda.stream(stream):
-            return call(stream.cuda_stream)
+            return fn(*args)
 
 
 def _per_sequence(cache, name, t):
     """The pointer of an optional int32 [B] of the cache's device."""
     if t is None:
         return None
-    _need(t.dtype is _i32 and t.dim() == 1 and t.shape[0] == cache.B and t.is_contiguous() and
-          t.get_device() == cache._dev, name)
-    return t.data_ptr()
+    if t.dtype is _i32 and t.shape == (cache.B,) and t.is_contiguous() and t.get_device() == cache._dev:
+        return t.data_ptr()
+    raise ValueError(name)
 
 
 _START = "start must be int32 [B] on the cache's device"
@@ -139,12 +137,17 @@ def seer_kv_write(cache, k, v, start=None, count=None, start_pos: int = 0, strea
     _need(len(shape) == 4 and shape == v.shape and shape[0] == cache.B and shape[1] == cache.Hkv and shape[3] == cache.d,
           "k and v must be [B,Hkv,n,d] of the cache")
     _need(k.dtype is _bf16 and v.dtype is _bf16, "k and v must be bf16")
-    _need(k.get_device() == cache._dev and v.get_device() == cache._dev, "k and v must be on the cache's device")
+    dev = cache._dev
+    _need(k.get_device() == dev and v.get_device() == dev, "k and v must be on the cache's device")
     sp, cp = _per_sequence(cache, _START, start), _per_sequence(cache, _COUNT, count)
+    if stream is not None or dev < 0 or dev != _current_device():
+        return _elsewhere(seer_kv_write, dev, stream, cache, k, v, start, count, start_pos)
     rows = B.seer_kv_rows(k.data_ptr(), v.data_ptr(), *_strides(k, shape, _LAYOUT), *_strides(v, shape, _LAYOUT))
     sh = B.seer_shape(cache.B, cache.Hkv, cache.Hkv, shape[2], cache.d)
-    _on(cache._dev, stream, lambda st: _check((B._lib or lib()).seer_kv_write(
-        _byref(sh), _byref(cache._c), _byref(rows), sp, cp, int(start_pos), st)))
+    st = (B._lib or lib()).seer_kv_write(_byref(sh), _byref(cache._c), _byref(rows), sp, cp, int(start_pos),
+                                         _current_stream(dev))
+    if st:
+        _check(st)
 
 
 def seer_kv_read(cache, n: int, start=None, count=None, start_pos: int = 0, k=None, v=None, stream=None):
@@ -155,16 +158,20 @@ def seer_kv_read(cache, n: int, start=None, count=None, start_pos: int = 0, k=No
         _need(t is None or (t.dtype is _bf16 and t.shape == shape and t.is_contiguous() and t.get_device() == cache._dev),
               "k and v must be contiguous bf16 [B,Hkv,n,d] on the cache's device")
     sp, cp = _per_sequence(cache, _START, start), _per_sequence(cache, _COUNT, count)
+    dev = cache._dev
+    if stream is not None or dev < 0 or dev != _current_device():
+        return _elsewhere(seer_kv_read, dev, stream, cache, n, start, count, start_pos, k, v)
+    make = torch.empty if count is None else torch.zeros
+    if k is None:
+        k = make(*shape, dtype=_bf16, device=cache.pages.device)
+    if v is None:
+        v = make(*shape, dtype=_bf16, device=cache.pages.device)
     sh = B.seer_shape(cache.B, cache.Hkv, cache.Hkv, int(n), cache.d)
-
-    def call(st):
-        make = torch.empty if count is None else torch.zeros
-        ko = make(*shape, dtype=_bf16, device=cache.pages.device) if k is None else k
-        vo = make(*shape, dtype=_bf16, device=cache.pages.device) if v is None else v
-        _check((B._lib or lib()).seer_kv_read(_byref(sh), _byref(cache._c), sp, cp, int(start_pos), ko.data_ptr(), vo.data_ptr(), st))
-        return ko, vo
-
-    return _on(cache._dev, stream, call)
+    st = (B._lib or lib()).seer_kv_read(_byref(sh), _byref(cache._c), sp, cp, int(start_pos), k.data_ptr(), v.data_ptr(),
+                                        _current_stream(dev))
+    if st:
+        _check(st)
+    return k, v
 
 
 def seer_gate_key_cache_quant(cache, wk, L: int, kt=None, first_block: int = 0, lens=None, rope_theta: float = 5e5,
@@ -182,16 +189,18 @@ def seer_gate_key_cache_quant(cache, wk, L: int, kt=None, first_block: int = 0, 
     _need(kt is None or (kt.dtype is _f32 and kt.shape == shape and kt.is_contiguous() and kt.get_device() == dev),
           "kt must be contiguous fp32 [B,Hkv,nb,d_gate] on the cache's device")
     lp = _per_sequence(cache, _LENS, lens)
+    if stream is not None or dev < 0 or dev != _current_device():
+        return _elsewhere(seer_gate_key_cache_quant, dev, stream, cache, wk, L, kt, first_block, lens, rope_theta, None,
+                          wk_head_stride, k_maxmin)
+    if kt is None:
+        kt = torch.empty(*shape, dtype=_f32, device=cache.pages.device)
     sh = B.seer_shape(cache.B, cache.Hkv, cache.Hkv, int(L), cache.d)
     gp = B.seer_gate_params(dg, float(rope_theta), 0, int(wk_head_stride), int(bool(k_maxmin)))
-
-    def call(st):
-        out = torch.empty(*shape, dtype=_f32, device=cache.pages.device) if kt is None else kt
-        _check((B._lib or lib()).seer_gate_key_cache_quant(_byref(sh), _byref(cache._c), lp, wk.data_ptr(), _byref(gp),
-                                               int(first_block), out.data_ptr(), st))
-        return out
-
-    return _on(dev, stream, call)
+    st = (B._lib or lib()).seer_gate_key_cache_quant(_byref(sh), _byref(cache._c), lp, wk.data_ptr(), _byref(gp),
+                                                     int(first_block), kt.data_ptr(), _current_stream(dev))
+    if st:
+        _check(st)
+    return kt
 
 
 def seer_block_sparse_decode_quant(q_tok, cache, mask, L: int, lens=None, softmax_scale: float = 0.0, o=None, lse=None,
@@ -211,18 +220,22 @@ def seer_block_sparse_decode_quant(q_tok, cache, mask, L: int, lens=None, softma
     _need(lse is None or (lse.dtype is _f32 and lse.shape == (cache.B, Hq) and lse.is_contiguous() and
                           lse.get_device() == dev), "lse must be contiguous fp32 [B,Hq] on the cache's device")
     lp = _per_sequence(cache, _LENS, lens)
+    if stream is not None or dev < 0 or dev != _current_device():
+        return _elsewhere(seer_block_sparse_decode_quant, dev, stream, q_tok, cache, mask, L, lens, softmax_scale, o, lse,
+                          return_lse, workspace)
+    if o is None:
+        o = torch.empty_like(q_tok)
+    if lse is None and return_lse:
+        lse = torch.empty(cache.B, Hq, dtype=_f32, device=cache.pages.device)
+    if workspace is None:
+        need = _attention_workspace(cache.B, Hq, cache.Hkv, cache.d)
+        workspace = cache.pages.new_empty(need)
+    else:
+        need = workspace.numel() * workspace.element_size()
     sh = B.seer_shape(cache.B, Hq, cache.Hkv, int(L), cache.d)
-
-    need = _attention_workspace(cache.B, Hq, cache.Hkv, cache.d)
-
-    def call(st):
-        out = torch.empty_like(q_tok) if o is None else o
-        ls = torch.empty(cache.B, Hq, dtype=_f32, device=cache.pages.device) if return_lse and lse is None else lse
-        ws = cache.pages.new_empty(need) if workspace is None else workspace
-        wsb = need if workspace is None else workspace.numel() * workspace.element_size()
-        _check((B._lib or lib()).seer_block_sparse_decode_quant(
-            _byref(sh), q_tok.data_ptr(), _byref(cache._c), lp, mask.data_ptr(), float(softmax_scale),
-            out.data_ptr(), None if ls is None else ls.data_ptr(), ws.data_ptr(), wsb, st))
-        return (out, ls) if ls is not None else out
-
-    return _on(dev, stream, call)
+    st = (B._lib or lib()).seer_block_sparse_decode_quant(
+        _byref(sh), q_tok.data_ptr(), _byref(cache._c), lp, mask.data_ptr(), float(softmax_scale), o.data_ptr(),
+        None if lse is None else lse.data_ptr(), workspace.data_ptr(), need, _current_stream(dev))
+    if st:
+        _check(st)
+    return o if lse is None else (o, lse)

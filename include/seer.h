@@ -425,7 +425,8 @@ SEER_API seer_status seer_gate_key_cache_quant(const seer_shape *shape, const se
  * cache: tokens below the sequence's length (lens as above) in its active
  * blocks.  q_tok, mask, softmax_scale, o and lse: as there (o = 0 and
  * lse = -inf where nothing is active).  The cache's values enter the products
- * unrounded.  Workspace: seer_workspace_bytes(SEER_CALL_BLOCK_SPARSE_DECODE_QUANT),
+ * unrounded, a probability times a scale with an error of at most 2^-16; a
+ * group's scale may be 2^100 below the largest that the head reads.  Workspace: seer_workspace_bytes(SEER_CALL_BLOCK_SPARSE_DECODE_QUANT),
  * 16-B aligned.
  */
 SEER_API seer_status seer_block_sparse_decode_quant(const seer_shape *shape, const void *q_tok,

@@ -14,15 +14,21 @@
 // way round (Sums<.., 16>).  Sixteen rows at most leave a tcgen05 tile nothing to
 // gain.
 //
-//  * The codes enter the MMA as they are: n <= 255 in the low bits of an fp16 is
-//    the subnormal n 2^-24, so one mask (4 bits) or byte permute (8 bits) makes
-//    a pair of operands, and scale and zero are applied outside:
+//  * The codes enter the MMA as they are: n <= 255 in the low bits of a bf16 is
+//    n 2^-133 (below 128 a subnormal, from there on the first binade, which has the
+//    same step), so one mask (4 bits) or byte permute (8 bits) makes a pair of
+//    operands, and scale and zero are applied outside:
 //      q . k   = sum_g s_g (q_g . n_g) + z_g sum(q_g)        per key; the second by an
 //                MMA of the params as they lie with sum(q_g) in three bf16 parts
-//      sum p v = sum_t (p_t s_t,g) n_t + sum_t p_t z_t,g      p s rounded to fp16
-//    q is exact in fp16 after a power of two per head; p s < 2^15 after a power
-//    of two that follows the largest scale seen (as a running maximum, so it
-//    holds for any range of V).  p z, the row sums and all accumulators are fp32.
+//      sum p v = sum_t (p_t s_t,g) (n_t - c) + sum_t p_t (z_t,g + c s_t,g)
+//    q is bf16 already, times a power of two per head: exact down to 2^-116 of the
+//    head's largest element.  p s is two bf16 parts, which leave at most 2^-16 of it
+//    (one fp16 leaves 2^-11 and has no room for scales 2^20 apart), times a power of two
+//    that follows the largest scale in the blocks that the head chose: the parts keep
+//    their bits down to 2^-100 of it, whatever other heads read.  c is the middle of the
+//    codes: without it the sum of p s n, some sqrt(tokens) times what is left after the
+//    zeros, loses as much more to the accumulators' rounding (16k tokens: 2^-13 of o).
+//    p z, the row sums and all accumulators are fp32.
 //  * The running maximum moves when a score is 2^6 above it, so the accumulators
 //    are rescaled a few times per warp, and p reaches 2^6 at most.
 //  * Work of a warp: half records of 32 tokens, each one contiguous bulk copy
@@ -40,7 +46,6 @@
 // end, some 8,000 cycles of latencies, and the join (32k at density 0.1: 10.8 us; 200
 // tokens: 4.6).
 #include <cuda_bf16.h>
-#include <cuda_fp16.h>
 
 #include "seer_internal.h"
 #include "seer_kv.cuh"
@@ -52,6 +57,12 @@ namespace {
 constexpr int kListMax = 513;             // blocks of a split (decode_quant_split)
 constexpr int kSlack = 6;                  // a maximum moves when a score is 2^kSlack above it
 constexpr int kNoPage = kMaxNb;           // flag of a list entry; block indices are below it
+// p s times scale_up(ve) is below 2^124 for scales whose exponent field is at
+// most ve; what the accumulators hold times kUnit and scale_un(ve) is in units of
+// V again.  ve is at least kLeastScale: p times scale_up stays a float.
+constexpr int kLeastScale = 124;
+constexpr int kSlackScale = 8;             // ve moves that much past a scale that is above it
+constexpr float kUnit = 18446744073709551616.f;   // 2^64 of the codes' 2^133
 
 __device__ __forceinline__ float exp2_approx(float x)
 {
@@ -63,7 +74,7 @@ __device__ __forceinline__ float exp2_approx(float x)
 __device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                          uint32_t b1)
 {
-    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
                  : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
                  : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
@@ -72,25 +83,9 @@ __device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1
 __device__ __forceinline__ void mma16816_0(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                            uint32_t b1)
 {
-    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
-        : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
-        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
-}
-
-__device__ __forceinline__ void mma16816_bf16_0(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
-                                                uint32_t b0, uint32_t b1)
-{
     asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
         : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
-}
-
-__device__ __forceinline__ void mma16816_bf16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
-                                              uint32_t b0, uint32_t b1)
-{
-    asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
-                 : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-                 : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
 __device__ __forceinline__ uint32_t movmatrix(uint32_t x)
@@ -100,14 +95,38 @@ __device__ __forceinline__ uint32_t movmatrix(uint32_t x)
     return y;
 }
 
-__device__ __forceinline__ uint32_t pack_half2(float lo, float hi)
+// Two values as kParts bf16 pairs each, every one the rounding of what the ones
+// before left: a part holds 8 bits, so two leave at most 2^-16 of a value.
+constexpr int kParts = 2;
+
+__device__ __forceinline__ void split(float x, float y, uint32_t (&part)[kParts])
 {
-    uint32_t r;
-    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
-    return r;
+#pragma unroll
+    for (int i = 0; i < kParts; ++i) {
+        asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(part[i]) : "f"(y), "f"(x));
+        if (i + 1 < kParts) {
+            x -= __uint_as_float(part[i] << 16);
+            y -= __uint_as_float(part[i] & 0xFFFF0000u);
+        }
+    }
 }
 
 __device__ __forceinline__ float pow2_field(int field) { return __uint_as_float((uint32_t)field << 23); }
+
+// Codes of V less the middle of their range (8 of 16, 128 of 256; the byte of two
+// 4-bit codes less 136), so that the accumulators hold what is about the size of
+// the result and not of sum p s n.  Exact: below 2^8 units.
+constexpr uint32_t kMid4 = 0x00080008u, kMidByte = 0x00880088u, kMid8 = 0x00800080u;
+
+__device__ __forceinline__ uint32_t less(uint32_t n, uint32_t mid)
+{
+    uint32_t r;
+    asm("sub.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(n), "r"(mid));
+    return r;
+}
+
+__device__ __forceinline__ float scale_up(int ve) { return pow2_field(371 - ve); }
+__device__ __forceinline__ float scale_un(int ve) { return pow2_field(127 + 133 - 64 - (371 - ve - 127)); }
 
 __device__ __forceinline__ void bulk_copy(uint32_t dst, const void *src, uint32_t bytes, uint32_t bar)
 {
@@ -157,7 +176,7 @@ __device__ __forceinline__ void load_words(uint32_t (&w)[N], const uint8_t *p)
 __device__ __forceinline__ int tile_token(int r) { return r ^ ((r >> 1) & 1); }
 
 // q for the MMAs: row gid of w holds head gid, or heads gid and gid + 8.  First
-// its elements in fp16 times 2^qe in the order of the codes' operands (at 4 bits
+// its elements (bf16) times 2^qe in the order of the codes' operands (at 4 bits
 // a word's elements 0,4,1,5,2,6,3,7 with the odd ones times 2^-4, as the codes'
 // masks give them), 16 bytes a lane at a time: two steps' B operands of eight
 // heads, one step's A operand of sixteen.  Then its group sums in three bf16
@@ -171,7 +190,7 @@ struct QShared {
     static constexpr int kSum = P * D / 2;
     static constexpr int LEN = kSum + P * 8 * STEPS;
     uint32_t w[H / P][LEN + (48 - LEN % 32) % 32];
-    float inv[H];                                   // 2^-qe
+    float inv[H];                                   // 2^(109 - qe)
 
     // Element e's half word.
     __device__ __forceinline__ static int at(int h, int e)
@@ -220,23 +239,22 @@ struct QShared {
 #pragma unroll
         for (int i = 0; i < N; ++i)
             mx = fmaxf(mx, fabsf(f[i]));
-        // max |q| 2^qe in [2^14, 2^15) where 2^qe is a float; no scaling for infinity
+        // max |q| 2^qe in [2^123, 2^124) where 2^qe is a float; no scaling for infinity
         const int eb = (int)(__reduce_max_sync(0xffffffffu, __float_as_uint(mx)) >> 23);
-        const int qe = eb == 255 ? 0 : min(141 - eb, 126);
-        const float up = pow2_field(127 + qe);
+        const int qe = eb == 255 ? 0 : min(250 - eb, 127);
+        const float up = pow2_field(127 + qe), up_sum = pow2_field(127 + qe - 109);
         uint32_t *row = w[h % 8];
         uint16_t *half = reinterpret_cast<uint16_t *>(row);
         float s = 0.f;
 #pragma unroll
         for (int i = 0; i < N; ++i) {
-            f[i] *= up;
-            s += f[i];
-            half[at(h, N * lane + i)] = __half_as_ushort(__float2half_rn(BITS == 4 && i & 1 ? f[i] * 0.0625f : f[i]));
+            s += f[i] * up_sum;
+            half[at(h, N * lane + i)] = (uint16_t)(__float_as_uint(f[i] * (BITS == 4 && i & 1 ? up * 0.0625f : up)) >> 16);
         }
 #pragma unroll
         for (int off = 1; off < GL; off <<= 1)
             s += __shfl_xor_sync(0xffffffffu, s, off);
-        s *= 5.9604644775390625e-8f;                // 2^-24: the unit of the codes' products
+        s *= 5.9604644775390625e-8f;                // 2^(qe - 109) 2^-24: the unit of the codes' products, 2^qe 2^-133
         if (lane % GL == 0)
 #pragma unroll
             for (int i = 0; i < kPlaces; ++i) {
@@ -245,7 +263,7 @@ struct QShared {
                 s -= __bfloat162float(part);
             }
         if (lane == 0)
-            inv[h] = pow2_field(127 - qe);
+            inv[h] = pow2_field(127 + 109 - qe);
     }
 };
 
@@ -365,6 +383,7 @@ template <int BITS, int D, int H>
 struct Sums {
     using F = KvFmt<BITS, D>;
     static constexpr int NG = F::NG, R = F::R;
+    static constexpr float kMid = BITS == 4 ? 8.f : 128.f;
     static constexpr int KS = D / 16;               // MMA steps of a score; also MMA rows of an output / 16
     static constexpr int KW = R / 16, VW = R / 32;  // 32-bit words of a lane's K row, V row
     static constexpr int UPG = KS / NG;             // MMAs of a group
@@ -373,7 +392,7 @@ struct Sums {
     using Q = QShared<BITS, D, H>;
 
     float m[2], l[2], zacc[NS][2], acc[KS][4], fac[2];
-    int ve;                                         // exponent field of V's largest scale so far
+    int ve[2];                                      // exponent field that V's scales stay within
     int gid, tig, tr, at_k, at_p, at_z, at_pv, at_v0, at_v1;
 
     __device__ __forceinline__ void clear()
@@ -392,7 +411,7 @@ struct Sums {
         for (int e = 0; e < 2; ++e)
             fac[e] = fminf(fmaxf(sq.inv[(2 * tig + e) & (H - 1)] * scale, 1.2e-38f), 3e38f);
         clear();
-        ve = 27;
+        ve[0] = ve[1] = kLeastScale;
 #pragma unroll
         for (int i = 0; i < KS; ++i)
             acc[i][0] = acc[i][1] = acc[i][2] = acc[i][3] = 0.f;
@@ -455,9 +474,9 @@ struct Sums {
 #pragma unroll
                 for (int i = 0; i < 4; ++i)
                     x[i] = *reinterpret_cast<const uint32_t *>(h + at_z + (16 * mt + 8 * (i & 1)) * F::PAR + Q::par_at(0, i >> 1));
-                mma16816_bf16_0(s[mt], x[0], x[1], x[2], x[3], qz[0], qz[1]);
+                mma16816_0(s[mt], x[0], x[1], x[2], x[3], qz[0], qz[1]);
                 if constexpr (Q::STEPS == 2)
-                    mma16816_bf16(s[mt], x[0], x[1], x[2], x[3], qz[2], qz[3]);
+                    mma16816(s[mt], x[0], x[1], x[2], x[3], qz[2], qz[3]);
             }
 #pragma unroll
             for (int gr = 0; gr < NG; ++gr) {
@@ -529,9 +548,6 @@ struct Sums {
             for (int gr = 0; gr + 1 < NS; gr += 2)
                 vmax = __vimax3_u16x2(vmax, vp[i / 2][i % 2][gr], vp[i / 2][i % 2][gr + 1]);
         }
-#pragma unroll
-        for (int off = H / 2; off < 4; off <<= 1)
-            vmax = __vmaxu2(vmax, __shfl_xor_sync(0xffffffffu, vmax, off));
         float mx[2];
 #pragma unroll
         for (int e = 0; e < 2; ++e)
@@ -540,25 +556,28 @@ struct Sums {
         for (int off = 4; off < 32; off <<= 1) {
             mx[0] = fmaxf(mx[0], __shfl_xor_sync(0xffffffffu, mx[0], off));
             mx[1] = fmaxf(mx[1], __shfl_xor_sync(0xffffffffu, mx[1], off));
-            vmax = __vmaxu2(vmax, __shfl_xor_sync(0xffffffffu, vmax, off));
         }
-        const int ve_new = max(ve, (int)(vmax >> 7 & 0xFFu));
-        // a head that left the block out: its maximum stays and its p are 0
+        // a head that left the block out: its maximum and power of two stay and its p are 0
         const bool more0 = act0 && (mx[0] - m[0]) * fac[0] > kSlack, more1 = act1 && (mx[1] - m[1]) * fac[1] > kSlack;
-        if (__any_sync(0xffffffffu, more0 || more1 || ve_new != ve)) {
-            float alpha[2];
+        int vm = (int)(vmax >> 7 & 0xFFu);             // of this lane's scales
+        if (__any_sync(0xffffffffu, more0 || more1 || (act0 && vm > ve[0]) || (act1 && vm > ve[1]))) {
+            vm = __reduce_max_sync(0xffffffffu, vm);
+            const bool over0 = act0 && vm > ve[0], over1 = act1 && vm > ve[1];
+            float alpha[2], down[2];
+            const int ve_new[2] = {over0 ? vm + kSlackScale : ve[0], over1 ? vm + kSlackScale : ve[1]};
             const float m_new[2] = {more0 ? mx[0] : m[0], more1 ? mx[1] : m[1]};
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
                 alpha[e] = m_new[e] == m[e] ? 1.f : exp2_approx((m[e] - m_new[e]) * fac[e]);
                 m[e] = m_new[e];
+                down[e] = alpha[e] * (ve[e] - ve_new[e] > -127 ? pow2_field(127 + ve[e] - ve_new[e]) : 0.f);
+                ve[e] = ve_new[e];
             }
-            const float down = ve - ve_new > -127 ? pow2_field(127 + ve - ve_new) : 0.f;
 #pragma unroll
             for (int i = 0; i < KS; ++i)
 #pragma unroll
                 for (int e = 0; e < 4; ++e)
-                    acc[i][e] *= alpha[e & 1] * down;
+                    acc[i][e] *= down[e & 1];
 #pragma unroll
             for (int gr = 0; gr < NS; ++gr) {
                 zacc[gr][0] *= alpha[0];
@@ -566,10 +585,9 @@ struct Sums {
             }
             l[0] *= alpha[0];
             l[1] *= alpha[1];
-            ve = ve_new;
         }
         const float mu[2] = {m[0] == -INFINITY ? 0.f : -m[0] * fac[0], m[1] == -INFINITY ? 0.f : -m[1] * fac[1]};
-        const float up = pow2_field(268 - kSlack - ve);        // 2^(14 - kSlack) over the power of two below the largest scale
+        const float up[2] = {scale_up(ve[0]), scale_up(ve[1])};
 
         // ---- P V
 #pragma unroll
@@ -594,13 +612,19 @@ struct Sums {
             float pu[4];
 #pragma unroll
             for (int e = 0; e < 4; ++e)
-                pu[e] = p[e] * up;
+                pu[e] = p[e] * up[e & 1];
 #pragma unroll
             for (int j = 0; j < NS; ++j) {
                 const float sa = kv_scale(vp[mt][0][j]), sb = kv_scale(vp[mt][1][j]);
-                const float za = kv_zero(vp[mt][0][j]), zb = kv_zero(vp[mt][1][j]);
-                const uint32_t b0 = movmatrix(pack_half2(pu[0] * sa, pu[1] * sa));
-                const uint32_t b1 = movmatrix(pack_half2(pu[2] * sb, pu[3] * sb));
+                const float za = fmaf(kMid, sa, kv_zero(vp[mt][0][j])), zb = fmaf(kMid, sb, kv_zero(vp[mt][1][j]));
+                uint32_t b0[kParts], b1[kParts];
+                split(pu[0] * sa, pu[1] * sa, b0);
+                split(pu[2] * sb, pu[3] * sb, b1);
+#pragma unroll
+                for (int k = 0; k < kParts; ++k) {
+                    b0[k] = movmatrix(b0[k]);
+                    b1[k] = movmatrix(b1[k]);
+                }
                 if (act0)                           // a NaN of V stays out of heads that left the block out
                     zacc[j][0] = fmaf(p[0], za, fmaf(p[2], zb, zacc[j][0]));
                 if (act1)
@@ -616,7 +640,11 @@ struct Sums {
                         for (int i = 0; i < UPG; ++i) {
                             const uint32_t y01 = i ? __byte_perm(x01, 0u, 0x4341) : x01 & 0x00FF00FFu;
                             const uint32_t y23 = i ? __byte_perm(x23, 0u, 0x4341) : x23 & 0x00FF00FFu;
-                            mma16816(acc[gr * UPG + i], y01 & 0x000F000Fu, y01, y23 & 0x000F000Fu, y23, b0, b1);
+                            const uint32_t n0 = less(y01 & 0x000F000Fu, kMid4), n1 = less(y01, kMidByte);
+                            const uint32_t n2 = less(y23 & 0x000F000Fu, kMid4), n3 = less(y23, kMidByte);
+#pragma unroll
+                            for (int k = 0; k < kParts; ++k)
+                                mma16816(acc[gr * UPG + i], n0, n1, n2, n3, b0[k], b1[k]);
                         }
                     } else {
 #pragma unroll
@@ -624,8 +652,11 @@ struct Sums {
                             const int w = 2 * gr + i / 2;
                             const unsigned sel = i & 1 ? 0x7632u : 0x5410u;
                             const uint32_t x01 = __byte_perm(v0[w], v1[w], sel), x23 = __byte_perm(v2[w], v3[w], sel);
-                            mma16816(acc[gr * UPG + i], __byte_perm(x01, 0u, 0x4240), __byte_perm(x01, 0u, 0x4341),
-                                     __byte_perm(x23, 0u, 0x4240), __byte_perm(x23, 0u, 0x4341), b0, b1);
+                            const uint32_t n0 = less(__byte_perm(x01, 0u, 0x4240), kMid8), n1 = less(__byte_perm(x01, 0u, 0x4341), kMid8);
+                            const uint32_t n2 = less(__byte_perm(x23, 0u, 0x4240), kMid8), n3 = less(__byte_perm(x23, 0u, 0x4341), kMid8);
+#pragma unroll
+                            for (int k = 0; k < kParts; ++k)
+                                mma16816(acc[gr * UPG + i], n0, n1, n2, n3, b0[k], b1[k]);
                         }
                     }
                 }
@@ -650,9 +681,9 @@ struct Sums {
             ml[h] = make_float2(m[0] == -INFINITY ? m[0] : m[0] * fac[0], l[0]);
             ml[h + 1] = make_float2(m[1] == -INFINITY ? m[1] : m[1] * fac[1], l[1]);
         }
-        const float un = pow2_field(ve - 14 + kSlack);       // with 2^24 the inverse of `up` and the codes' unit
 #pragma unroll
-        for (int e = 0; e < 2; ++e)
+        for (int e = 0; e < 2; ++e) {
+            const float un = scale_un(ve[e]);
 #pragma unroll
             for (int j = 0; j < NS; ++j)
 #pragma unroll
@@ -666,12 +697,13 @@ struct Sums {
                             lo = place == r ? acc[(r * NS + j) * UPG + i + k][e] : lo;
                             hi = place == r ? acc[(r * NS + j) * UPG + i + k][e + 2] : hi;
                         }
-                        v[2 * k] = lo * un * 16777216.f + zacc[j][e];
-                        v[2 * k + 1] = (BITS == 4 ? (hi - lo) * un * 1048576.f : hi * un * 16777216.f) + zacc[j][e];
+                        v[2 * k] = lo * kUnit * un + zacc[j][e];
+                        v[2 * k + 1] = (BITS == 4 ? (hi - lo) * (kUnit * 0.0625f) : hi * kUnit) * un + zacc[j][e];
                     }
                     const float4 r = make_float4(v[0], v[1], v[2], v[3]);
                     *reinterpret_cast<float4 *>(so + (h + e) * D + F::G * (place * NS + j) + gid * (F::G / 8) + 2 * i) = r;
                 }
+        }
     }
 };
 
@@ -684,10 +716,11 @@ struct Sums<BITS, D, 16> {
     using F = KvFmt<BITS, D>;
     using Q = QShared<BITS, D, 16>;
     static constexpr int NG = F::NG, R = F::R;
+    static constexpr float kMid = BITS == 4 ? 8.f : 128.f;
     static constexpr int KS = D / 16, KW = R / 16, VW = R / 32, UPG = KS / NG;
 
     float m[2], l[2], zacc[NG][2], acc[KS][2][4], fac[2];
-    int ve;                                         // exponent field of V's largest scale so far
+    int ve[2], ve_least;                            // exponent field that V's scales stay within; of all heads
     int lane, gid, tig, t0, t1, at_k, at_z, at_v0, at_v1;
 
     __device__ __forceinline__ void clear()
@@ -705,7 +738,7 @@ struct Sums<BITS, D, 16> {
         for (int hh = 0; hh < 2; ++hh)
             fac[hh] = fminf(fmaxf(sq.inv[gid + 8 * hh] * scale, 1.2e-38f), 3e38f);
         clear();
-        ve = 27;
+        ve[0] = ve[1] = ve_least = kLeastScale;
 #pragma unroll
         for (int i = 0; i < KS; ++i)
 #pragma unroll
@@ -758,9 +791,9 @@ struct Sums<BITS, D, 16> {
                     else
                         load_words(w, at);
                     if (st == 0)
-                        mma16816_bf16_0(s[mt][nt], x.x, x.y, x.z, x.w, w[0], w[1]);
+                        mma16816_0(s[mt][nt], x.x, x.y, x.z, x.w, w[0], w[1]);
                     else
-                        mma16816_bf16(s[mt][nt], x.x, x.y, x.z, x.w, w[0], w[1]);
+                        mma16816(s[mt][nt], x.x, x.y, x.z, x.w, w[0], w[1]);
                 }
             }
             uint32_t par[4][NG];                    // of this lane's keys 2 tig, 2 tig + 1 and 8 further
@@ -825,7 +858,7 @@ struct Sums<BITS, D, 16> {
 #pragma unroll
             for (int gr = 0; gr < NG; ++gr)
                 vmax = __vmaxu2(vmax, w[gr]);
-            vmax = __reduce_max_sync(0xffffffffu, lane < keys ? vmax & 0xFFFFu : 0u);
+            vmax = lane < keys ? vmax : 0u;
         }
         float mx[2];
 #pragma unroll
@@ -840,24 +873,28 @@ struct Sums<BITS, D, 16> {
             mx[0] = fmaxf(mx[0], __shfl_xor_sync(0xffffffffu, mx[0], off));
             mx[1] = fmaxf(mx[1], __shfl_xor_sync(0xffffffffu, mx[1], off));
         }
-        const int ve_new = max(ve, (int)(vmax >> 7));
-        // a head that left the block out: its maximum stays and its p are 0
+        // a head that left the block out: its maximum and power of two stay and its p are 0
         const bool more0 = act0 && (mx[0] - m[0]) * fac[0] > kSlack, more1 = act1 && (mx[1] - m[1]) * fac[1] > kSlack;
-        if (__any_sync(0xffffffffu, more0 || more1 || ve_new != ve)) {
-            float alpha[2];
+        int vm = (int)(vmax >> 7 & 0xFFu);             // of this lane's token
+        if (__any_sync(0xffffffffu, more0 || more1 || vm > ve_least)) {
+            vm = __reduce_max_sync(0xffffffffu, vm);
+            const bool over0 = act0 && vm > ve[0], over1 = act1 && vm > ve[1];
+            float alpha[2], down[2];
+            const int ve_new[2] = {over0 ? vm + kSlackScale : ve[0], over1 ? vm + kSlackScale : ve[1]};
             const float m_new[2] = {more0 ? mx[0] : m[0], more1 ? mx[1] : m[1]};
 #pragma unroll
             for (int hh = 0; hh < 2; ++hh) {
                 alpha[hh] = m_new[hh] == m[hh] ? 1.f : exp2_approx((m[hh] - m_new[hh]) * fac[hh]);
                 m[hh] = m_new[hh];
+                down[hh] = alpha[hh] * (ve[hh] - ve_new[hh] > -127 ? pow2_field(127 + ve[hh] - ve_new[hh]) : 0.f);
+                ve[hh] = ve_new[hh];
             }
-            const float down = ve - ve_new > -127 ? pow2_field(127 + ve - ve_new) : 0.f;
 #pragma unroll
             for (int i = 0; i < KS; ++i)
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
-                    acc[i][0][e] *= alpha[e >> 1] * down;
-                    acc[i][1][e] *= alpha[e >> 1] * down;
+                    acc[i][0][e] *= down[e >> 1];
+                    acc[i][1][e] *= down[e >> 1];
                 }
 #pragma unroll
             for (int gr = 0; gr < NG; ++gr) {
@@ -866,10 +903,10 @@ struct Sums<BITS, D, 16> {
             }
             l[0] *= alpha[0];
             l[1] *= alpha[1];
-            ve = ve_new;
+            ve_least = __reduce_min_sync(0xffffffffu, min(ve[0], ve[1]));
         }
         const float mu[2] = {m[0] == -INFINITY ? 0.f : -m[0] * fac[0], m[1] == -INFINITY ? 0.f : -m[1] * fac[1]};
-        const float up = pow2_field(268 - kSlack - ve);        // 2^(14 - kSlack) over the power of two below the largest scale
+        const float up[2] = {scale_up(ve[0]), scale_up(ve[1])};
 
         // ---- P V
 #pragma unroll
@@ -890,7 +927,7 @@ struct Sums<BITS, D, 16> {
                 l[1] += p[nt][2] + p[nt][3];
 #pragma unroll
                 for (int e = 0; e < 4; ++e)
-                    pu[nt][e] = p[nt][e] * up;
+                    pu[nt][e] = p[nt][e] * up[e >> 1];
             }
             uint32_t par[4][NG], v0[VW], v1[VW], v2[VW], v3[VW];
 #pragma unroll
@@ -911,13 +948,13 @@ struct Sums<BITS, D, 16> {
             load_words(v3, h + at_v1 + (16 * mt + 8) * R);
 #pragma unroll
             for (int gr = 0; gr < NG; ++gr) {
-                uint32_t a[4];
+                uint32_t a[4][kParts];
 #pragma unroll
                 for (int nt = 0; nt < 2; ++nt) {
                     const float sa = kv_scale(par[2 * nt][gr]), sb = kv_scale(par[2 * nt + 1][gr]);
-                    const float za = kv_zero(par[2 * nt][gr]), zb = kv_zero(par[2 * nt + 1][gr]);
-                    a[2 * nt] = pack_half2(pu[nt][0] * sa, pu[nt][1] * sb);
-                    a[2 * nt + 1] = pack_half2(pu[nt][2] * sa, pu[nt][3] * sb);
+                    const float za = fmaf(kMid, sa, kv_zero(par[2 * nt][gr])), zb = fmaf(kMid, sb, kv_zero(par[2 * nt + 1][gr]));
+                    split(pu[nt][0] * sa, pu[nt][1] * sb, a[2 * nt]);
+                    split(pu[nt][2] * sa, pu[nt][3] * sb, a[2 * nt + 1]);
                     if (act0)                       // a NaN of V stays out of heads that left the block out
                         zacc[gr][0] = fmaf(p[nt][0], za, fmaf(p[nt][1], zb, zacc[gr][0]));
                     if (act1)
@@ -931,8 +968,13 @@ struct Sums<BITS, D, 16> {
                     for (int i = 0; i < UPG; ++i) {
                         const uint32_t y01 = i ? __byte_perm(x01, 0u, 0x4341) : x01 & 0x00FF00FFu;
                         const uint32_t y23 = i ? __byte_perm(x23, 0u, 0x4341) : x23 & 0x00FF00FFu;
-                        mma16816(acc[gr * UPG + i][0], a[0], a[1], a[2], a[3], y01 & 0x000F000Fu, y23 & 0x000F000Fu);
-                        mma16816(acc[gr * UPG + i][1], a[0], a[1], a[2], a[3], y01, y23);
+                        const uint32_t n0 = less(y01 & 0x000F000Fu, kMid4), n1 = less(y01, kMidByte);
+                        const uint32_t n2 = less(y23 & 0x000F000Fu, kMid4), n3 = less(y23, kMidByte);
+#pragma unroll
+                        for (int k = 0; k < kParts; ++k) {
+                            mma16816(acc[gr * UPG + i][0], a[0][k], a[1][k], a[2][k], a[3][k], n0, n2);
+                            mma16816(acc[gr * UPG + i][1], a[0][k], a[1][k], a[2][k], a[3][k], n1, n3);
+                        }
                     }
                 } else {
 #pragma unroll
@@ -940,10 +982,13 @@ struct Sums<BITS, D, 16> {
                         const int w = 2 * gr + i / 2;
                         const unsigned sel = i & 1 ? 0x7632u : 0x5410u;
                         const uint32_t x01 = __byte_perm(v0[w], v1[w], sel), x23 = __byte_perm(v2[w], v3[w], sel);
-                        mma16816(acc[gr * UPG + i][0], a[0], a[1], a[2], a[3], __byte_perm(x01, 0u, 0x4240),
-                                 __byte_perm(x23, 0u, 0x4240));
-                        mma16816(acc[gr * UPG + i][1], a[0], a[1], a[2], a[3], __byte_perm(x01, 0u, 0x4341),
-                                 __byte_perm(x23, 0u, 0x4341));
+                        const uint32_t n0 = less(__byte_perm(x01, 0u, 0x4240), kMid8), n1 = less(__byte_perm(x01, 0u, 0x4341), kMid8);
+                        const uint32_t n2 = less(__byte_perm(x23, 0u, 0x4240), kMid8), n3 = less(__byte_perm(x23, 0u, 0x4341), kMid8);
+#pragma unroll
+                        for (int k = 0; k < kParts; ++k) {
+                            mma16816(acc[gr * UPG + i][0], a[0][k], a[1][k], a[2][k], a[3][k], n0, n2);
+                            mma16816(acc[gr * UPG + i][1], a[0][k], a[1][k], a[2][k], a[3][k], n1, n3);
+                        }
                     }
                 }
             }
@@ -966,9 +1011,9 @@ struct Sums<BITS, D, 16> {
             ml[gid] = make_float2(m[0] == -INFINITY ? m[0] : m[0] * fac[0], l[0]);
             ml[gid + 8] = make_float2(m[1] == -INFINITY ? m[1] : m[1] * fac[1], l[1]);
         }
-        const float un = pow2_field(ve - 14 + kSlack);       // with 2^24 the inverse of `up` and the codes' unit
 #pragma unroll
-        for (int hh = 0; hh < 2; ++hh)
+        for (int hh = 0; hh < 2; ++hh) {
+            const float un = scale_un(ve[hh]);
 #pragma unroll
             for (int e = 0; e < 2; ++e)
 #pragma unroll
@@ -979,12 +1024,13 @@ struct Sums<BITS, D, 16> {
 #pragma unroll
                         for (int k = 0; k < 2; ++k) {
                             const float lo = acc[gr * UPG + i + k][0][2 * hh + e], hi = acc[gr * UPG + i + k][1][2 * hh + e];
-                            v[2 * k] = lo * un * 16777216.f + zacc[gr][hh];
-                            v[2 * k + 1] = (BITS == 4 ? (hi - lo) * un * 1048576.f : hi * un * 16777216.f) + zacc[gr][hh];
+                            v[2 * k] = lo * kUnit * un + zacc[gr][hh];
+                            v[2 * k + 1] = (BITS == 4 ? (hi - lo) * (kUnit * 0.0625f) : hi * kUnit) * un + zacc[gr][hh];
                         }
                         *reinterpret_cast<float4 *>(so + (gid + 8 * hh) * D + F::G * gr + (2 * tig + e) * (F::G / 8) + 2 * i) =
                             make_float4(v[0], v[1], v[2], v[3]);
                     }
+        }
     }
 };
 

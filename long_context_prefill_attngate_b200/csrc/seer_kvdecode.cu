@@ -30,7 +30,7 @@
 //    zeros, loses as much more to the accumulators' rounding (16k tokens: 2^-13 of o).
 //    p z, the row sums and all accumulators are fp32.
 //  * The running maximum moves when a score is 2^6 above it, so the accumulators
-//    are rescaled a few times per warp, and p reaches 2^6 at most.
+//    are rescaled a few times per warp; p is 2^-26 at the maximum and reaches 2^-20.
 //  * Work of a warp: half records of 32 tokens, each one contiguous bulk copy
 //    into the warp's own ring, so no warp waits for another until the end.
 //  * P leaves K Q^T with keys across lanes and enters V^T P with keys across a
@@ -56,11 +56,14 @@ namespace {
 
 constexpr int kListMax = 513;             // blocks of a split (decode_quant_split)
 constexpr int kSlack = 6;                  // a maximum moves when a score is 2^kSlack above it
+// p is 2^-kTop at the running maximum, so at most 2^-20: 2^20 tokens of values below
+// 2^126 sum up within fp32.
+constexpr float kTop = 26.f;
 constexpr int kNoPage = kMaxNb;           // flag of a list entry; block indices are below it
 // p s times scale_up(ve) is below 2^124 for scales whose exponent field is at
 // most ve; what the accumulators hold times kUnit and scale_un(ve) is in units of
 // V again.  ve is at least kLeastScale: p times scale_up stays a float.
-constexpr int kLeastScale = 124;
+constexpr int kLeastScale = 143;
 constexpr int kSlackScale = 8;             // ve moves that much past a scale that is above it
 constexpr float kUnit = 18446744073709551616.f;   // 2^64 of the codes' 2^133
 
@@ -125,8 +128,8 @@ __device__ __forceinline__ uint32_t less(uint32_t n, uint32_t mid)
     return r;
 }
 
-__device__ __forceinline__ float scale_up(int ve) { return pow2_field(371 - ve); }
-__device__ __forceinline__ float scale_un(int ve) { return pow2_field(127 + 133 - 64 - (371 - ve - 127)); }
+__device__ __forceinline__ float scale_up(int ve) { return pow2_field(397 - ve); }
+__device__ __forceinline__ float scale_un(int ve) { return pow2_field(127 + 133 - 64 - (397 - ve - 127)); }
 
 __device__ __forceinline__ void bulk_copy(uint32_t dst, const void *src, uint32_t bytes, uint32_t bar)
 {
@@ -142,10 +145,10 @@ __device__ __forceinline__ float split_weight(float m, float l, float M)
     return m == -INFINITY ? (l == 0.f ? 0.f : l) : exp2_approx(m - M);
 }
 
-// Natural log of l 2^M; -inf where nothing was active.
+// Natural log of l 2^M; -inf where nothing was active.  (l is at least 2^-kTop.)
 __device__ __forceinline__ float log_sum(float M, float l)
 {
-    return l == 0.f ? -INFINITY : ((M == -INFINITY ? 0.f : M) + __log2f(l)) * 0.69314718055994530942f;
+    return l == 0.f ? -INFINITY : ((M == -INFINITY ? 0.f : M - kTop) + __log2f(l * 67108864.f)) * 0.69314718055994530942f;
 }
 
 template <int N>
@@ -586,7 +589,8 @@ struct Sums {
             l[0] *= alpha[0];
             l[1] *= alpha[1];
         }
-        const float mu[2] = {m[0] == -INFINITY ? 0.f : -m[0] * fac[0], m[1] == -INFINITY ? 0.f : -m[1] * fac[1]};
+        const float mu[2] = {m[0] == -INFINITY ? 0.f : fmaf(-m[0], fac[0], -kTop),
+                             m[1] == -INFINITY ? 0.f : fmaf(-m[1], fac[1], -kTop)};
         const float up[2] = {scale_up(ve[0]), scale_up(ve[1])};
 
         // ---- P V
@@ -678,8 +682,8 @@ struct Sums {
                     zacc[j][e] += __shfl_xor_sync(0xffffffffu, zacc[j][e], off);
             }
         if (gid == 0 && place == 0) {
-            ml[h] = make_float2(m[0] == -INFINITY ? m[0] : m[0] * fac[0], l[0]);
-            ml[h + 1] = make_float2(m[1] == -INFINITY ? m[1] : m[1] * fac[1], l[1]);
+            ml[h] = make_float2(m[0] == -INFINITY ? m[0] : fmaf(m[0], fac[0], kTop), l[0]);
+            ml[h + 1] = make_float2(m[1] == -INFINITY ? m[1] : fmaf(m[1], fac[1], kTop), l[1]);
         }
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
@@ -905,7 +909,8 @@ struct Sums<BITS, D, 16> {
             l[1] *= alpha[1];
             ve_least = __reduce_min_sync(0xffffffffu, min(ve[0], ve[1]));
         }
-        const float mu[2] = {m[0] == -INFINITY ? 0.f : -m[0] * fac[0], m[1] == -INFINITY ? 0.f : -m[1] * fac[1]};
+        const float mu[2] = {m[0] == -INFINITY ? 0.f : fmaf(-m[0], fac[0], -kTop),
+                             m[1] == -INFINITY ? 0.f : fmaf(-m[1], fac[1], -kTop)};
         const float up[2] = {scale_up(ve[0]), scale_up(ve[1])};
 
         // ---- P V
@@ -1008,8 +1013,8 @@ struct Sums<BITS, D, 16> {
                     zacc[gr][hh] += __shfl_xor_sync(0xffffffffu, zacc[gr][hh], off);
             }
         if (tig == 0) {
-            ml[gid] = make_float2(m[0] == -INFINITY ? m[0] : m[0] * fac[0], l[0]);
-            ml[gid + 8] = make_float2(m[1] == -INFINITY ? m[1] : m[1] * fac[1], l[1]);
+            ml[gid] = make_float2(m[0] == -INFINITY ? m[0] : fmaf(m[0], fac[0], kTop), l[0]);
+            ml[gid + 8] = make_float2(m[1] == -INFINITY ? m[1] : fmaf(m[1], fac[1], kTop), l[1]);
         }
 #pragma unroll
         for (int hh = 0; hh < 2; ++hh) {

@@ -50,12 +50,11 @@ def ones(B, Hq, L):
 @pytest.mark.parametrize("bits,d", FORMATS)
 @pytest.mark.parametrize("B,Hq", HEADS)
 def test_probabilities_keep_their_bits(bits, d, B, Hq):
-    """Every element's value is 0 (z = -1, s n = 1), so o is what the rounding of p s leaves: tokens of equal
-    probability, a third of the largest, all rounded the same way."""
-    L = 450
+    """Every element's value is 0 (z = -1, s n = 1), so o is what the rounding of p s leaves: 31 tokens of 32 have p of
+    1/2 + 2^-12 of the others', the middle of two numbers of 11 bits, all rounded the same way."""
+    L, scale = 450, -float(np.log(0.5 + 2.0 ** -12))
     k = torch.zeros((1, 1, L, d))
-    k[0, 0, :, 0] = 1.0
-    k[0, 0, 100, 0] = 2.0                                   # e times the others: p = 0.3679
+    k[0, 0, :, 0] = -(torch.arange(L) % 32 != 5).float()
     q = torch.zeros((B, Hq, d))
     q[..., 0] = 1.0
     v = torch.zeros((1, 1, L, d))
@@ -63,9 +62,9 @@ def test_probabilities_keep_their_bits(bits, d, B, Hq):
     v[..., 1::32] = 2.0 ** bits - 2
     k, v, q = (x.to(torch.bfloat16) for x in (k, v, q))
     mask = ones(B, Hq, L)
-    o, lse, kv = run(bits, d, B, Hq, k, v, q, mask, 1.0)
+    o, lse, kv = run(bits, d, B, Hq, k, v, q, mask, scale)
     assert np.all(kv[1][1][:, :, :L] == 1.0)
-    check(o, lse, q, kv, mask, [L] * B, (0, B - 1), 1.0)
+    check(o, lse, q, kv, mask, [L] * B, (0, B - 1), scale)
 
 
 @pytest.mark.parametrize("bits,d", [(4, 128), (4, 64), (8, 128)])
@@ -83,13 +82,13 @@ def test_groups_of_a_row_far_apart(bits, d, B, Hq, apart):
 
 @pytest.mark.parametrize("bits,d", FORMATS)
 @pytest.mark.parametrize("B,Hq", HEADS)
-@pytest.mark.parametrize("apart", [26, 40, 110])
+@pytest.mark.parametrize("apart", [26, 40, 110, 180])
 def test_block_of_large_values_that_other_heads_leave_out(bits, d, B, Hq, apart):
     """V of one block 2^apart times the others; every other head leaves it out, and its result is the ordinary one."""
     L = 450
     k, v, q = bf16((1, 1, L, d), 1), bf16((1, 1, L, d), 2).float(), bf16((B, Hq, d), 3)
-    v *= 2.0 ** -60
-    v[:, :, 128:192] *= 2.0 ** apart
+    block = torch.arange(L) // 64 == 2
+    v *= torch.where(block, 2.0 ** (apart - 60), 2.0 ** -60).view(1, 1, L, 1)
     mask = ones(B, Hq, L)
     mask[:, 1::2, 2] = 0
     o, lse, kv = run(bits, d, B, Hq, k, v.to(torch.bfloat16), q, mask)
@@ -135,3 +134,21 @@ def test_q_elements_far_apart(bits, d, B, Hq, apart):
     mask = ones(B, Hq, L)
     o, lse, kv = run(bits, d, B, Hq, k, v, q, mask)
     check(o, lse, q, kv, mask, [L] * B, (0, B - 1))
+
+
+@pytest.mark.parametrize("bits,d", FORMATS)
+@pytest.mark.parametrize("Hq", [2, 4, 8, 16])
+def test_values_near_the_largest_with_scores_that_rise(bits, d, Hq):
+    """V of 2^125 at a late token whose score is the largest, 20 times the first ones': a weighted sum that is in
+    fp32's range stays there."""
+    B, L = 150, 1500
+    k, v = torch.zeros((1, 1, L, d)), bf16((1, 1, L, d), 2).float()
+    k[0, 0, 1400, 0] = 3.0
+    v[0, 0, 1400] = 2.0 ** 125
+    v[0, 0, 1400, 1::2] = -2.0 ** 125
+    q = torch.zeros((B, Hq, d))
+    q[..., 0] = 1.0
+    k, v, q = (x.to(torch.bfloat16) for x in (k, v, q))
+    mask = ones(B, Hq, L)
+    o, lse, kv = run(bits, d, B, Hq, k, v, q, mask, 1.0)
+    check(o, lse, q, kv, mask, [L] * B, (0, B - 1), 1.0)

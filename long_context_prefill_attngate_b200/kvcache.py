@@ -219,6 +219,8 @@ def seer_block_sparse_decode_quant(q_tok, cache, mask, L: int, lens=None, softma
           "o must be contiguous bf16 [B,Hq,d] on the cache's device")
     _need(lse is None or (lse.dtype is _f32 and lse.shape == (cache.B, Hq) and lse.is_contiguous() and
                           lse.get_device() == dev), "lse must be contiguous fp32 [B,Hq] on the cache's device")
+    _need(workspace is None or (workspace.is_contiguous() and workspace.get_device() == dev),
+          "workspace must be contiguous on the cache's device")
     lp = _per_sequence(cache, _LENS, lens)
     if stream is not None or dev < 0 or dev != _current_device():
         return _elsewhere(seer_block_sparse_decode_quant, dev, stream, q_tok, cache, mask, L, lens, softmax_scale, o, lse,

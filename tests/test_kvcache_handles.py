@@ -1,0 +1,20 @@
+"""What the quantised-cache calls refuse of the handles that they are given, on
+the CPU: nothing here launches a kernel."""
+import pytest
+import torch
+
+import long_context_prefill_attngate_b200 as seer
+
+
+@pytest.fixture
+def cache():
+    return seer.SeerKVCache.empty(2, 2, 200, 128, bits=4, device="cpu")
+
+
+def test_workspace_is_checked_like_every_other_tensor(cache):
+    q, m = torch.zeros((2, 4, 128), dtype=torch.bfloat16), torch.zeros((2, 4, 4), dtype=torch.uint8)
+    need = seer.seer_workspace_bytes(seer.SEER_CALL_BLOCK_SPARSE_DECODE_QUANT, seer.seer_shape(2, 4, 2, 200, 128))
+    with pytest.raises(ValueError, match="workspace"):
+        seer.seer_block_sparse_decode_quant(q, cache, m, 200, workspace=torch.empty(2 * need, dtype=torch.uint8)[::2])
+    with pytest.raises(ValueError, match="CUDA"):           # a good one: the cache is what is refused
+        seer.seer_block_sparse_decode_quant(q, cache, m, 200, workspace=torch.empty(need, dtype=torch.uint8))

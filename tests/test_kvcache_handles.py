@@ -18,3 +18,18 @@ def test_workspace_is_checked_like_every_other_tensor(cache):
         seer.seer_block_sparse_decode_quant(q, cache, m, 200, workspace=torch.empty(2 * need, dtype=torch.uint8)[::2])
     with pytest.raises(ValueError, match="CUDA"):           # a good one: the cache is what is refused
         seer.seer_block_sparse_decode_quant(q, cache, m, 200, workspace=torch.empty(need, dtype=torch.uint8))
+
+
+@pytest.mark.parametrize("name", ["pages", "block_table", "d", "bits", "Hkv", "B", "max_blocks"])
+def test_a_cache_keeps_its_tensors_and_sizes(name):
+    """The calls hold the tensors' addresses: what they were made from is not exchanged behind them."""
+    pages = torch.zeros((8, 2, seer.seer_kv_record_bytes(4, 128)), dtype=torch.uint8)
+    table = torch.arange(8, dtype=torch.int32).view(2, 4)
+    c = seer.SeerKVCache(pages, 128, 4, block_table=table)
+    was = getattr(c, name)
+    with pytest.raises(AttributeError):
+        setattr(c, name, {"pages": pages.clone(), "block_table": table.flip(1)}.get(name, 64))
+    assert getattr(c, name) is was
+    assert c.pages is pages and c.block_table is table and (c.d, c.bits, c.Hkv, c.B, c.max_blocks) == (128, 4, 2, 2, 4)
+    c.block_table[0, 0] = 7                                 # their contents may change
+    assert table[0, 0] == 7

@@ -192,6 +192,8 @@ def seer_gate_key_cache_quant(cache, wk, L: int, kt=None, first_block: int = 0, 
     dg = ws[-1]
     if wk_head_stride is None:
         wk_head_stride = 0 if len(ws) == 2 else dk * dg
+    _need(0 <= wk_head_stride and (cache._Hkv - 1) * wk_head_stride + dk * dg <= wk.numel(),
+          "wk_head_stride leads out of wk")
     shape = (cache._B, cache._Hkv, -(-L // B.BLOCK), dg)
     _need(kt is None or (kt.dtype is _f32 and kt.shape == shape and kt.is_contiguous() and kt.get_device() == dev),
           "kt must be contiguous fp32 [B,Hkv,nb,d_gate] on the cache's device")

@@ -33,3 +33,17 @@ def test_a_cache_keeps_its_tensors_and_sizes(name):
     assert c.pages is pages and c.block_table is table and (c.d, c.bits, c.Hkv, c.B, c.max_blocks) == (128, 4, 2, 2, 4)
     c.block_table[0, 0] = 7                                 # their contents may change
     assert table[0, 0] == 7
+
+
+@pytest.mark.parametrize("shape,stride", [((128, 64), 128 * 64), ((2, 128, 64), 2 * 128 * 64), ((2, 128, 64), 128 * 64 + 1),
+                                          ((2, 128, 64), -8)])
+def test_a_head_stride_that_leads_out_of_the_weights_is_refused(cache, shape, stride):
+    wk = torch.zeros(shape, dtype=torch.bfloat16)
+    with pytest.raises(ValueError, match="wk_head_stride"):
+        seer.seer_gate_key_cache_quant(cache, wk, 200, wk_head_stride=stride)
+
+
+@pytest.mark.parametrize("stride", [0, 64, 128 * 64])
+def test_a_head_stride_within_the_weights_is_taken(cache, stride):
+    with pytest.raises(ValueError, match="CUDA"):           # the cache is what is refused
+        seer.seer_gate_key_cache_quant(cache, torch.zeros((2, 128, 64), dtype=torch.bfloat16), 200, wk_head_stride=stride)

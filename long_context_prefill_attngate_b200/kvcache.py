@@ -99,6 +99,7 @@ def _elsewhere(fn, dev: int, stream, *args):
     """fn(*args) with device `dev` current and, if a stream is given, that stream current too: what torch allocates
     then belongs to the stream that uses it."""
     _need(dev >= 0, "the cache must be on a CUDA device")
+    _need(getattr(stream, "device_index", dev) == dev, "the stream must be on the cache's device")
     with torch.cuda.device(dev):
         if stream is None:
             return fn(*args)

@@ -47,3 +47,14 @@ def test_a_head_stride_that_leads_out_of_the_weights_is_refused(cache, shape, st
 def test_a_head_stride_within_the_weights_is_taken(cache, stride):
     with pytest.raises(ValueError, match="CUDA"):           # the cache is what is refused
         seer.seer_gate_key_cache_quant(cache, torch.zeros((2, 128, 64), dtype=torch.bfloat16), 200, wk_head_stride=stride)
+
+
+def test_a_stream_of_another_device_is_refused():
+    """What is given as the stream decides nothing else: the call would have run on the other device's current stream."""
+    from long_context_prefill_attngate_b200 import kvcache
+
+    class Stream:
+        cuda_stream, device_index = 0, 1
+
+    with pytest.raises(ValueError, match="stream"):
+        kvcache._elsewhere(lambda: None, 0, Stream())

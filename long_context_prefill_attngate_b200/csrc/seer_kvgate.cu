@@ -485,20 +485,27 @@ __global__ void __launch_bounds__(kGateThreads, 2)
     }
 }
 
+constexpr size_t gate_smem(int DK, int dg)
+{
+    return sizeof(__nv_bfloat16) * ((size_t)DK * (((dg + 7) & ~7) + kPad) + 3 * kGateRows * (DK + kPad)) +
+           sizeof(double) * (dg / 2) + sizeof(float) * kGateRows * (DK + dg + 1);
+}
+
 template <int BITS, int D, bool MAXMIN>
 cudaError_t launch(int B, int Hkv, int L, const KvView &kv, const int32_t *lens, int first, const void *wk,
                    long long wk_stride, int dg, float theta, float *kt, int *status, cudaStream_t stream)
 {
     constexpr int DK = MAXMIN ? 2 * D : D;
-    const int nb = num_blocks(L), dgp = (dg + 7) & ~7;
-    const size_t smem = sizeof(__nv_bfloat16) * ((size_t)DK * (dgp + kPad) + 3 * kGateRows * (DK + kPad)) +
-                        sizeof(double) * (dg / 2) + sizeof(float) * kGateRows * (DK + dg + 1);
+    const int nb = num_blocks(L);
+    // the limit for every d_gate at once: another thread's call may lie between this one and the launch
+    constexpr size_t kMost = gate_smem(DK, 256);
+    static_assert(kMost <= 226 * 1024);
     const cudaError_t e = cudaFuncSetAttribute(kv_gate_kernel<BITS, D, MAXMIN>,
-                                               cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+                                               cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kMost);
     if (e != cudaSuccess)
         return e;
     return launch_programmatic(kv_gate_kernel<BITS, D, MAXMIN>, dim3((nb - first + kGateRows - 1) / kGateRows, B * Hkv),
-                               kGateThreads, smem, stream, kv, Hkv, L, lens, nb, first,
+                               kGateThreads, gate_smem(DK, dg), stream, kv, Hkv, L, lens, nb, first,
                                static_cast<const __nv_bfloat16 *>(wk), wk_stride, dg, -2.0 * log((double)theta) / dg, kt,
                                status);
 }

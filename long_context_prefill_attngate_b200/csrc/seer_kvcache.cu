@@ -12,6 +12,8 @@
 // HBM is the floor of both directions.  32k rows of 8 heads at 4 bits (D = 128,
 // 176 MB): reading back 31 us (5.7 TB/s), HBM-bound; writing 37 us (4.8 TB/s),
 // its instructions 70 % of the issue slots.
+#include <type_traits>
+
 #include <cuda_bf16.h>
 
 #include "seer_internal.h"
@@ -151,22 +153,27 @@ __device__ __forceinline__ uint2 k8_from_store(uint2 w, int lane)
     return j & 1 ? make_uint2(y0, y1) : make_uint2(x0, x1);
 }
 
-// The code words and the param of a lane's sixteen elements.  t / s is divided as
-// IEEE division would (quotient by the reciprocal, then one step with the exact
-// remainder), which puts a half where it is one: bf16 differences and an 8-bit s
-// keep every other quotient further from a half than 2^-24 of it.
+// A group as it is stored: the extrema of the lane's sixteen elements w, joined over
+// the lanes that share the group.
+struct Group {
+    float lo, s, inv;                                    // inv: about 1 / s, 0 for s = 0
+    uint32_t par;
+    bool ok;                                             // no NaN, no magnitude of 2^126 or more
+    bool open;                                           // see quantise16
+};
+
 template <int BITS, int D>
-__device__ __forceinline__ uint32_t quantise16(const uint4 (&in)[2], uint32_t (&code)[BITS / 2])
+__device__ __forceinline__ Group group_of(const uint32_t (&w)[8])
 {
     using F = KvFmt<BITS, D>;
     constexpr int GL = RowMap<BITS, D, 16>::GL;
-    const uint32_t w[8] = {in[0].x, in[0].y, in[0].z, in[0].w, in[1].x, in[1].y, in[1].z, in[1].w};
-    __nv_bfloat162 mn, mx;
+    __nv_bfloat162 mn, mx, least;                        // of the elements, of their magnitudes
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
         const __nv_bfloat162 p = *reinterpret_cast<const __nv_bfloat162 *>(&w[i]);
         mn = i == 0 ? p : __hmin2_nan(mn, p);
         mx = i == 0 ? p : __hmax2_nan(mx, p);
+        least = i == 0 ? __habs2(p) : __hmin2(least, __habs2(p));
     }
 #pragma unroll
     for (int off = 1; off < GL; off <<= 1) {
@@ -175,27 +182,47 @@ __device__ __forceinline__ uint32_t quantise16(const uint4 (&in)[2], uint32_t (&
     }
     const __nv_bfloat16 lob = __hmin_nan(mn.x, mn.y), hib = __hmax_nan(mx.x, mx.y);
     const float lo = __bfloat162float(lob), hi = __bfloat162float(hib);
-    const bool ok = lo > -8.507059173023462e37f && hi < 8.507059173023462e37f;   // 2^126; false for a NaN
+    Group g;
+    g.ok = lo > -8.507059173023462e37f && hi < 8.507059173023462e37f;           // 2^126; false for a NaN
+    // range / TOP: the product with the rounded reciprocal, corrected once by its exact
+    // remainder (Markstein's division on a fused multiply-add, IBM J. Res. Dev. 34, 1990)
     constexpr float kInvTop = 1.f / F::TOP;
-    const float range = hi - lo, s0 = range * kInvTop;   // range / TOP as IEEE division rounds it
+    const float range = hi - lo, s0 = range * kInvTop;
     __nv_bfloat16 sb = __float2bfloat16_rn(fmaf(fmaf(s0, -(float)F::TOP, range), kInvTop, s0));
-    if (!ok || __bfloat162float(sb) < 7.888609052210118e-31f)                   // 2^-100
+    if (!g.ok || __bfloat162float(sb) < 7.888609052210118e-31f)                 // 2^-100
         sb = __float2bfloat16_rn(0.f);
-    const float s = __bfloat162float(sb);
-    float inv;
-    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(inv) : "f"(s));
-    inv = s > 0.f ? inv : 0.f;
-    const float zr = ok ? lo : 0.f;
+    g.s = __bfloat162float(sb);
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(g.inv) : "f"(g.s));
+    g.inv = g.s > 0.f ? g.inv : 0.f;
+    g.lo = g.ok ? lo : 0.f;
+    g.par = (uint32_t)__bfloat16_as_ushort(sb) | (g.ok ? (uint32_t)__bfloat16_as_ushort(lob) : 0x7FC0u) << 16;
+    const float most = fmaxf(fabsf(lo), fabsf(hi)) * 0.000030517578125f;        // 2^-15
+    const float r = fmaf(rintf(lo * g.inv), -g.s, lo);   // what -z / s is off an integer, times s
+    g.open = g.s > 0.f && ((fminf(__low2float(least), __high2float(least)) < most && fabsf(r) > 0.484f * g.s) ||
+                           (fabsf(lo) < most && lo != 0.f));
+    return g;
+}
+
+// The code words of a lane's sixteen elements.  The quotient of t = x - z by s is
+// taken as the group's scale is: one that is a half is one then.  Where x and z are
+// within 2^15 of the group's largest, t is exact (23 bits; 24 where neither is far below),
+// and with an 8-bit s every other quotient is further from a half than it is off.  Of
+// two codes the wrong one may come out where z is further below, or where x is and
+// -z / s lies within 2^-6 of a half (x / s is below 2^-7): Group::open, then nearest_codes.
+template <int BITS>
+__device__ __forceinline__ void quantise16(const uint32_t (&w)[8], const Group &g, uint32_t (&code)[BITS / 2])
+{
+    constexpr float kTop = (1 << BITS) - 1;
     constexpr uint32_t kMagic = 0x4B400000u;             // 1.5 2^23: adding it leaves the integer in the low bits
     uint32_t pair[8];                                    // n of two elements in the low bits
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
         const float2 v = make_float2(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xFFFF0000u));
-        const float2 t = add2(v, both(-zr));
-        float2 q = mul2(t, both(inv));
-        q = fma2(fma2(q, both(-s), t), both(inv), q);
+        const float2 t = add2(v, both(-g.lo));
+        float2 q = mul2(t, both(g.inv));
+        q = fma2(fma2(q, both(-g.s), t), both(g.inv), q);
         if (BITS == 8)                                   // s may be up to 2^-8 below the range / 255, not so at 15
-            q = make_float2(fminf(q.x, (float)F::TOP), fminf(q.y, (float)F::TOP));
+            q = make_float2(fminf(q.x, kTop), fminf(q.y, kTop));
         const float2 m = add2(q, both(__uint_as_float(kMagic)));
         pair[i] = __float_as_uint(m.y) * (1u << BITS) + __float_as_uint(m.x);
     }
@@ -209,11 +236,95 @@ __device__ __forceinline__ uint32_t quantise16(const uint4 (&in)[2], uint32_t (&
         for (int i = 0; i < 4; ++i)
             code[i] = __byte_perm(pair[2 * i], pair[2 * i + 1], 0x5410);
     }
-    if (!ok)
+    if (!g.ok)
 #pragma unroll
         for (int i = 0; i < BITS / 2; ++i)
             code[i] = 0u;
-    return (uint32_t)__bfloat16_as_ushort(sb) | (ok ? (uint32_t)__bfloat16_as_ushort(lob) : 0x7FC0u) << 16;
+}
+
+__device__ __forceinline__ float element(const uint32_t (&w)[8], int i)
+{
+    return __uint_as_float(i & 1 ? w[i / 2] & 0xFFFF0000u : w[i / 2] << 16);
+}
+
+// Whether a quotient of the lane's lies next to a half.
+__device__ __forceinline__ bool next_to_a_half(const uint32_t (&w)[8], const Group &g)
+{
+    float most = 0.f;
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+        const float t = element(w, i) - g.lo;
+        most = fmaxf(most, fabsf(fmaf(-rintf(t * g.inv), g.s, t)));
+    }
+    return most > 0.4999f * g.s;
+}
+
+// The codes by the definition, the integers nearest to (x - z) / s, with nothing
+// rounded on the way to the decision.  t + e is x - z exactly (Knuth's two-sum).  n0, t
+// times the reciprocal rounded, is off by one at most, and only next to a half;
+// r = t - n0 s is a float (t and n0 s are within a factor of two of each other, or
+// t's last place is above 2^-24 s).  |e| is below every difference that r and s / 2
+// can have but 0 (t < 2^9 s), so it decides where they are equal, and nowhere else.
+template <int BITS>
+__device__ __forceinline__ void nearest_codes(const uint32_t (&w)[8], const Group &g, uint32_t (&code)[BITS / 2])
+{
+    constexpr int kTop = (1 << BITS) - 1;
+#pragma unroll
+    for (int i = 0; i < BITS / 2; ++i)
+        code[i] = 0u;
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+        const float x = element(w, i), t = x - g.lo, back = t - x, e = (x - (t - back)) + (-g.lo - back);
+        const float n0 = rintf(t * g.inv), r = fmaf(-n0, g.s, t), half = 0.5f * g.s;
+        int n = (int)n0;
+        const bool odd = n & 1;
+        if (r > half || (r == half && (e > 0.f || (e == 0.f && odd))))
+            ++n;
+        else if (r < -half || (r == -half && (e < 0.f || (e == 0.f && odd))))
+            --n;
+        code[i * BITS / 32] |= (uint32_t)(g.ok && g.s > 0.f ? min(n, kTop) : 0) << (i * BITS % 32);
+    }
+}
+
+// Token tok's code words of a lane (sixteen elements c of the row) to their places in
+// the half record `half`.  All lanes of the warp; `mine`: this lane has a row.
+template <int BITS, int D, bool V>
+__device__ __forceinline__ void store_codes(uint8_t *half, int tok, int c, bool mine, const uint32_t (&code)[BITS / 2])
+{
+    using F = KvFmt<BITS, D>;
+    uint8_t *row = half + (V ? F::kCodeV : 0) + tok * F::R;
+    if constexpr (BITS == 4 && !V) {                     // words 2c and 2c + 1
+#pragma unroll
+        for (int k = 0; k < 2; ++k)
+            if (mine)
+                *reinterpret_cast<uint32_t *>(row + (((2 * c + k) % 4) * F::NG + c / 2) * 4) = code[k];
+    } else if constexpr (BITS == 4) {
+        // 16-bit runs of chunks 4h .. 4h + 3 (h = c % 2) of group c / 2; a stored word is
+        // two groups of one chunk: the lanes of an even and an odd group trade the two
+        // upper and the two lower chunks
+        const int gr = c / 2, h = c % 2, odd = gr & 1;
+        const uint32_t got = __shfl_xor_sync(0xffffffffu, odd ? code[0] : code[1], 2);
+        const uint32_t lo = odd ? got : code[0], hi = odd ? code[1] : got;        // even group, odd group
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+            const int chunk = 4 * h + 2 * odd + k;
+            if (mine)
+                *reinterpret_cast<uint32_t *>(row + (chunk ^ F::v_swizzle(tok)) * (2 * F::NG) + (gr >> 1) * 4) =
+                    __byte_perm(lo, hi, k ? 0x7632 : 0x5410);
+        }
+    } else if constexpr (!V) {                           // words 4c .. 4c + 3, sixteen bytes apart
+        const int p = D == 128 ? (c / 4) ^ (tok & 1) : 0;
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+            if (mine)
+                *reinterpret_cast<uint32_t *>(row + (p * 16 + k * 4 + c % 4) * 4) = code[k];
+    } else {                                             // runs of chunks 2c and 2c + 1 (of eight) of group c / 4
+#pragma unroll
+        for (int k = 0; k < 2; ++k)
+            if (mine)
+                *reinterpret_cast<uint2 *>(row + ((2 * c % 8 + k) ^ F::v_swizzle(tok)) * (8 * F::NG) + c / 4 * 8) =
+                    make_uint2(code[2 * k], code[2 * k + 1]);
+    }
 }
 
 template <int BITS, int D>
@@ -232,68 +343,66 @@ __global__ void __launch_bounds__(kRowThreads) kv_write_kernel(KvView kv, KvRows
     const __nv_bfloat16 *src[2] = {
         static_cast<const __nv_bfloat16 *>(x.k) + b * x.k_stride_b + kvh * x.k_stride_h + r.row0 * x.k_stride_t + 16 * c,
         static_cast<const __nv_bfloat16 *>(x.v) + b * x.v_stride_b + kvh * x.v_stride_h + r.row0 * x.v_stride_t + 16 * c};
-    uint4 in[2][NI][2];
-#pragma unroll
-    for (int is_v = 0; is_v < 2; ++is_v)
-#pragma unroll
-        for (int i = 0; i < NI; ++i) {
-            const int t = (i * (kRowThreads / 32) + warp) * M::RPW + lane / M::CH;
-            in[is_v][i][0] = in[is_v][i][1] = make_uint4(0u, 0u, 0u, 0u);
-            if (t >= r.lo && t < r.hi) {
-                const uint4 *at = reinterpret_cast<const uint4 *>(src[is_v] + t * (is_v ? x.v_stride_t : x.k_stride_t));
-                in[is_v][i][0] = load(at);
-                in[is_v][i][1] = load(at + 1);
-            }
+    uint32_t in[2][NI][8];
+    auto token = [&](int i) { return (i * (kRowThreads / 32) + warp) * M::RPW; };         // the warp's first
+    auto fetch = [&](int is_v, int t, uint32_t (&w)[8]) {
+        uint4 a = make_uint4(0u, 0u, 0u, 0u), b = a;
+        if (t >= r.lo && t < r.hi) {
+            const uint4 *at = reinterpret_cast<const uint4 *>(src[is_v] + t * (is_v ? x.v_stride_t : x.k_stride_t));
+            a = load(at);
+            b = load(at + 1);
         }
+        w[0] = a.x, w[1] = a.y, w[2] = a.z, w[3] = a.w, w[4] = b.x, w[5] = b.y, w[6] = b.z, w[7] = b.w;
+    };
+    auto store = [&](auto is_v, int t, const uint32_t (&code)[M::NW]) {
+        store_codes<BITS, D, is_v>(r.record + t / 32 * F::HALF, t % 32, c, t >= r.lo && t < r.hi, code);
+    };
+    auto none = [&](int tw) { return tw + M::RPW <= r.lo || tw >= r.hi; };                  // of the whole warp's rows
 #pragma unroll
     for (int is_v = 0; is_v < 2; ++is_v)
 #pragma unroll
+        for (int i = 0; i < NI; ++i)
+            fetch(is_v, token(i) + lane / M::CH, in[is_v][i]);
+    unsigned open = 0u;                                  // items whose codes are not certain yet
+    auto rows = [&](auto is_v) {
+#pragma unroll
         for (int i = 0; i < NI; ++i) {
-            const int tw = (i * (kRowThreads / 32) + warp) * M::RPW, t = tw + lane / M::CH;
-            if (tw + M::RPW <= r.lo || tw >= r.hi)
-                continue;                                // the whole warp
+            const int tw = token(i), t = tw + lane / M::CH;
+            if (none(tw))
+                continue;
+            const Group g = group_of<BITS, D>(in[is_v][i]);
             uint32_t code[M::NW];
-            const uint32_t par = quantise16<BITS, D>(in[is_v][i], code);
-            const int tok = t % 32;
-            uint8_t *half = r.record + t / 32 * F::HALF, *row = half + (is_v ? F::kCodeV : 0) + tok * F::R;
-            const bool mine = t >= r.lo && t < r.hi;
-            if constexpr (BITS == 4) {
-                if (!is_v) {                             // words 2c and 2c + 1
-#pragma unroll
-                    for (int k = 0; k < 2; ++k)
-                        if (mine)
-                            *reinterpret_cast<uint32_t *>(row + (((2 * c + k) % 4) * F::NG + c / 2) * 4) = code[k];
-                } else {
-                    // 16-bit runs of chunks 4h .. 4h + 3 (h = c % 2) of group c / 2; a stored
-                    // word is two groups of one chunk: the lanes of an even and an odd
-                    // group trade the two upper and the two lower chunks
-                    const int gr = c / 2, h = c % 2, odd = gr & 1;
-                    const uint32_t got = __shfl_xor_sync(0xffffffffu, odd ? code[0] : code[1], 2);
-                    const uint32_t lo = odd ? got : code[0], hi = odd ? code[1] : got;    // even group, odd group
-#pragma unroll
-                    for (int k = 0; k < 2; ++k) {
-                        const int chunk = 4 * h + 2 * odd + k;
-                        if (mine)
-                            *reinterpret_cast<uint32_t *>(row + (chunk ^ F::v_swizzle(tok)) * (2 * F::NG) + (gr >> 1) * 4) =
-                                __byte_perm(lo, hi, k ? 0x7632 : 0x5410);
-                    }
-                }
-            } else if (!is_v) {                          // words 4c .. 4c + 3, sixteen bytes apart
-                const int p = D == 128 ? (c / 4) ^ (tok & 1) : 0;
-#pragma unroll
-                for (int k = 0; k < 4; ++k)
-                    if (mine)
-                        *reinterpret_cast<uint32_t *>(row + (p * 16 + k * 4 + c % 4) * 4) = code[k];
-            } else {                                     // runs of chunks 2c and 2c + 1 (of eight) of group c / 4
-#pragma unroll
-                for (int k = 0; k < 2; ++k)
-                    if (mine)
-                        *reinterpret_cast<uint2 *>(row + ((2 * c % 8 + k) ^ F::v_swizzle(tok)) * (8 * F::NG) + c / 4 * 8) =
-                            make_uint2(code[2 * k], code[2 * k + 1]);
-            }
-            if (mine && c % M::GL == 0)
-                *reinterpret_cast<uint32_t *>(half + (is_v ? F::kParV : F::kParK) + tok * F::PAR + c / M::GL * 4) = par;
+            quantise16<BITS>(in[is_v][i], g, code);
+            store(is_v, t, code);
+            if (t >= r.lo && t < r.hi && c % M::GL == 0)
+                *reinterpret_cast<uint32_t *>(r.record + t / 32 * F::HALF + (is_v ? F::kParV : F::kParK) + t % 32 * F::PAR +
+                                              c / M::GL * 4) = g.par;
+            open |= (unsigned)g.open << (is_v * NI + i);
         }
+    };
+    // Rows with an open lane (one in a thousand of a warp's accesses of normal ones) are
+    // read again: kept in registers, or decided on the spot, they would cost every row.
+    auto again = [&](auto is_v) {
+#pragma unroll 1
+        for (int i = 0; i < NI; ++i) {
+            if (!__any_sync(0xffffffffu, open >> (is_v * NI + i) & 1u))
+                continue;
+            const int t = token(i) + lane / M::CH;
+            uint32_t w[8], code[M::NW];
+            fetch(is_v, t, w);
+            const Group g = group_of<BITS, D>(w);
+            if (!__any_sync(0xffffffffu, g.open && next_to_a_half(w, g)))
+                continue;
+            nearest_codes<BITS>(w, g, code);
+            store(is_v, t, code);
+        }
+    };
+    rows(std::false_type{});
+    rows(std::true_type{});
+    if (__any_sync(0xffffffffu, open != 0u)) {
+        again(std::false_type{});
+        again(std::true_type{});
+    }
 }
 
 template <int BITS, int D>

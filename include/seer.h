@@ -309,6 +309,18 @@ SEER_API seer_status seer_decode_gate_scores_cached(const seer_shape *shape, con
                                                     void *workspace, size_t ws_bytes, void *stream);
 
 /*
+ * seer_decode_gate_scores_cached_lens — the same for a batch of sequences of
+ * their own lengths: lens is DEVICE int32 [B] (clamped to 0 .. S, S = L the
+ * longest) or NULL for S.  Sequence b has nb_b = ceil(lens[b] / 64) blocks: q is
+ * rotated at nb_b - 1, the softmax is over j < nb_b, and scores are 0 from nb_b on
+ * (everywhere for a sequence without a token).  Key rows from nb_b on are not read.
+ */
+SEER_API seer_status seer_decode_gate_scores_cached_lens(const seer_shape *shape, const void *q_tok, const float *kt,
+                                                         const void *wq, const seer_gate_params *gp,
+                                                         const int32_t *lens, float *scores, void *workspace,
+                                                         size_t ws_bytes, void *stream);
+
+/*
  * seer_decode_block_mask — the mask row of the token: seer_block_mask's row
  * i = nb - 1 (threshold or TopK with k from k_fixed, k_per_row[nb-1] or
  * ceil(density * nb); block 0 and the last block forced as flagged).
@@ -316,6 +328,15 @@ SEER_API seer_status seer_decode_gate_scores_cached(const seer_shape *shape, con
  */
 SEER_API seer_status seer_decode_block_mask(const seer_shape *shape, const float *scores,
                                             const seer_mask_params *mp, uint8_t *mask, void *stream);
+
+/*
+ * seer_decode_block_mask_lens — the same for sequences of their own lengths
+ * (lens as above): the row of sequence b is seer_block_mask's row nb_b - 1 (its k
+ * from nb_b, its own last block the forced one), 0 from nb_b on.
+ */
+SEER_API seer_status seer_decode_block_mask_lens(const seer_shape *shape, const float *scores,
+                                                 const seer_mask_params *mp, const int32_t *lens, uint8_t *mask,
+                                                 void *stream);
 
 /*
  * seer_block_sparse_decode — attention of the token over the active blocks:

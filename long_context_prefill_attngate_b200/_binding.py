@@ -44,7 +44,7 @@ EXPORTS = (
     "seer_last_error", "seer_version", "seer_gate_scores_noalloc", "seer_distill_loss",
     "seer_decode_gate_scores", "seer_decode_block_mask", "seer_block_sparse_decode",
     "seer_gate_key_cache", "seer_decode_gate_scores_cached", "seer_topk_from_density",
-    "seer_kv_record_bytes", "seer_kv_write", "seer_kv_read", "seer_gate_key_cache_quant",
+    "seer_decode_gate_scores_cached_lens", "seer_decode_block_mask_lens", "seer_kv_record_bytes", "seer_kv_write", "seer_kv_read", "seer_gate_key_cache_quant",
     "seer_block_sparse_decode_quant",
 )
 
@@ -114,6 +114,8 @@ def lib() -> ctypes.CDLL:
             L.seer_gate_key_cache.argtypes = [SP, P, P, ctypes.POINTER(seer_gate_params), I, P, P, Z, P]
             L.seer_decode_gate_scores_cached.argtypes = [SP, P, P, P, ctypes.POINTER(seer_gate_params), P, P, Z, P]
             L.seer_topk_from_density.argtypes = [ctypes.c_double, I, I, I, ctypes.POINTER(ctypes.c_int32)]
+            L.seer_decode_gate_scores_cached_lens.argtypes = [SP, P, P, P, ctypes.POINTER(seer_gate_params), P, P, P, Z, P]
+            L.seer_decode_block_mask_lens.argtypes = [SP, P, ctypes.POINTER(seer_mask_params), P, P, P]
             CP = ctypes.POINTER(seer_kv_cache)
             L.seer_kv_write.argtypes = [SP, CP, ctypes.POINTER(seer_kv_rows), P, P, I, P]
             L.seer_kv_read.argtypes = [SP, CP, P, P, I, P, P, P]
@@ -125,6 +127,7 @@ def lib() -> ctypes.CDLL:
                        "seer_block_sparse_prefill", "seer_attn_pooled_map", "seer_check_status",
                        "seer_distill_loss", "seer_decode_gate_scores", "seer_decode_block_mask",
                        "seer_block_sparse_decode", "seer_gate_key_cache", "seer_decode_gate_scores_cached",
+                       "seer_decode_gate_scores_cached_lens", "seer_decode_block_mask_lens",
                        "seer_topk_from_density", "seer_kv_write", "seer_kv_read", "seer_gate_key_cache_quant",
                        "seer_block_sparse_decode_quant"):
                 getattr(L, fn).restype = I
@@ -391,15 +394,22 @@ def seer_gate_key_cache(k, wk, kt=None, first_block: int = 0, rope_theta: float 
     return kt
 
 
+def _need_lens(lens, Bsz, device):
+    _need(lens is None or (lens.dtype == _torch().int32 and tuple(lens.shape) == (Bsz,) and lens.is_contiguous() and
+                           lens.device == device), "lens must be int32 [B] on the other tensors' device")
+
+
 def seer_decode_gate_scores_cached(q_tok, kt, wq, L: int, Hkv: int, rope_theta: float = 5e5, scores=None,
-                                   workspace=None, stream=None, wq_head_stride: int | None = None):
-    """Decode gate row fp32 [B,Hq,nb] from cached key rows kt [B,Hkv,nb,d_gate] (cache of L tokens)."""
+                                   workspace=None, stream=None, wq_head_stride: int | None = None, lens=None):
+    """Decode gate row fp32 [B,Hq,nb] from cached key rows kt [B,Hkv,nb,d_gate] (cache of L tokens, or of lens[b]
+    (device int32 [B]) tokens each: q at the sequence's own last block, scores 0 behind it)."""
     torch = _torch()
     _need(q_tok.is_contiguous() and wq.is_contiguous() and kt.is_contiguous(), "tensors must be contiguous")
     Bsz, Hq, d = q_tok.shape
     dg = wq.shape[-1]
     nb = -(-L // BLOCK)
     _need(tuple(kt.shape) == (Bsz, Hkv, nb, dg) and kt.dtype == torch.float32, "kt must be fp32 [B,Hkv,nb,d_gate]")
+    _need_lens(lens, Bsz, q_tok.device)
     sh = seer_shape(Bsz, Hq, Hkv, L, d)
     if wq_head_stride is None:
         wq_head_stride = 0 if wq.dim() == 2 else d * dg
@@ -407,27 +417,30 @@ def seer_decode_gate_scores_cached(q_tok, kt, wq, L: int, Hkv: int, rope_theta: 
         scores = torch.empty((Bsz, Hq, nb), dtype=torch.float32, device=q_tok.device)
     workspace, wsb = _workspace(SEER_CALL_DECODE_GATE_CACHED, sh, q_tok.device, workspace)
     gp = seer_gate_params(int(dg), float(rope_theta), int(wq_head_stride), 0, 0)
-    _check(lib().seer_decode_gate_scores_cached(ctypes.byref(sh), _ptr(q_tok), _ptr(kt), _ptr(wq), ctypes.byref(gp),
-                                                _ptr(scores), _ptr(workspace), wsb, _stream_ptr(stream)))
+    _check(lib().seer_decode_gate_scores_cached_lens(ctypes.byref(sh), _ptr(q_tok), _ptr(kt), _ptr(wq), ctypes.byref(gp),
+                                                     _ptr(lens), _ptr(scores), _ptr(workspace), wsb,
+                                                     _stream_ptr(stream)))
     return scores
 
 
 def seer_decode_block_mask(scores, mode: str = "topk", threshold: float = 0.0, density: float = 1.0,
                            k_fixed: int = 0, force_first: bool = True, force_diag: bool = True, mask=None,
-                           stream=None):
-    """Decode mask row u8 [B,Hq,nb] from the gate row (threshold or TopK)."""
+                           stream=None, lens=None):
+    """Decode mask row u8 [B,Hq,nb] from the gate row (threshold or TopK); lens (device int32 [B]): the sequences' own
+    lengths in tokens, each row for its sequence's blocks alone."""
     torch = _torch()
     _need(scores.dtype == torch.float32 and scores.is_contiguous() and scores.dim() == 3,
           "scores must be contiguous fp32 [B,Hq,nb]")
     B, Hq, nb = scores.shape
+    _need_lens(lens, B, scores.device)
     sh = seer_shape(B, Hq, 1, nb * BLOCK, 64)
     if mask is None:
         mask = torch.empty((B, Hq, nb), dtype=torch.uint8, device=scores.device)
     m = {"threshold": SEER_MASK_THRESHOLD, "topk": SEER_MASK_TOPK}[mode]
     mp = seer_mask_params(m, float(threshold), float(density), int(k_fixed), None,
                           int(bool(force_first)), int(bool(force_diag)))
-    _check(lib().seer_decode_block_mask(ctypes.byref(sh), _ptr(scores), ctypes.byref(mp), _ptr(mask),
-                                        _stream_ptr(stream)))
+    _check(lib().seer_decode_block_mask_lens(ctypes.byref(sh), _ptr(scores), ctypes.byref(mp), _ptr(lens), _ptr(mask),
+                                             _stream_ptr(stream)))
     return mask
 
 

@@ -525,6 +525,13 @@ seer_status seer_decode_gate_scores_cached(const seer_shape *shape, const void *
                                            const void *wq, const seer_gate_params *gp, float *scores, void *workspace,
                                            size_t ws_bytes, void *stream)
 {
+    return seer_decode_gate_scores_cached_lens(shape, q_tok, kt, wq, gp, nullptr, scores, workspace, ws_bytes, stream);
+}
+
+seer_status seer_decode_gate_scores_cached_lens(const seer_shape *shape, const void *q_tok, const float *kt,
+                                                const void *wq, const seer_gate_params *gp, const int32_t *lens,
+                                                float *scores, void *workspace, size_t ws_bytes, void *stream)
+{
     const seer_status st = check_gate_args("seer_decode_gate_scores_cached", shape, q_tok, kt, wq, wq, gp, scores,
                                            workspace, ws_bytes, 3);
     if (st != SEER_OK)
@@ -532,8 +539,8 @@ seer_status seer_decode_gate_scores_cached(const seer_shape *shape, const void *
     if ((reinterpret_cast<uintptr_t>(kt) & 15u) != 0)
         return fail(SEER_ERR_INVALID_ARG, "kt must be 16-byte aligned");
     const cudaError_t e = launch_decode_gate_cached(shape->B, shape->Hq, shape->Hkv, shape->S, shape->d, gp->d_gate,
-                                                    gp->rope_theta, q_tok, wq, gp->wq_head_stride, kt, scores,
-                                                    workspace, static_cast<cudaStream_t>(stream));
+                                                    gp->rope_theta, q_tok, wq, gp->wq_head_stride, kt, lens,
+                                                    scores, workspace, static_cast<cudaStream_t>(stream));
     if (e != cudaSuccess)
         return cuda_fail(e, "seer_decode_gate_scores_cached launch");
     return ok();
@@ -565,6 +572,12 @@ seer_status seer_topk_from_density(double density, int nb, int force_first, int 
 seer_status seer_decode_block_mask(const seer_shape *shape, const float *scores, const seer_mask_params *mp,
                                    uint8_t *mask, void *stream)
 {
+    return seer_decode_block_mask_lens(shape, scores, mp, nullptr, mask, stream);
+}
+
+seer_status seer_decode_block_mask_lens(const seer_shape *shape, const float *scores, const seer_mask_params *mp,
+                                        const int32_t *lens, uint8_t *mask, void *stream)
+{
     seer_status st = check_shape(shape);
     if (st != SEER_OK)
         return st;
@@ -578,9 +591,10 @@ seer_status seer_decode_block_mask(const seer_shape *shape, const float *scores,
     if (mp->mode == SEER_MASK_THRESHOLD && std::isnan(mp->threshold))
         return fail(SEER_ERR_INVALID_ARG, "threshold is NaN");
     const int nb = num_blocks(shape->S);
-    const cudaError_t e = launch_mask_rows(shape->B, shape->Hq, nb, 1, nb - 1, scores, mp->mode, mp->threshold,
-                                           mp->density, mp->k_fixed, mp->k_per_row, mp->force_first ? 1 : 0,
-                                           mp->force_diag ? 1 : 0, mask, static_cast<cudaStream_t>(stream));
+    const cudaError_t e = launch_mask_rows(shape->B, shape->Hq, nb, 1, nb - 1, SeqLens{lens, shape->S}, scores, mp->mode,
+                                           mp->threshold, mp->density, mp->k_fixed, mp->k_per_row,
+                                           mp->force_first ? 1 : 0, mp->force_diag ? 1 : 0, mask,
+                                           static_cast<cudaStream_t>(stream));
     if (e != cudaSuccess)
         return cuda_fail(e, "seer_decode_block_mask launch");
     return ok();

@@ -161,9 +161,10 @@ struct ProjJob {
 // Two projections in one launch (the Q and K sides of the gate: the K grid
 // alone would leave most of the GPU idle): blockIdx.x < ny0 is head row
 // blockIdx.x of job j0, the rest are job j1's; blockIdx.y is the chunk of
-// kProjRows blocks.
+// kProjRows blocks.  Lengths given: row 0 of a sequence's heads stands at its last
+// block instead of at pos0 (a decode step's q).
 __global__ void __launch_bounds__(kProjThreads)
-    project_rope_kernel(ProjJob j0, ProjJob j1, int ny0, int nb, int ld, int dg, double theta, int pos0)
+    project_rope_kernel(ProjJob j0, ProjJob j1, int ny0, int nb, int ld, int dg, double theta, int pos0, SeqLens seq)
 {
     extern __shared__ float4 psm4[];
     const bool second = (int)blockIdx.x >= ny0;
@@ -182,6 +183,8 @@ __global__ void __launch_bounds__(kProjThreads)
     const int i0 = blockIdx.y * kProjRows;
     const int rows = min(kProjRows, nb - i0);
     const int half = dg / 2;
+    if (seq.lens != nullptr)
+        pos0 = seq.blocks(bh / H) - 1;
     const __nv_bfloat16 *wh = w + (long long)h * w_stride;
     // W as 16-byte pieces (8 bf16) when this head's weights start 16-byte aligned
     if ((reinterpret_cast<uintptr_t>(wh) & 15) == 0 && ((d * dg) & 7) == 0) {
@@ -680,11 +683,12 @@ __global__ void q_to_f32_kernel(const __nv_bfloat16 *__restrict__ q, long long n
 constexpr int kDecThreads = 256;
 
 // Decode gate row: scores[bh, j] = softmax_j(qt[bh] . kt[b, h/g, j] / sqrt(dg))
-// over every block j < nb (the token sits in the last block).  One CTA per
-// (b, h): logits into shared memory (nb floats), then max / sum / normalise.
+// over every block j of the sequence (the token sits in the last one), 0 for the
+// others of the nb.  One CTA per (b, h): logits into shared memory (nb floats), then
+// max / sum / normalise.
 __global__ void __launch_bounds__(kDecThreads)
-    decode_gate_kernel(const float *__restrict__ qt, const float *__restrict__ kt, int Hq, int Hkv, int nb, int dg,
-                       float scale, float *__restrict__ scores)
+    decode_gate_kernel(const float *__restrict__ qt, const float *__restrict__ kt, int Hq, int Hkv, int row_len, int dg,
+                       float scale, SeqLens seq, float *__restrict__ scores)
 {
     extern __shared__ float dsm[];
     float *sq = dsm;                 // dg
@@ -692,7 +696,13 @@ __global__ void __launch_bounds__(kDecThreads)
     __shared__ float red[kDecThreads / 32];
     const int bh = blockIdx.x;
     const int b = bh / Hq, h = bh % Hq;
-    const float *kb = kt + (long long)(b * Hkv + h / (Hq / Hkv)) * nb * dg;
+    const float *kb = kt + (long long)(b * Hkv + h / (Hq / Hkv)) * row_len * dg;
+    const int nb = seq.blocks(b);
+    float *row = scores + (long long)bh * row_len;
+    for (int j = nb + threadIdx.x; j < row_len; j += kDecThreads)
+        row[j] = 0.f;
+    if (nb == 0)
+        return;
     for (int c = threadIdx.x; c < dg; c += kDecThreads)
         sq[c] = qt[(long long)bh * dg + c];
     __syncthreads();
@@ -737,7 +747,7 @@ __global__ void __launch_bounds__(kDecThreads)
         sum += red[w];
     const float inv = 1.0f / sum;
     for (int j = threadIdx.x; j < nb; j += kDecThreads)
-        scores[(long long)bh * nb + j] = sl[j] * inv;
+        row[j] = sl[j] * inv;
 }
 
 size_t align256(size_t x) { return (x + 255) & ~size_t(255); }
@@ -881,13 +891,13 @@ cudaError_t launch_gate_keys(int B, int Hkv, int L, int d, int dg, float theta, 
     const ProjJob jk{kp + (size_t)first_block * dk, Hkv, dk, static_cast<const __nv_bfloat16 *>(wk), wk_stride,
                      kt + (size_t)first_block * dg};
     project_rope_kernel<<<dim3(B * Hkv, (nsel + kProjRows - 1) / kProjRows), kProjThreads, psmem, stream>>>(
-        jk, jk, B * Hkv, nsel, nb, dg, (double)theta, first_block);
+        jk, jk, B * Hkv, nsel, nb, dg, (double)theta, first_block, SeqLens{nullptr, 0});
     return cudaGetLastError();
 }
 
 cudaError_t launch_decode_gate_cached(int B, int Hq, int Hkv, int L, int d, int dg, float theta, const void *q_tok,
-                                      const void *wq, long long wq_stride, const float *kt, float *scores, void *ws,
-                                      cudaStream_t stream)
+                                      const void *wq, long long wq_stride, const float *kt, const int32_t *lens,
+                                      float *scores, void *ws, cudaStream_t stream)
 {
     const int nb = num_blocks(L);
     float *qp = static_cast<float *>(ws);                               // [B*Hq, d]
@@ -900,10 +910,11 @@ cudaError_t launch_decode_gate_cached(int B, int Hq, int Hkv, int L, int d, int 
                                          (int)gate_projection_smem(2 * d, dg));
     if (e != cudaSuccess)
         return e;
-    // the token's q: one row per head, rotated at its block, nb - 1
+    // the token's q: one row per head, rotated at its block, the sequence's last
+    const SeqLens seq{lens, L};
     const ProjJob jq{qp, Hq, d, static_cast<const __nv_bfloat16 *>(wq), wq_stride, qt};
     project_rope_kernel<<<dim3(B * Hq, 1), kProjThreads, psmem_q, stream>>>(jq, jq, B * Hq, 1, 1, dg, (double)theta,
-                                                                         nb - 1);
+                                                                         nb - 1, seq);
     e = cudaGetLastError();
     if (e != cudaSuccess)
         return e;
@@ -912,7 +923,7 @@ cudaError_t launch_decode_gate_cached(int B, int Hq, int Hkv, int L, int d, int 
     if (e != cudaSuccess)
         return e;
     decode_gate_kernel<<<B * Hq, kDecThreads, dsmem, stream>>>(qt, kt, Hq, Hkv, nb, dg, 1.0f / sqrtf((float)dg),
-                                                                scores);
+                                                                seq, scores);
     return cudaGetLastError();
 }
 
@@ -940,7 +951,7 @@ cudaError_t launch_decode_gate(int B, int Hq, int Hkv, int L, int d, int dg, flo
     cudaError_t e = launch_gate_keys(B, Hkv, L, d, dg, theta, k_maxmin, k, wk, wk_stride, 0, kt, kws, stream);
     if (e != cudaSuccess)
         return e;
-    return launch_decode_gate_cached(B, Hq, Hkv, L, d, dg, theta, q_tok, wq, wq_stride, kt, scores, ws, stream);
+    return launch_decode_gate_cached(B, Hq, Hkv, L, d, dg, theta, q_tok, wq, wq_stride, kt, nullptr, scores, ws, stream);
 }
 
 } // namespace seer

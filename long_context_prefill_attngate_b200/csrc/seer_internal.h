@@ -15,6 +15,18 @@ constexpr int kBlock = 64;            // block size of gate, mask and kernels
 // Blocks of a sequence of S tokens; the last one holds S - 64 (nb - 1) tokens
 // when S is not a multiple of 64.
 inline int num_blocks(int S) { return (S + kBlock - 1) / kBlock; }
+// A batch's lengths on the device: sequence b has lens[b] of at most L tokens (null: L each).
+struct SeqLens {
+    const int32_t *lens;
+    int L;
+#ifdef __CUDACC__
+    __device__ __forceinline__ int blocks(int b) const
+    {
+        const int n = lens != nullptr ? max(0, min(lens[b], L)) : L;
+        return (n + kBlock - 1) / kBlock;
+    }
+#endif
+};
 constexpr int kMaxNb = 16384;         // S <= 1M tokens
 constexpr int kMaxAttnCtas = 296;     // tile pipelines in flight: 2 slots x 148 SMs
 constexpr int kAttnThreads = 512;     // 2 slots x (4 softmax + Q/K producer + MMA + list builder + V producer) warps
@@ -54,8 +66,8 @@ cudaError_t launch_gate_keys(int B, int Hkv, int L, int d, int dg, float theta, 
                              const void *wk, long long wk_stride, int first_block, float *kt, void *ws,
                              cudaStream_t stream);
 cudaError_t launch_decode_gate_cached(int B, int Hq, int Hkv, int L, int d, int dg, float theta, const void *q_tok,
-                                      const void *wq, long long wq_stride, const float *kt, float *scores, void *ws,
-                                      cudaStream_t stream);
+                                      const void *wq, long long wq_stride, const float *kt, const int32_t *lens,
+                                      float *scores, void *ws, cudaStream_t stream);
 size_t gate_key_ws_bytes(int B, int Hkv, int L, int d, bool k_maxmin);
 size_t decode_gate_ws_bytes(int B, int Hq, int Hkv, int L, int d, int dg, bool k_maxmin);
 
@@ -86,9 +98,9 @@ cudaError_t launch_decode_quant(int bits, int B, int Hq, int Hkv, int L, int d, 
 cudaError_t launch_mask(int B, int Hq, int nb, const float *scores, int mode, float threshold,
                         double density, int k_fixed, const int32_t *k_per_row, int force_first,
                         int force_diag, uint8_t *mask, cudaStream_t stream);
-cudaError_t launch_mask_rows(int B, int Hq, int nb, int R, int i0, const float *scores, int mode, float threshold,
-                             double density, int k_fixed, const int32_t *k_per_row, int ff, int fd, uint8_t *mask,
-                             cudaStream_t stream);
+cudaError_t launch_mask_rows(int B, int Hq, int nb, int R, int i0, SeqLens seq, const float *scores, int mode,
+                             float threshold, double density, int k_fixed, const int32_t *k_per_row, int ff, int fd,
+                             uint8_t *mask, cudaStream_t stream);
 cudaError_t launch_compact(int B, int Hq, int nb, const uint8_t *mask, int32_t *lists, int32_t *counts,
                            cudaStream_t stream);
 

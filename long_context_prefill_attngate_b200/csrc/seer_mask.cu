@@ -22,14 +22,21 @@ namespace {
 
 constexpr int kThrThreads = 256;
 
+// The causal row of score row `row`: i0 + row % R or, with lengths given, the last
+// block of its sequence (per_seq rows each; -1 where that has no token).
+__device__ __forceinline__ int row_index(long long row, int R, int i0, SeqLens seq, int per_seq)
+{
+    return seq.lens != nullptr ? seq.blocks((int)(row / per_seq)) - 1 : i0 + (int)(row % R);
+}
+
 __global__ void __launch_bounds__(kThrThreads)
-    threshold_kernel(const float *__restrict__ scores, long long total, int nb, int R, int i0, float thr, int ff,
-                     int fd, uint8_t *__restrict__ mask)
+    threshold_kernel(const float *__restrict__ scores, long long total, int nb, int R, int i0, SeqLens seq, int per_seq,
+                     float thr, int ff, int fd, uint8_t *__restrict__ mask)
 {
     for (long long e = (long long)blockIdx.x * kThrThreads + threadIdx.x; e < total;
          e += (long long)gridDim.x * kThrThreads) {
         const int j = (int)(e % nb);
-        const int i = i0 + (int)((e / nb) % R);
+        const int i = row_index(e / nb, R, i0, seq, per_seq);
         uint8_t m = 0;
         if (j <= i)
             m = (scores[e] > thr) || (ff && j == 0) || (fd && j == i);
@@ -85,8 +92,8 @@ __device__ __forceinline__ int block_exclusive_scan(int v, int *sbuf, int *total
 
 // One CTA per row (b, h, i).
 __global__ void __launch_bounds__(kTopThreads)
-    topk_kernel(const float *__restrict__ scores, int nb, int R, int i0, double density, int k_fixed,
-                const int32_t *__restrict__ k_per_row, int ff, int fd, uint8_t *__restrict__ mask)
+    topk_kernel(const float *__restrict__ scores, int nb, int R, int i0, SeqLens seq, int per_seq, double density,
+                int k_fixed, const int32_t *__restrict__ k_per_row, int ff, int fd, uint8_t *__restrict__ mask)
 {
     extern __shared__ uint32_t keys[];        // nb entries
     __shared__ int hist[256];
@@ -94,13 +101,15 @@ __global__ void __launch_bounds__(kTopThreads)
     __shared__ uint32_t s_prefix;
     __shared__ int s_remaining;
     const long long row = blockIdx.x;
-    const int i = i0 + (int)(row % R);
+    const int i = row_index(row, R, i0, seq, per_seq);
     const float *srow = scores + row * nb;
     uint8_t *mrow = mask + row * nb;
     const int n = i + 1;
     const int n_forced = (ff ? 1 : 0) + ((fd && !(ff && i == 0)) ? 1 : 0);
     int k;
-    if (k_per_row != nullptr) {
+    if (n == 0) {
+        k = 0;
+    } else if (k_per_row != nullptr) {
         k = k_per_row[i];
     } else if (k_fixed > 0) {
         k = k_fixed;
@@ -182,7 +191,9 @@ __global__ void __launch_bounds__(kTopThreads)
 __device__ __forceinline__ int row_k(int i, double density, int k_fixed, const int32_t *k_per_row, int n_forced)
 {
     int k;
-    if (k_per_row != nullptr) {
+    if (i < 0) {
+        return 0;
+    } else if (k_per_row != nullptr) {
         k = k_per_row[i];
     } else if (k_fixed > 0) {
         k = k_fixed;
@@ -205,14 +216,15 @@ __device__ __forceinline__ int row_k(int i, double density, int k_fixed, const i
 // Absent entries (j > i) hold key 0, below every real key.
 template <int PER>
 __global__ void __launch_bounds__(256)
-    topk_warp_kernel(const float *__restrict__ scores, long long rows, int nb, int R, int i0, double density,
-                     int k_fixed, const int32_t *__restrict__ k_per_row, int ff, int fd, uint8_t *__restrict__ mask)
+    topk_warp_kernel(const float *__restrict__ scores, long long rows, int nb, int R, int i0, SeqLens seq, int per_seq,
+                     double density, int k_fixed, const int32_t *__restrict__ k_per_row, int ff, int fd,
+                     uint8_t *__restrict__ mask)
 {
     const long long row = (long long)blockIdx.x * 8 + (threadIdx.x >> 5);
     if (row >= rows)
         return;
     const int lane = threadIdx.x & 31;
-    const int i = i0 + (int)(row % R);
+    const int i = row_index(row, R, i0, seq, per_seq);
     const int n = i + 1;
     const float *srow = scores + row * nb;
     uint8_t *mrow = mask + row * nb;
@@ -301,48 +313,50 @@ __global__ void __launch_bounds__(256)
 cudaError_t launch_mask(int B, int Hq, int nb, const float *scores, int mode, float threshold, double density,
                         int k_fixed, const int32_t *k_per_row, int ff, int fd, uint8_t *mask, cudaStream_t stream)
 {
-    return launch_mask_rows(B, Hq, nb, nb, 0, scores, mode, threshold, density, k_fixed, k_per_row, ff, fd, mask,
-                            stream);
+    return launch_mask_rows(B, Hq, nb, nb, 0, SeqLens{nullptr, 0}, scores, mode, threshold, density, k_fixed, k_per_row,
+                            ff, fd, mask, stream);
 }
 
 // R score rows of nb entries per head, row r holding causal row i0 + r (the
-// prefill square: R = nb, i0 = 0; a decode step: R = 1, i0 = nb - 1).
-cudaError_t launch_mask_rows(int B, int Hq, int nb, int R, int i0, const float *scores, int mode, float threshold,
-                             double density, int k_fixed, const int32_t *k_per_row, int ff, int fd, uint8_t *mask,
-                             cudaStream_t stream)
+// prefill square: R = nb, i0 = 0; a decode step: R = 1, i0 = nb - 1, or the last
+// block of each sequence of seq).
+cudaError_t launch_mask_rows(int B, int Hq, int nb, int R, int i0, SeqLens seq, const float *scores, int mode,
+                             float threshold, double density, int k_fixed, const int32_t *k_per_row, int ff, int fd,
+                             uint8_t *mask, cudaStream_t stream)
 {
+    const int per_seq = Hq * R;
     const long long rows = (long long)B * Hq * R;
     if (mode == 0) {
         const long long total = rows * nb;
         long long blocks = (total + kThrThreads - 1) / kThrThreads;
         if (blocks > 148LL * 64)
             blocks = 148LL * 64;
-        threshold_kernel<<<(unsigned)blocks, kThrThreads, 0, stream>>>(scores, total, nb, R, i0, threshold, ff, fd,
-                                                                       mask);
+        threshold_kernel<<<(unsigned)blocks, kThrThreads, 0, stream>>>(scores, total, nb, R, i0, seq, per_seq,
+                                                                       threshold, ff, fd, mask);
         return cudaGetLastError();
     }
     if (nb <= 1024) {
         const unsigned grid = (unsigned)((rows + 7) / 8);
         if (nb <= 128)
-            topk_warp_kernel<4><<<grid, 256, 0, stream>>>(scores, rows, nb, R, i0, density, k_fixed, k_per_row, ff,
-                                                               fd, mask);
+            topk_warp_kernel<4><<<grid, 256, 0, stream>>>(scores, rows, nb, R, i0, seq, per_seq, density, k_fixed,
+                                                               k_per_row, ff, fd, mask);
         else if (nb <= 256)
-            topk_warp_kernel<8><<<grid, 256, 0, stream>>>(scores, rows, nb, R, i0, density, k_fixed, k_per_row, ff,
-                                                               fd, mask);
+            topk_warp_kernel<8><<<grid, 256, 0, stream>>>(scores, rows, nb, R, i0, seq, per_seq, density, k_fixed,
+                                                               k_per_row, ff, fd, mask);
         else if (nb <= 512)
-            topk_warp_kernel<16><<<grid, 256, 0, stream>>>(scores, rows, nb, R, i0, density, k_fixed, k_per_row, ff,
-                                                               fd, mask);
+            topk_warp_kernel<16><<<grid, 256, 0, stream>>>(scores, rows, nb, R, i0, seq, per_seq, density, k_fixed,
+                                                               k_per_row, ff, fd, mask);
         else
-            topk_warp_kernel<32><<<grid, 256, 0, stream>>>(scores, rows, nb, R, i0, density, k_fixed, k_per_row, ff,
-                                                               fd, mask);
+            topk_warp_kernel<32><<<grid, 256, 0, stream>>>(scores, rows, nb, R, i0, seq, per_seq, density, k_fixed,
+                                                               k_per_row, ff, fd, mask);
         return cudaGetLastError();
     }
     const size_t smem = sizeof(uint32_t) * (size_t)nb;
     cudaError_t e = cudaFuncSetAttribute(topk_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess)
         return e;
-    topk_kernel<<<(unsigned)rows, kTopThreads, smem, stream>>>(scores, nb, R, i0, density, k_fixed, k_per_row, ff, fd,
-                                                               mask);
+    topk_kernel<<<(unsigned)rows, kTopThreads, smem, stream>>>(scores, nb, R, i0, seq, per_seq, density, k_fixed, k_per_row,
+                                                               ff, fd, mask);
     return cudaGetLastError();
 }
 

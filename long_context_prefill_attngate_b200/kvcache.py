@@ -9,6 +9,9 @@
     scores = seer_decode_gate_scores_cached(q_tok, kt, wq, L, Hkv)
     o = seer_block_sparse_decode_quant(q_tok, cache, seer_decode_block_mask(scores, density=0.1), L)
 
+For sequences of their own lengths (device int32 [B], the new token counted) the four calls of a step take them as
+lens=..., the write as start=lens, start_pos=-1, and L is the longest.
+
 Like the other calls these marshal arguments only, and take their tensors as
 they are on the stream they are given.  They run on the cache's device; what
 they allocate belongs to the stream they run on.  A decode step makes these

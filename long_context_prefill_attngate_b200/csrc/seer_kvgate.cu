@@ -3,12 +3,11 @@
 //   Kt_j = RoPE_j( pool_{t in block j, t < len}(z_t + s_t n_t) @ Wk )
 //
 // One kernel: a CTA pools sixteen blocks of a head and projects them.
-//  * Pooling reads the K half of each record once (HBM-bound for a whole
-//    cache).  The mean is an MMA too: the codes are the fp16 subnormals n 2^-24 on
-//    M (as in the decode kernel), a group's scales are two columns of N, normalised
-//    by the block's largest scale (exact in fp16 down to 2^-29 of it), and z is
-//    summed in fp32.  Half an integer operation an element instead of two and two
-//    fp32 ones.
+//  * Pooling reads the K half of each record once.  The mean is an MMA too: the codes
+//    are the bf16 numbers n 2^-133 on M (as in the decode kernel), a group's scales
+//    are two columns of N times a power of two of the block's largest (exact down to
+//    2^-116 of it), and z is summed in fp32.  Half an integer operation an element
+//    instead of two and two fp32 ones.
 //    Max and min (the other pooling) take z + s n element by element; their
 //    warps share a block's rows when the CTA has few blocks.
 //  * Projection: sixteen pooled rows are the M of an mma.sync m16n8k16 (the
@@ -67,11 +66,16 @@ __device__ __forceinline__ void ldmatrix2_trans(uint32_t &r0, uint32_t &r1, uint
     asm volatile("ldmatrix.sync.aligned.m8n8.x2.trans.shared.b16 {%0,%1}, [%2];" : "=r"(r0), "=r"(r1) : "r"(addr));
 }
 
-__device__ __forceinline__ void mma_bf16(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1)
+__device__ __forceinline__ void mma_bf16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                         uint32_t b1)
 {
     asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
                  : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-                 : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+                 : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ void mma_bf16(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1)
+{
+    mma_bf16(c, a[0], a[1], a[2], a[3], b0, b1);
 }
 
 // A NaN wins, as it does in a sum.
@@ -115,21 +119,6 @@ __device__ __forceinline__ uint32_t max_key(float x)
 __device__ __forceinline__ float from_max_key(uint32_t k)
 {
     return k == 0xFFFFFFFFu ? __uint_as_float(0x7FC00000u) : __uint_as_float(k >> 31 ? k & 0x7FFFFFFFu : ~k);
-}
-
-__device__ __forceinline__ void mma_f16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
-                                        uint32_t b1)
-{
-    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
-                 : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-                 : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
-}
-
-__device__ __forceinline__ uint32_t pack_half2(float lo, float hi)
-{
-    uint32_t r;
-    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
-    return r;
 }
 
 template <int N>
@@ -201,13 +190,14 @@ __device__ __forceinline__ void pool_mean(const uint8_t *rec, int rows, float *r
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             smax = __vmaxu2(smax, par[mt][i]);
-            zs += kv_zero(par[mt][i]);
+            zs = fmaf(kv_zero(par[mt][i]), 0.015625f, zs);
         }
     zs += __shfl_xor_sync(0xffffffffu, zs, 1);
     zs += __shfl_xor_sync(0xffffffffu, zs, 2);
     smax = __reduce_max_sync(0xffffffffu, smax & 0xFFFFu);
-    const int se = max((int)(smax >> 7), 27);            // exponent field of the largest scale, at least 2^-100's
-    const float up = __uint_as_float((uint32_t)(268 - se) << 23);      // scales to at most 2^15
+    // scales to at most 2^124, those of 2^-3 and below by 2^127: exact in bf16 down to 2^-116 of the largest
+    const int uf = min(254, 377 - (int)(smax >> 7));
+    const float up = __uint_as_float((uint32_t)uf << 23);
     const unsigned first = gid & 1 ? 0x1044u : 0x4410u, second = gid & 1 ? 0x3244u : 0x4432u;
     float c[VW][U][4];
 #pragma unroll
@@ -219,7 +209,8 @@ __device__ __forceinline__ void pool_mean(const uint8_t *rec, int rows, float *r
     for (int mt = 0; mt < 4; ++mt)
 #pragma unroll
         for (int i = 0; i < 4; i += 2) {
-            const uint32_t s2 = pack_half2(kv_scale(par[mt][i]) * up, kv_scale(par[mt][i + 1]) * up);
+            const uint32_t s2 = __byte_perm(__float_as_uint(kv_scale(par[mt][i]) * up),
+                                            __float_as_uint(kv_scale(par[mt][i + 1]) * up), 0x7632);
             const uint32_t b0 = __byte_perm(s2, 0u, first), b1 = __byte_perm(s2, 0u, second);
 #pragma unroll
             for (int k = 0; k < VW; ++k) {
@@ -227,18 +218,20 @@ __device__ __forceinline__ void pool_mean(const uint8_t *rec, int rows, float *r
                 if constexpr (BITS == 4) {
 #pragma unroll
                     for (int u = 0; u < 2; ++u) {
-                        mma_f16(c[k][u], x & 0x000F000Fu, x & 0x00F000F0u, y & 0x000F000Fu, y & 0x00F000F0u, b0, b1);
+                        mma_bf16(c[k][u], x & 0x000F000Fu, x & 0x00F000F0u, y & 0x000F000Fu, y & 0x00F000F0u, b0, b1);
                         x >>= 8;
                         y >>= 8;
                     }
                 } else {
-                    mma_f16(c[k][0], __byte_perm(x, 0u, 0x4140), __byte_perm(x, 0u, 0x4342), __byte_perm(y, 0u, 0x4140),
+                    mma_bf16(c[k][0], __byte_perm(x, 0u, 0x4140), __byte_perm(x, 0u, 0x4342), __byte_perm(y, 0u, 0x4140),
                             __byte_perm(y, 0u, 0x4342), b0, b1);
                 }
             }
         }
-    // a lane holds the sums of the words whose group is tig
-    const float down = __uint_as_float((uint32_t)(se - 14) << 23), inv = 1.f / (float)rows;
+    // a lane holds the sums of the words whose group is tig: 2^133 / up, a 64th of each
+    // (as z's), so that blocks of the largest values stay within fp32
+    const float down = __uint_as_float((uint32_t)(127 + 133 - 6 - 64 - (uf - 127)) << 23), inv = 64.f / (float)rows;
+    constexpr float kUnit = 18446744073709551616.f, kUnitOdd = BITS == 4 ? kUnit * 0.0625f : kUnit;        // 2^64
     const float z = __shfl_sync(0xffffffffu, zs, 8 * tig);
 #pragma unroll
     for (int k = 0; k < VW; ++k) {
@@ -258,9 +251,8 @@ __device__ __forceinline__ void pool_mean(const uint8_t *rec, int rows, float *r
             continue;
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-            const float v0 = c[k][u][0] * down * 16777216.f, v1 = c[k][u][1] * down * 16777216.f;
-            const float v2 = c[k][u][2] * down * (BITS == 4 ? 1048576.f : 16777216.f);
-            const float v3 = c[k][u][3] * down * (BITS == 4 ? 1048576.f : 16777216.f);
+            const float v0 = c[k][u][0] * kUnit * down, v1 = c[k][u][1] * kUnit * down;
+            const float v2 = c[k][u][2] * kUnitOdd * down, v3 = c[k][u][3] * kUnitOdd * down;
             float2 *at = reinterpret_cast<float2 *>(row + e0 + 2 * u);
             if (BITS == 4) {                             // elements 2u, 2u + 1 and four further
                 at[0] = make_float2((v0 + z) * inv, (v2 + z) * inv);

@@ -121,6 +121,8 @@ def _per_sequence(cache, name, t):
     raise ValueError(name)
 
 
+_INT32 = range(-2 ** 31, 2 ** 31)
+_POS = "start_pos must be within 32 bits"
 _START = "start must be int32 [B] on the cache's device"
 _COUNT = "count must be int32 [B] on the cache's device"
 _LENS = "lens must be int32 [B] on the cache's device"
@@ -150,6 +152,7 @@ def seer_kv_write(cache, k, v, start=None, count=None, start_pos: int = 0, strea
     _need(k.dtype is _bf16 and v.dtype is _bf16, "k and v must be bf16")
     dev = cache._dev
     _need(k.get_device() == dev and v.get_device() == dev, "k and v must be on the cache's device")
+    _need(start_pos in _INT32, _POS)
     sp, cp = _per_sequence(cache, _START, start), _per_sequence(cache, _COUNT, count)
     if stream is not None or dev < 0 or dev != _current_device():
         return _elsewhere(seer_kv_write, dev, stream, cache, k, v, start, count, start_pos)
@@ -168,6 +171,7 @@ def seer_kv_read(cache, n: int, start=None, count=None, start_pos: int = 0, k=No
     for t in (k, v):
         _need(t is None or (t.dtype is _bf16 and t.shape == shape and t.is_contiguous() and t.get_device() == cache._dev),
               "k and v must be contiguous bf16 [B,Hkv,n,d] on the cache's device")
+    _need(start_pos in _INT32, _POS)
     sp, cp = _per_sequence(cache, _START, start), _per_sequence(cache, _COUNT, count)
     dev = cache._dev
     if stream is not None or dev < 0 or dev != _current_device():
@@ -201,6 +205,7 @@ def seer_gate_key_cache_quant(cache, wk, L: int, kt=None, first_block: int = 0, 
     shape = (cache._B, cache._Hkv, -(-L // B.BLOCK), dg)
     _need(kt is None or (kt.dtype is _f32 and kt.shape == shape and kt.is_contiguous() and kt.get_device() == dev),
           "kt must be contiguous fp32 [B,Hkv,nb,d_gate] on the cache's device")
+    _need(0 <= first_block <= shape[2], "first_block must be within the blocks of L")
     lp = _per_sequence(cache, _LENS, lens)
     if stream is not None or dev < 0 or dev != _current_device():
         return _elsewhere(seer_gate_key_cache_quant, dev, stream, cache, wk, L, kt, first_block, lens, rope_theta, None,

@@ -58,3 +58,15 @@ def test_a_stream_of_another_device_is_refused():
 
     with pytest.raises(ValueError, match="stream"):
         kvcache._elsewhere(lambda: None, 0, Stream())
+
+
+@pytest.mark.parametrize("n", [2 ** 31, 2 ** 32, 2 ** 32 + 5, -2 ** 31 - 1])
+def test_positions_of_more_than_32_bits_are_refused(cache, n):
+    """The C calls take ints: what does not fit would have named another position."""
+    k = torch.zeros((2, 2, 5, 128), dtype=torch.bfloat16)
+    with pytest.raises(ValueError, match="start_pos"):
+        seer.seer_kv_write(cache, k, k, start_pos=n)
+    with pytest.raises(ValueError, match="start_pos"):
+        seer.seer_kv_read(cache, 5, start_pos=n)
+    with pytest.raises(ValueError, match="first_block"):
+        seer.seer_gate_key_cache_quant(cache, torch.zeros((2, 128, 64), dtype=torch.bfloat16), 200, first_block=n)

@@ -166,7 +166,7 @@ def seer_kv_write(cache, k, v, start=None, count=None, start_pos: int = 0, strea
 
 def seer_kv_read(cache, n: int, start=None, count=None, start_pos: int = 0, k=None, v=None, stream=None):
     """K and V (bf16 [B,Hkv,n,d]) as the cache holds them from position start[b] + start_pos on; rows from count[b] on
-    are not written (zero where the tensor is not given)."""
+    and rows that the cache does not have are not written (zero where the tensor is not given)."""
     shape = (cache._B, cache._Hkv, n, cache._d)
     for t in (k, v):
         _need(t is None or (t.dtype is _bf16 and t.shape == shape and t.is_contiguous() and t.get_device() == cache._dev),
@@ -176,7 +176,9 @@ def seer_kv_read(cache, n: int, start=None, count=None, start_pos: int = 0, k=No
     dev = cache._dev
     if stream is not None or dev < 0 or dev != _current_device():
         return _elsewhere(seer_kv_read, dev, stream, cache, n, start, count, start_pos, k, v)
-    make = torch.empty if count is None else torch.zeros
+    # zeros where the call may leave rows out: behind counts, outside the cache, on pages that a table does not have
+    whole = count is None and start is None and cache._block_table is None and 0 <= start_pos <= 64 * cache._max_blocks - n
+    make = torch.empty if whole else torch.zeros
     if k is None:
         k = make(*shape, dtype=_bf16, device=cache._pages.device)
     if v is None:

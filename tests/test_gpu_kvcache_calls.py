@@ -49,3 +49,33 @@ def test_gate_keys_of_two_widths_from_two_threads():
     torch.cuda.synchronize()
     assert not errors, errors
     assert all(torch.equal(got[dg], want[dg]) for dg in wk)
+
+
+@pytest.mark.parametrize("what", ["start", "start_pos", "table"])
+def test_rows_that_the_cache_does_not_have_read_as_zero(what):
+    """Where the call makes the output, not what the memory held before: rows behind the cache, below 0 and on a page
+    that the table does not have; a device error besides."""
+    B, Hkv, d, n = 1, 2, 128, 100
+    cache, table = make_cache(B, Hkv, 2, d, 4, what == "table", 0)
+    k = bf16((B, Hkv, 128, d), 1).cuda()
+    seer.seer_kv_write(cache, k, k)
+    held = seer.seer_kv_read(cache, 128)[0]
+    args, at = {}, 0
+    if what == "table":
+        cache.block_table[0, 1] = -1
+    elif what == "start":
+        args, at = dict(start=torch.tensor([64], dtype=torch.int32, device="cuda")), 64
+    else:
+        args, at = dict(start_pos=64), 64
+    torch.cuda.synchronize()
+    for _ in range(4):                                      # what the allocator hands out next
+        a = [torch.full((B, Hkv, n, d), 7.0, dtype=torch.bfloat16, device="cuda") for _ in range(3)]
+        del a
+    out = seer.seer_kv_read(cache, n, **args)
+    with pytest.raises(seer.SeerError):
+        seer.seer_check_status()
+    for t in out:
+        assert torch.equal(t[:, :, :64], held[:, :, at:at + 64]) and not t[:, :, 64:].any()
+    whole = seer.seer_kv_read(cache, 64)
+    seer.seer_check_status()
+    assert torch.equal(whole[0], held[:, :, :64])

@@ -416,7 +416,9 @@ SEER_API size_t seer_kv_record_bytes(int bits, int d);
  * row t of sequence b goes to position start[b] + start_pos + t for
  * t < min(count[b], n).  start, count: DEVICE int32 [B] or NULL (0, and n).
  * A decode step that keeps its lengths on the device passes them as start with
- * start_pos = -1.  Other tokens of the pages are left as they are.
+ * start_pos = -1, and count 0 for slots without a sequence: a row at a position below
+ * 0 is a device error, that of a length 0 too.  Other tokens of the pages are left as
+ * they are.
  */
 SEER_API seer_status seer_kv_write(const seer_shape *shape, const seer_kv_cache *cache, const seer_kv_rows *rows,
                                    const int32_t *start, const int32_t *count, int start_pos, void *stream);

@@ -89,12 +89,6 @@ struct KvFmt {
             return D == 128 ? ((t >> 2) & 1) * 4 : 0;
         return D == 128 ? ((t >> 1) & 3) * 2 : ((t >> 2) & 1) * 4;
     }
-    __host__ __device__ static int v_off(int t, int m)
-    {
-        if (BITS == 4)
-            return t * R + (((m % 16) / 2) ^ v_swizzle(t)) * (2 * NG) + (m / 16) * 2 + m % 2;
-        return t * R + (((m % 64) / 8) ^ v_swizzle(t)) * (8 * NG) + (m / 64) * 8 + m % 8;
-    }
 };
 
 // The page of block j of sequence b, or -1 (recorded in the status word) when

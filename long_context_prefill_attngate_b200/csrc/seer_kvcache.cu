@@ -10,8 +10,9 @@
 //
 // A row costs 2 D bytes on the bf16 side and D bits / 8 + 4 D / G on the other, so
 // HBM is the floor of both directions.  32k rows of 8 heads at 4 bits (D = 128,
-// 176 MB): reading back 31 us (5.7 TB/s), HBM-bound; writing 37 us (4.8 TB/s),
-// its instructions 70 % of the issue slots.
+// 176 MB): reading back 30.5 us (5.8 TB/s), writing 37.1 us (4.8 TB/s; 32.2 before codes
+// next to a half were looked for); at 8 bits 34.1 and 38.1.  Both are near the copy rate
+// and bound by their instructions (69 and 72 % of the issue slots, the integer pipe first).
 #include <type_traits>
 
 #include <cuda_bf16.h>
@@ -26,10 +27,10 @@ namespace {
 constexpr int kRowThreads = 256;
 
 // A lane holds E elements of a row.  Reading, eight: one 16-byte store each,
-// which leaves the kernel at 87 % of the copy rate.  Writing is bound by its
-// instructions, not by HBM, so there a lane has sixteen, over which the group's
-// extrema, scale and addresses are shared (37 us against 45 with eight for
-// a 32k prompt of 8 heads).
+// which leaves the kernel at 88 % of the copy rate.  Writing has more instructions an
+// element, so there a lane has sixteen, over which the group's extrema, scale and
+// addresses are shared (37 us against 45 with eight for a 32k prompt of 8 heads, before
+// codes next to a half were looked for).
 template <int BITS, int D, int E>
 struct RowMap {
     using F = KvFmt<BITS, D>;
@@ -464,7 +465,9 @@ __global__ void __launch_bounds__(kRowThreads) kv_read_kernel(KvView kv, int Hkv
             for (int e = 0; e < 4; ++e) {
                 constexpr int per = 32 / BITS;
                 const uint32_t q0 = w[2 * e / per] >> (2 * e % per * BITS), q1 = w[(2 * e + 1) / per] >> ((2 * e + 1) % per * BITS);
-                // the code as a float: 2^23 + n, less 2^23
+                // the code as a float: 2^23 + n, less 2^23.  (The sum rounded to fp32 and then to
+                // bf16 is the sum rounded once: fp32 is inexact only where s n is below half a bf16
+                // step of z, and then 255 * 255 / 2^16 keeps it away from the middle.)
                 float2 f = make_float2(__uint_as_float((q0 & (uint32_t)F::TOP) | 0x4B000000u),
                                        __uint_as_float((q1 & (uint32_t)F::TOP) | 0x4B000000u));
                 f = fma2(add2(f, both(-8388608.f)), both(s), both(z));

@@ -38,12 +38,13 @@
 //  * Split over the union's blocks by rank, so splits differ by one block at
 //    most; a second kernel joins them.
 //
-// What bounds it: with 8 bits and long caches HBM (128k tokens at density 0.17: the loop
-// itself reads 7 TB/s; 35.2 us a call with start, end and join, 22.8 at the copy
-// rate).  With 4 bits the instructions of the loop, about half of them on the integer
-// pipe at two cycles each, against 6 cycles a token that HBM allows (32k tokens of a
-// layer, all active: 17.9 us, 6.4 at the copy rate).  Short ones: a CTA's start and
-// end, some 8,000 cycles of latencies, and the join (32k at density 0.1: 10.8 us; 200
+// What bounds it: with 8 bits and long caches HBM and what is around the loop (128k
+// tokens at density 0.17: 35.6 us with start, end and join, 22.8 at the copy rate).
+// With 4 bits the loop (32k tokens of a layer, all active: 19.7 us, 6.4 at the copy rate):
+// its warps issue in 52 % of the cycles (46 % with sixteen heads, whose registers allow
+// eight warps an SM) and no pipe is busier than 41 %, so the latency of a warp's chain,
+// scores to maximum to exponential to P V, is not hidden.  Short ones: a CTA's start and
+// end, some 8,000 cycles of latencies, and the join (32k at density 0.1: 11.8 us; 200
 // tokens: 4.6).
 #include <cuda_bf16.h>
 
@@ -290,8 +291,8 @@ struct DecodeArgs {
 // products; one has twice the warps for its list and half the splits to join.  The
 // rings hold 70 to 200 KB, where the SM's share of HBM (24 bytes a cycle) needs some
 // 40 KB in flight.  Sixteen heads: at D = 128 the accumulators leave eight warps of an
-// SM their registers (64 units of 256 blocks at 4 bits: 72 us, 74 with twelve, which
-// spill; at 8 bits 59 and 65), at D = 64 twelve.
+// SM their registers (64 units of 256 blocks at 4 bits, p s in one part: 72 us, 74 with
+// twelve, which spill; at 8 bits 59 and 65), at D = 64 twelve.
 template <int BITS, int D, int H, int P>
 struct DecodeCfg {
     static constexpr int W = (H == 16 ? (D == 128 ? 4 : 6) : BITS == 8 && D == 128 ? 6 : 8) * (P == 1 ? 2 : 1);
@@ -381,7 +382,8 @@ __device__ __forceinline__ int splits_of(const DecodeArgs &a, int b, int lane)
 // Up to eight heads: on N, keys or output elements on M.  Up to four stand in N
 // twice (up to two four times), and the places share the groups of a row: each has
 // p s and p z of its own, and one B operand serves a group of every place (32k tokens
-// of a layer, groups of four, all active: 17.9 us, 19.5 with eight columns).
+// of a layer, groups of four, all active, p s in one part: 17.9 us, 19.5 with eight
+// columns).
 template <int BITS, int D, int H>
 struct Sums {
     using F = KvFmt<BITS, D>;
@@ -1333,7 +1335,7 @@ __global__ void __launch_bounds__(DecodeCfg<BITS, D, H, P>::W * 32, P) decode_qu
 // share an output element, every Q-th split each, and their first loads are in
 // flight before a weight is known.  Four from nine splits on: one latency, not
 // one per eight splits (128k tokens, 37 splits: 2.7 us less of 40.8); one for few
-// (1024 heads of two splits: 90 us a call, 96 with four).
+// (1024 heads of two splits: 90 us a call, 96 with four; both with an earlier loop).
 template <int D, int Q>
 __global__ void __launch_bounds__(Q * D) decode_quant_merge_kernel(const DecodeArgs a)
 {
@@ -1415,11 +1417,16 @@ struct Plan {
 //   two, but no more CTAs than SMs    6                8
 //                                     0.4              0.65
 //   the second kernel                 2 and 0.04 a split
-// Measured (4 bits, D = 128, eight columns of heads): 8 units (a sequence's head
-// tile) of 512 blocks, all active: P = 1, 9 splits 26.0 us, 12: 22.3, 18: 19.4;
-// P = 2, 18: 20.7, 37: 19.8; a tenth active: P = 1, 9: 14.3, 18: 12.0; P = 2, 18: 11.6,
-// 37: 12.4; 128 units of 256, P = 2: 1 split 97 us, 2: 86, 4: 91.  Sixteen heads, 64
-// units of 256 blocks, P = 2: 1 split 172 us, 2: 93, 4: 70; of 64 blocks: 50, 32, 27.
+// The constants are of the loop with p s in one part, 4 bits, D = 128 and eight columns
+// of heads, and order the plans: with two parts a block takes up to a fifth more, of every
+// plan.  Measured now, groups of four, D = 128, 8 units (a sequence's head tile) of 512
+// blocks, 4 | 8 bits, all active: P = 1, 9 splits 25.9 | 24.7 us, 12: 21.8 | 21.5, 18:
+// 19.2 | 20.6; P = 2, 18: 20.6 | 22.2, 37: 18.3 | 21.4; a tenth active: P = 1, 9: 14.4 |
+// 14.4, 18: 13.0 | 13.6; P = 2, 18: 12.9 | 14.4, 37: 13.2 | 13.8.  At D = 64, all active: P = 1,
+// 18: 14.4 | 15.3; P = 2, 18: 15.1 | 15.6, 37: 13.8 | 14.9.  128 units of 256, P = 2: 1 split
+// 111 | 121 us, 2: 93 | 94, 4: 96 | 98.  Sixteen heads, 64 units of 256 blocks, P = 2: 1 split
+// 198 | 176 us, 2: 107 | 97, 4: 84 | 75; of 64 blocks: 56 | 50, 35 | 40, 30 | 29.  What is chosen is
+// within 5 % of the best of these, but for sixteen heads on sparse masks (below).
 double decode_quant_us(const Plan &p, long long ctas, double blocks, double splits, int sms)
 {
     const bool two = p.H == 16;
@@ -1436,10 +1443,11 @@ double decode_quant_us(const Plan &p, long long ctas, double blocks, double spli
 // blocks active (the mask is on the device) and at least a block for every
 // second warp.  Lengths given: a CTA for each place on the SMs, where there are
 // enough for every sequence's tiles, shared out by length: a batch of 8 from 32k
-// tokens down took 45 us with 4 splits each, 39 so.  Not for two or three
-// sequences, whose CTAs pair up on the SMs (64k and 37k tokens at 8 bits: 40.7 us with
-// 18 splits each, 45 shared out, 41.5 with one CTA per SM), and in whole splits where
-// a sequence has few (16 of 16k tokens: 88 us with two each, 90 with 37 slots).
+// tokens down takes 52 us with 4 splits each, 43 so.  Not for two or three
+// sequences, whose CTAs pair up on the SMs (64k and 37k tokens at 8 bits: 44 us with
+// 18 splits each, 50 in 18 slots, 43 in 37, 45 with one CTA per SM), and in whole splits where
+// a sequence has few (16 of 16k tokens, an earlier loop: 88 us with two each, 90 with 37
+// slots).
 void decode_quant_split(DecodeArgs &a, Plan &p, int sms)
 {
     const int g = a.Hq / a.Hkv;
@@ -1544,8 +1552,9 @@ cudaError_t launch_decode_quant(int bits, int B, int Hq, int Hkv, int L, int d, 
         return e;
     // Two, four or eight heads a CTA by the heads of a KV head or, for more, sixteen, and one CTA per SM or two of
     // half the warps: what is estimated fastest.  Sixteen for enough blocks (groups of
-    // 16, 64 units of 256 blocks, all active: 71 us, 88 by eights; 8 of 512, a tenth
-    // active: 24 and 21), one CTA for one round of long ones (decode_quant_us).
+    // 16, 64 units of 256 blocks, all active: 84 us, 103 by eights; a tenth active, where
+    // the union of sixteen heads is larger: 75 and 69), one CTA for one round of long
+    // ones (decode_quant_us).
     Plan best{};
     DecodeArgs args = a;
     const int g = Hq / Hkv, groups = d / (bits == 4 ? 32 : 64);

@@ -19,9 +19,10 @@
 //    reduced modulo 2 pi, then fp32.
 //
 // 512 blocks of 8 heads at 4 bits (D = d_gate = 128): 9.9 us for 23 MB, of which the
-// pooling of a warp's two blocks, one after the other, is half (latency and
-// instructions; HBM alone would be 3.6 us), the projection and the rotation 8 % each;
-// the last block of 4 sequences (max+min, 8 bits): 5.0 us, all latency.
+// pooling of a warp's two blocks, one after the other, is half, the projection and the
+// rotation 8 % each (HBM alone would be 3.6 us; issue 40 %, DRAM 19 %: the phases wait for
+// one another, and both CTAs of an SM are in the same one).  The last block of 4
+// sequences (max+min, 8 bits): 5.0 us, all latency.
 #include <cmath>
 
 #include <cuda_bf16.h>

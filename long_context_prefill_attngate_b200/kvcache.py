@@ -10,7 +10,8 @@
     o = seer_block_sparse_decode_quant(q_tok, cache, seer_decode_block_mask(scores, density=0.1), L)
 
 For sequences of their own lengths (device int32 [B], the new token counted) the four calls of a step take them as
-lens=..., the write as start=lens, start_pos=-1, and L is the longest.
+lens=..., the write as start=lens, start_pos=-1 (with count=0 for idle slots, whose row would have no place), and L is
+the longest.
 
 Like the other calls these marshal arguments only, and take their tensors as
 they are on the stream they are given.  They run on the cache's device; what

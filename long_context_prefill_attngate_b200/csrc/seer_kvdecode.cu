@@ -31,6 +31,8 @@
 //    p z, the row sums and all accumulators are fp32.
 //  * The running maximum moves when a score is 2^6 above it, so the accumulators
 //    are rescaled a few times per warp; p is 2^-26 at the maximum and reaches 2^-20.
+//    It is subtracted before the factor of the exponent: of scores beyond 2^24 the
+//    product's rounding alone would be more than p's whole range.
 //  * Work of a warp: half records of 32 tokens, each one contiguous bulk copy
 //    into the warp's own ring, so no warp waits for another until the end.
 //  * P leaves K Q^T with keys across lanes and enters V^T P with keys across a
@@ -591,8 +593,7 @@ struct Sums {
             l[0] *= alpha[0];
             l[1] *= alpha[1];
         }
-        const float mu[2] = {m[0] == -INFINITY ? 0.f : fmaf(-m[0], fac[0], -kTop),
-                             m[1] == -INFINITY ? 0.f : fmaf(-m[1], fac[1], -kTop)};
+        const float mu[2] = {m[0] == -INFINITY ? 0.f : m[0], m[1] == -INFINITY ? 0.f : m[1]};
         const float up[2] = {scale_up(ve[0]), scale_up(ve[1])};
 
         // ---- P V
@@ -601,7 +602,7 @@ struct Sums {
             float p[4];
 #pragma unroll
             for (int e = 0; e < 4; ++e)
-                p[e] = exp2_approx(fmaf(s[mt][e], fac[e & 1], mu[e & 1]));
+                p[e] = exp2_approx(fmaf(s[mt][e] - mu[e & 1], fac[e & 1], -kTop));
             if (!all_heads) {
                 p[0] = act0 ? p[0] : 0.f;
                 p[1] = act1 ? p[1] : 0.f;
@@ -911,8 +912,7 @@ struct Sums<BITS, D, 16> {
             l[1] *= alpha[1];
             ve_least = __reduce_min_sync(0xffffffffu, min(ve[0], ve[1]));
         }
-        const float mu[2] = {m[0] == -INFINITY ? 0.f : fmaf(-m[0], fac[0], -kTop),
-                             m[1] == -INFINITY ? 0.f : fmaf(-m[1], fac[1], -kTop)};
+        const float mu[2] = {m[0] == -INFINITY ? 0.f : m[0], m[1] == -INFINITY ? 0.f : m[1]};
         const float up[2] = {scale_up(ve[0]), scale_up(ve[1])};
 
         // ---- P V
@@ -923,7 +923,7 @@ struct Sums<BITS, D, 16> {
             for (int nt = 0; nt < 2; ++nt) {
 #pragma unroll
                 for (int e = 0; e < 4; ++e)
-                    p[nt][e] = exp2_approx(fmaf(s[mt][nt][e], fac[e >> 1], mu[e >> 1]));
+                    p[nt][e] = exp2_approx(fmaf(s[mt][nt][e] - mu[e >> 1], fac[e >> 1], -kTop));
                 if (!all_heads) {
                     p[nt][0] = act0 ? p[nt][0] : 0.f;
                     p[nt][1] = act0 ? p[nt][1] : 0.f;

@@ -152,3 +152,25 @@ def test_values_near_the_largest_with_scores_that_rise(bits, d, Hq):
     mask = ones(B, Hq, L)
     o, lse, kv = run(bits, d, B, Hq, k, v, q, mask, 1.0)
     check(o, lse, q, kv, mask, [L] * B, (0, B - 1), 1.0)
+
+
+@pytest.mark.parametrize("bits,d", FORMATS)
+@pytest.mark.parametrize("B,Hq", HEADS)
+@pytest.mark.parametrize("e", [20, 30, 40, 60, 100])
+def test_scores_beyond_fp32_steps_of_one(bits, d, B, Hq, e):
+    """Scores of 2^e and more, each a 256th of the largest from the next: the largest key takes all."""
+    L = 450
+    k = torch.zeros((1, 1, L, d))
+    top = torch.randperm(L, generator=torch.Generator().manual_seed(e))
+    k[0, 0, :, 0] = (top % 128 + 64).float() * 2.0 ** (e // 2)
+    k[0, 0, 333, 0] = 255.0 * 2.0 ** (e // 2)               # the largest of all
+    q = torch.zeros((B, Hq, d))
+    q[..., 0] = 2.0 ** (e - e // 2)
+    k, q, v = k.to(torch.bfloat16), q.to(torch.bfloat16), bf16((1, 1, L, d), 2)
+    o, lse, kv = run(bits, d, B, Hq, k, v, q, ones(B, Hq, L), 1.0)
+    score = ref.values(*kv[0])[0, 0, :L] @ f64(q[0, 0])
+    best = int(np.argmax(score))
+    want = ref.values(*kv[1])[0, 0, best]
+    assert best == 333 and np.sort(score)[-2] < score[best] * (1 - 2.0 ** -9)
+    assert np.all(np.abs(f64(o) - want) <= (2.0 ** -8 + 2.0 ** -15) * np.abs(want) + 2.0 ** -15 * (np.abs(want).max()))
+    assert np.all(np.abs(f64(lse) - score[best]) <= 2.0 ** -21 * score[best])

@@ -41,9 +41,9 @@
 //    most; a second kernel joins them.
 //
 // What bounds it: with 8 bits and long caches HBM and what is around the loop (128k
-// tokens at density 0.17: 35.6 us with start, end and join, 22.8 at the copy rate).
-// With 4 bits the loop (32k tokens of a layer, all active: 19.7 us, 6.4 at the copy rate):
-// its warps issue in 52 % of the cycles (46 % with sixteen heads, whose registers allow
+// tokens at density 0.17: 35.5 us with start, end and join, 22.8 at the copy rate).
+// With 4 bits the loop (32k tokens of a layer, all active: 19.6 us, 6.4 at the copy rate):
+// its warps issue in 51 % of the cycles (47 % with sixteen heads, whose registers allow
 // eight warps an SM) and no pipe is busier than 41 %, so the latency of a warp's chain,
 // scores to maximum to exponential to P V, is not hidden.  Short ones: a CTA's start and
 // end, some 8,000 cycles of latencies, and the join (32k at density 0.1: 11.8 us; 200
